@@ -324,6 +324,128 @@ int entmaxkv_decode_full(const entmaxkv_shape* shape, const float* q, const void
                          hipEvent_t* events);
 
 /*
+ * Softmax decode attention over a sliding window with attention sinks, for
+ * the layers of a model that keep softmax beside alpha-entmax ones. Each
+ * sequence brings the queries of its last q_tokens tokens, whose keys are in
+ * the cache: query i of sequence b is the token at position
+ * p = seq_lens[b] - q_tokens + i and sees the tokens t <= p with
+ * t > p - window (window counts p itself) or t < sinks:
+ *     out = sum_t exp(z_t - m) v_t / sum_t exp(z_t - m),   z_t = q . k_t,
+ *     lse = m + ln sum_t exp(z_t - m),                     m = max_t z_t.
+ * A window of at least every sequence's length is full attention; sinks may
+ * be 0. A query that sees nothing (p < 0: a padded sequence, or q_tokens >
+ * seq_lens[b]; every page invalid) gets out = 0 and lse = -inf, and so does
+ * one whose visible scores are all -inf. What lies in hidden tokens' rows, in
+ * page tails and in pages that no query sees has no effect, NaN and
+ * infinities included; a visible key or value that is not finite makes the
+ * outputs it enters not finite.
+ *   q        q_dtype [batch, q_tokens, num_q_heads, head_dim]
+ *   q_dtype  ENTMAXKV_F32, or ENTMAXKV_BF16 with a BF16 cache (else
+ *            ENTMAXKV_ERR_UNSUPPORTED)
+ *   out      q_dtype, the shape of q (16-byte aligned)
+ *   lse      float32 [batch, q_tokens, num_q_heads] (nullable)
+ *   window   >= 1; sinks >= 0; q_tokens >= 1 (else ENTMAXKV_ERR_INVALID);
+ *            batch * q_tokens * num_q_heads <= 2^24
+ * Products and sums are float32; float32 queries and weights meet bf16 keys
+ * and values in exact bf16 parts, so that no product is rounded. The result
+ * does not depend on what else runs (no atomics).
+ * Workspace: entmaxkv_softmax_window_ws bytes for the same arguments (0: ws
+ * may be null). Kernels launched: 2 (attention, join of the splits; the
+ * second only when the workspace is not 0 bytes).
+ */
+int entmaxkv_softmax_window(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
+                            int32_t q_tokens, const void* k_pool, const void* v_pool,
+                            const int32_t* block_table, const int32_t* seq_lens, int32_t window,
+                            int32_t sinks, void* out, float* lse, void* ws, size_t ws_bytes,
+                            hipStream_t stream, hipEvent_t* events);
+int entmaxkv_softmax_window_ws(const entmaxkv_shape* shape, int32_t q_tokens, int32_t window,
+                               int32_t sinks, size_t* bytes);
+
+/*
+ * Softmax decode attention of one token per sequence, for a batch whose
+ * sequences all begin with the same prefix_pages whole pages (a system
+ * prompt, a document). The shared pages are read once for the whole batch,
+ * every sequence's queries as rows of one product.
+ *   prefix_table  int32 [prefix_pages]: physical pages of the prefix
+ *   block_table   as elsewhere, over whole sequences; its first prefix_pages
+ *                 columns are not read
+ *   prefix_pages  1 .. max_pages_per_seq (else ENTMAXKV_ERR_INVALID)
+ * Sequence b sees its tokens t < seq_lens[b], token t < prefix_pages *
+ * page_size in prefix_table's pages; a sequence may be shorter than the
+ * prefix, or empty (out = 0, lse = -inf). q and out are q_dtype [batch,
+ * num_q_heads, head_dim], lse is [batch, num_q_heads]; everything else as for
+ * entmaxkv_softmax_window with q_tokens = 1 and an unlimited window.
+ * Workspace: entmaxkv_softmax_prefix_ws bytes. Kernels launched: 2.
+ */
+int entmaxkv_softmax_prefix(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
+                            const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+                            int32_t prefix_pages, const int32_t* block_table,
+                            const int32_t* seq_lens, void* out, float* lse, void* ws,
+                            size_t ws_bytes, hipStream_t stream, hipEvent_t* events);
+int entmaxkv_softmax_prefix_ws(const entmaxkv_shape* shape, int32_t prefix_pages, size_t* bytes);
+
+/*
+ * Attention weight of every cached token, added to a decayed running sum:
+ *     weights_out[b, g, t] = decay * weights_in[b, g, t]
+ *                            + sum over the query heads h of KV head g of p(h, t)
+ * for t < seq_lens[b]; entries behind are left as they were. p is what a
+ * decode of the same q gave token t:
+ *     alpha = 1  p = exp(z_t - tau), tau the lse of a softmax decode;
+ *     alpha > 1  p = [(alpha-1) z_t - tau]_+^(1/(alpha-1)), tau that of
+ *                entmaxkv_decode_full (for a sparse decode it is the weight
+ *                that its tau gives, on unselected pages too).
+ * Tokens outside the window and the sinks of position seq_lens[b] - 1 (as in
+ * entmaxkv_softmax_window; window >= 1, any larger than the sequences for
+ * none) and tokens of invalid pages have p = 0. The sums over heads are
+ * float32.
+ *   q            q_dtype [batch, num_q_heads, head_dim] (types as above)
+ *   alpha        >= 1 and finite; decay finite (else ENTMAXKV_ERR_INVALID)
+ *   tau          float32 [batch, num_q_heads]
+ *   weights_in   float32 [batch, num_kv_heads, max_pages_per_seq * page_size],
+ *                by logical token; nullable: all zero
+ *   weights_out  the same shape; may be weights_in itself
+ * Kernels launched: 1.
+ */
+int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
+                                const void* k_pool, const int32_t* block_table,
+                                const int32_t* seq_lens, float alpha, const float* tau,
+                                int32_t window, int32_t sinks, float decay,
+                                const float* weights_in, float* weights_out, hipStream_t stream,
+                                hipEvent_t* events);
+
+/*
+ * Eviction by accumulated weight: keeps n = min(seq_lens[b], keep) tokens of
+ * each (sequence, KV head) and copies their K and V rows, in token order, to
+ * new pages. A sequence of at most `keep` tokens keeps them all; of a longer
+ * one the first `sinks` tokens, the last `recent` tokens and, of those
+ * between, the keep - sinks - recent with the largest weights stay (ties to
+ * the lower token; -0 equals +0, a NaN counts as the largest).
+ *   keep         1 .. 2^25; sinks, recent >= 0 with sinks + recent <= keep (else
+ *                ENTMAXKV_ERR_INVALID)
+ *   weights      float32 [batch, num_kv_heads, max_pages_per_seq * page_size]
+ *   new_table    int32 [batch, max_pages_per_seq], the block table afterwards:
+ *                its first ceil(n / page_size) columns name the pages written,
+ *                which no sequence may read in this call (a page that is read
+ *                and written gives wrong rows) and which are distinct
+ *   kept         int32 [batch, num_kv_heads, keep]: the kept tokens'
+ *                positions before the call, ascending, then -1
+ *   new_lens     int32 [batch]: n
+ *   new_weights  nullable, the shape of weights: the kept tokens' weights by
+ *                their new position, then 0
+ * The old pages keep their rows (a prefix shared with other sequences stays
+ * whole). Slots of an invalid page, old or new, are not copied. The outputs
+ * may not overlap the inputs they replace (the same pointer is
+ * ENTMAXKV_ERR_INVALID). Page boxes and moments of the new pages are built by
+ * entmaxkv_build_page_meta / _moments with new_table and new_lens. Kernels
+ * launched: 2 (selection, copy).
+ */
+int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
+                   const int32_t* block_table, const int32_t* seq_lens, const float* weights,
+                   int32_t keep, int32_t sinks, int32_t recent, const int32_t* new_table,
+                   int32_t* kept, int32_t* new_lens, float* new_weights, hipStream_t stream,
+                   hipEvent_t* events);
+
+/*
  * Workspace size in bytes for `which` (ENTMAXKV_WS_*) at this shape and
  * budget (budget is ignored for ENTMAXKV_WS_FULL). Writes *bytes and returns
  * ENTMAXKV_OK, or an error code for an invalid or unsupported shape.

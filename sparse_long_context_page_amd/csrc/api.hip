@@ -300,6 +300,74 @@ int topk_ws(const LaunchShape& s, int budget, TopkWs* w) {
   return ENTMAXKV_OK;
 }
 
+// Windows and sinks beyond every sequence mean all of it; clamped so that
+// positions plus either stay inside int32.
+constexpr int32_t kMaxWindow = 1 << 25;
+
+int check_window(int32_t* window, int32_t* sinks) {
+  if (*window <= 0 || *sinks < 0) return ENTMAXKV_ERR_INVALID;
+  if (*window > kMaxWindow) *window = kMaxWindow;
+  if (*sinks > kMaxWindow) *sinks = kMaxWindow;
+  return ENTMAXKV_OK;
+}
+
+int check_q_dtype(const LaunchShape& s, int32_t q_dtype) {
+  if (q_dtype != ENTMAXKV_F32 && q_dtype != ENTMAXKV_BF16) return ENTMAXKV_ERR_UNSUPPORTED;
+  // a bf16 query against a float32 cache is not built
+  return q_dtype == ENTMAXKV_BF16 && !s.bf16 ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
+}
+
+int check_plan(const AttendPlan& p) {
+  return p.items > 0x7fffffffLL ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
+}
+
+int window_plan(const entmaxkv_shape* shape, int32_t q_tokens, int32_t* window, int32_t* sinks,
+                LaunchShape* s, AttendPlan* p) {
+  int rc = check_shape(shape, s);
+  if (rc) return rc;
+  if (q_tokens <= 0) return ENTMAXKV_ERR_INVALID;
+  if ((rc = check_window(window, sinks))) return rc;
+  if ((long long)s->batch * s->num_q_heads * q_tokens > (1LL << 24))
+    return ENTMAXKV_ERR_UNSUPPORTED;
+  *p = plan_attend(*s, q_tokens, *window, *sinks, 0);
+  return check_plan(*p);
+}
+
+int prefix_plan(const entmaxkv_shape* shape, int32_t prefix_pages, LaunchShape* s,
+                AttendPlan* p) {
+  int rc = check_shape(shape, s);
+  if (rc) return rc;
+  if (prefix_pages <= 0 || prefix_pages > s->max_pages) return ENTMAXKV_ERR_INVALID;
+  *p = plan_attend(*s, 1, kMaxWindow, 0, prefix_pages);
+  return check_plan(*p);
+}
+
+int attend_common(const LaunchShape& s, const AttendPlan& p, const void* q, int32_t q_dtype,
+                  int n, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+                  int prefix_pages, const int32_t* block_table, const int32_t* seq_lens,
+                  int window, int sinks, void* out, float* lse, void* ws, size_t ws_bytes,
+                  hipStream_t stream, hipEvent_t* events) {
+  if (int rc = check_q_dtype(s, q_dtype)) return rc;
+  if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out) return ENTMAXKV_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
+    return ENTMAXKV_ERR_INVALID;
+  if (p.ws_bytes) {
+    if (!ws || ws_bytes < p.ws_bytes) return ENTMAXKV_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return ENTMAXKV_ERR_INVALID;
+  }
+  const bool q_bf16 = q_dtype == ENTMAXKV_BF16;
+  const Events ev{events, stream};
+  if (!ev.before(0)) return ENTMAXKV_ERR_HIP;
+  if (launch_attend(s, p, q, q_bf16, n, k_pool, v_pool, prefix_table, prefix_pages, block_table,
+                    seq_lens, window, sinks, out, lse, ws, stream) != hipSuccess)
+    return ENTMAXKV_ERR_HIP;
+  if (!ev.after(0) || !ev.before(1)) return ENTMAXKV_ERR_HIP;
+  if (p.slots > 1 && launch_join(s, p, q_bf16, out, lse, ws, stream) != hipSuccess)
+    return ENTMAXKV_ERR_HIP;
+  if (!ev.after(1)) return ENTMAXKV_ERR_HIP;
+  return ENTMAXKV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -594,6 +662,111 @@ int entmaxkv_decode_full(const entmaxkv_shape* shape, const float* q, const void
                          hipEvent_t* events) {
   return decode_common(shape, q, k_pool, v_pool, block_table, seq_lens, nullptr, 0, alpha, out,
                        tau, support, ws, ws_bytes, stream, events);
+}
+
+
+int entmaxkv_softmax_window_ws(const entmaxkv_shape* shape, int32_t q_tokens, int32_t window,
+                               int32_t sinks, size_t* bytes) {
+  LaunchShape s;
+  AttendPlan p;
+  if (int rc = window_plan(shape, q_tokens, &window, &sinks, &s, &p)) return rc;
+  if (!bytes) return ENTMAXKV_ERR_INVALID;
+  *bytes = p.ws_bytes;
+  return ENTMAXKV_OK;
+}
+
+int entmaxkv_softmax_window(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
+                            int32_t q_tokens, const void* k_pool, const void* v_pool,
+                            const int32_t* block_table, const int32_t* seq_lens, int32_t window,
+                            int32_t sinks, void* out, float* lse, void* ws, size_t ws_bytes,
+                            hipStream_t stream, hipEvent_t* events) {
+  LaunchShape s;
+  AttendPlan p;
+  if (int rc = window_plan(shape, q_tokens, &window, &sinks, &s, &p)) return rc;
+  return attend_common(s, p, q, q_dtype, q_tokens, k_pool, v_pool, nullptr, 0, block_table,
+                       seq_lens, window, sinks, out, lse, ws, ws_bytes, stream, events);
+}
+
+int entmaxkv_softmax_prefix_ws(const entmaxkv_shape* shape, int32_t prefix_pages, size_t* bytes) {
+  LaunchShape s;
+  AttendPlan p;
+  if (int rc = prefix_plan(shape, prefix_pages, &s, &p)) return rc;
+  if (!bytes) return ENTMAXKV_ERR_INVALID;
+  *bytes = p.ws_bytes;
+  return ENTMAXKV_OK;
+}
+
+int entmaxkv_softmax_prefix(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
+                            const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+                            int32_t prefix_pages, const int32_t* block_table,
+                            const int32_t* seq_lens, void* out, float* lse, void* ws,
+                            size_t ws_bytes, hipStream_t stream, hipEvent_t* events) {
+  LaunchShape s;
+  AttendPlan p;
+  if (int rc = prefix_plan(shape, prefix_pages, &s, &p)) return rc;
+  if (!prefix_table) return ENTMAXKV_ERR_INVALID;
+  return attend_common(s, p, q, q_dtype, 1, k_pool, v_pool, prefix_table, prefix_pages,
+                       block_table, seq_lens, kMaxWindow, 0, out, lse, ws, ws_bytes, stream,
+                       events);
+}
+
+int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
+                                const void* k_pool, const int32_t* block_table,
+                                const int32_t* seq_lens, float alpha, const float* tau,
+                                int32_t window, int32_t sinks, float decay,
+                                const float* weights_in, float* weights_out, hipStream_t stream,
+                                hipEvent_t* events) {
+  LaunchShape s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if ((rc = check_q_dtype(s, q_dtype))) return rc;
+  if (!isfinite(alpha) || !(alpha >= 1.0f) || !isfinite(decay)) return ENTMAXKV_ERR_INVALID;
+  if ((rc = check_window(&window, &sinks))) return rc;
+  if (!q || !k_pool || !block_table || !seq_lens || !tau || !weights_out)
+    return ENTMAXKV_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k_pool, 16)) return ENTMAXKV_ERR_INVALID;
+  const Events ev{events, stream};
+  if (!ev.before(0)) return ENTMAXKV_ERR_HIP;
+  if (launch_weights(s, q, q_dtype == ENTMAXKV_BF16, k_pool, block_table, seq_lens, alpha, tau,
+                     window, sinks, decay, weights_in, weights_out, stream) != hipSuccess)
+    return ENTMAXKV_ERR_HIP;
+  if (!ev.after(0)) return ENTMAXKV_ERR_HIP;
+  return ENTMAXKV_OK;
+}
+
+int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
+                   const int32_t* block_table, const int32_t* seq_lens, const float* weights,
+                   int32_t keep, int32_t sinks, int32_t recent, const int32_t* new_table,
+                   int32_t* kept, int32_t* new_lens, float* new_weights, hipStream_t stream,
+                   hipEvent_t* events) {
+  LaunchShape s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if (keep <= 0 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
+    return ENTMAXKV_ERR_INVALID;
+  const long long max_tokens = (long long)s.max_pages * s.page_size;
+  if (keep > kMaxWindow) return ENTMAXKV_ERR_UNSUPPORTED;
+  // at most one workgroup per 64 tokens of a (sequence, KV head)
+  if ((long long)s.batch * s.num_kv_heads * (max_tokens / 64 + 2) > 0x7fffffffLL)
+    return ENTMAXKV_ERR_UNSUPPORTED;
+  if (!k_pool || !v_pool || !block_table || !seq_lens || !weights || !new_table || !kept ||
+      !new_lens)
+    return ENTMAXKV_ERR_INVALID;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16)) return ENTMAXKV_ERR_INVALID;
+  // the copies run in any order
+  if (new_weights == weights || new_lens == seq_lens || new_table == block_table)
+    return ENTMAXKV_ERR_INVALID;
+  const Events ev{events, stream};
+  if (!ev.before(0)) return ENTMAXKV_ERR_HIP;
+  if (launch_evict_select(s, seq_lens, weights, keep, sinks, recent, kept, new_lens, stream) !=
+      hipSuccess)
+    return ENTMAXKV_ERR_HIP;
+  if (!ev.after(0) || !ev.before(1)) return ENTMAXKV_ERR_HIP;
+  if (launch_evict_copy(s, k_pool, v_pool, block_table, seq_lens, weights, keep, new_table, kept,
+                        new_weights, stream) != hipSuccess)
+    return ENTMAXKV_ERR_HIP;
+  if (!ev.after(1)) return ENTMAXKV_ERR_HIP;
+  return ENTMAXKV_OK;
 }
 
 }  // extern "C"

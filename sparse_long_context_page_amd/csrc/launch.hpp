@@ -278,5 +278,37 @@ hipError_t launch_tau_pv_f32(const LaunchShape& s, const SplitPlan& p, const voi
                              int budget, float alpha, float window, float* out, float* tau,
                              int32_t* support, void* ws, const DecodeWs& L, hipStream_t st);
 
+// Softmax attention (softmax.hip). A row block is 16 query rows of one KV
+// head; its tokens are split over `splits` workgroups (`pre_splits` over the
+// shared prefix), whose parts are joined by a second kernel when there is
+// more than one per row.
+constexpr int kAttWgsPerCU = 2;     // workgroups a CU holds at the kernel's register use
+constexpr int kAttMaxSplits = 256;  // parts of a row block
+struct AttendPlan {
+  long long rows = 0, items = 0, pre_items = 0;
+  int pre_tiles = 0, pre_splits = 0, row_tiles = 0, splits = 0, slots = 0;
+  size_t ml_off = 0, ws_bytes = 0;
+};
+AttendPlan plan_attend(const LaunchShape& s, int n, int window, int sinks, int prefix_pages);
+hipError_t launch_attend(const LaunchShape& s, const AttendPlan& p, const void* q, bool q_bf16,
+                         int n, const void* k_pool, const void* v_pool,
+                         const int32_t* prefix_table, int prefix_pages,
+                         const int32_t* block_table, const int32_t* seq_lens, int window,
+                         int sinks, void* out, float* lse, void* ws, hipStream_t st);
+hipError_t launch_join(const LaunchShape& s, const AttendPlan& p, bool q_bf16, void* out,
+                       float* lse, void* ws, hipStream_t st);
+
+// Attention weights and eviction (evict.hip).
+hipError_t launch_weights(const LaunchShape& s, const void* q, bool q_bf16, const void* k_pool,
+                          const int32_t* bt, const int32_t* lens, float alpha, const float* tau,
+                          int window, int sinks, float decay, const float* w_in, float* w_out,
+                          hipStream_t st);
+hipError_t launch_evict_select(const LaunchShape& s, const int32_t* lens, const float* weights,
+                               int keep, int sinks, int recent, int32_t* kept,
+                               int32_t* new_lens, hipStream_t st);
+hipError_t launch_evict_copy(const LaunchShape& s, void* k_pool, void* v_pool, const int32_t* bt,
+                             const int32_t* lens, const float* weights, int keep,
+                             const int32_t* new_table, const int32_t* kept, float* new_weights,
+                             hipStream_t st);
 
 }  // namespace ekv

@@ -1,0 +1,371 @@
+// Tiles of the paged cache in registers and their products on the matrix
+// cores, shared by the softmax decode and the attention-weight kernels.
+//
+// Scores are computed transposed, S^T = K Q^T (A = K: 16 tokens, B = Q: 16
+// query rows), so that a lane holds the scores of ONE row (lane % 16) for the
+// tokens of its lane group (lane / 16). These are the lanes and registers
+// that the second product, O^T = V^T P^T, wants its B operand P^T in: the
+// tokens of a bf16 tile are dealt to the A rows so that group c ends with
+// tokens 8c .. 8c+7 (k indices of the 16x16x32 instruction), those of a
+// float32 tile so that element i of group c is token 4c + i (k = c of the
+// i-th 16x16x4 instruction). No value crosses lanes between the products, and
+// row statistics, scores and outputs all sit at row = lane % 16.
+#pragma once
+
+#include <float.h>
+
+#include <type_traits>
+
+#include "launch.hpp"
+#include "mfma.hpp"
+
+namespace ekv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Tokens of one tile: two 16-token score tiles for bf16 caches (the 32 k
+// indices of one V^T P^T instruction), one for float32 caches. A tile starts
+// at a multiple of its length, so it lies in one page, or in two of 16 rows.
+template <bool BF>
+constexpr int kTile = BF ? 32 : 16;
+
+// The physical pages of one tile: p0, and p1 for tokens 16..31 of a bf16 tile
+// in 16-row pages (else equal to p0); -1 where the page table entry is not a
+// physical page (such tokens are masked and page 0 is read in their place).
+struct TilePages {
+  int p0, p1;
+};
+
+// Geometry that the tile loads need: the pool, the rows of a page and the KV
+// head, as byte strides.
+struct KvView {
+  const char* base;   // pool + KV head offset
+  size_t page_bytes;  // num_kv_heads * page_size * head_dim * element size
+  int page_size;      // a power of two
+};
+
+template <bool BF, int D>
+__device__ __forceinline__ const char* row_ptr(const KvView& v, const TilePages& p, int t0,
+                                               int tok) {
+  constexpr int kRow = D * (BF ? 2 : 4);
+  int pg = p.p0;
+  if constexpr (BF) pg = (v.page_size == 16 && tok >= 16) ? p.p1 : p.p0;
+  const int row = (t0 + tok) & (v.page_size - 1);
+  return v.base + (size_t)max(pg, 0) * v.page_bytes + (size_t)row * kRow;
+}
+
+template <bool kStream, typename T>
+__device__ __forceinline__ T load_vec(const char* p) {
+  if constexpr (kStream) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+  return *reinterpret_cast<const T*>(p);
+}
+
+// ---------------------------------------------------------------------------
+// bf16 <-> float32 splits
+
+// x = p0 + p1 + p2 exactly, each part a bf16 value (the top 8 significant
+// bits left of what remains): parts as float32 with the low half clear.
+__device__ __forceinline__ void split3(float x, uint32_t (&p)[3]) {
+  p[0] = __float_as_uint(x) & 0xffff0000u;
+  const float r1 = x - __uint_as_float(p[0]);
+  p[1] = __float_as_uint(r1) & 0xffff0000u;
+  p[2] = __float_as_uint(r1 - __uint_as_float(p[1]));
+}
+
+// (hi16(b) << 16) | hi16(a): two bf16 values of one register pair
+__device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+__device__ __forceinline__ uint32_t pack_lo(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x05040100u);
+}
+
+// bf16 bits of x rounded to nearest even, NaN kept
+__device__ __forceinline__ uint32_t bf16_round(float x) {
+  return x != x ? 0x7fc0u : bf16_rne_bits(x);
+}
+
+__device__ __forceinline__ bf16x8 as_bf(const u32x4& v) { return __builtin_bit_cast(bf16x8, v); }
+
+// ---------------------------------------------------------------------------
+// Query rows as the B operand
+
+// PARTS: bf16 parts of a query value (3 for float32 queries: the exact split
+// above, so products with bf16 keys are exact; 1 for bf16 queries).
+template <bool BF, int D, int PARTS>
+struct QFrag;
+
+template <int D, int PARTS>
+struct QFrag<true, D, PARTS> {
+  u32x4 f[PARTS][D / 32];
+  // `row`: the row's first value (null: a row of zeros)
+  __device__ __forceinline__ void load(const char* row, int c) {
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+      const int d = s * 32 + c * 8;
+      if constexpr (PARTS == 1) {
+        f[0][s] = row ? *reinterpret_cast<const u32x4*>(row + 2 * d) : u32x4{0, 0, 0, 0};
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4 x = row ? *reinterpret_cast<const f32x4*>(row + 4 * (d + 4 * h))
+                              : f32x4{0, 0, 0, 0};
+          uint32_t p[4][3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split3(x[e], p[e]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            f[k][s][2 * h] = pack_hi(p[0][k], p[1][k]);
+            f[k][s][2 * h + 1] = pack_hi(p[2][k], p[3][k]);
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int D, int PARTS>
+struct QFrag<false, D, PARTS> {
+  f32x4 f[D / 16];
+  __device__ __forceinline__ void load(const char* row, int c) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      f[s] = row ? *reinterpret_cast<const f32x4*>(row + 4 * (s * 16 + c * 4))
+                 : f32x4{0, 0, 0, 0};
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Key tiles and scores. z[i]: the score of this lane's row and token
+// tile_token<BF>(lane group, i).
+
+template <bool BF>
+__device__ __forceinline__ constexpr int scores_per_lane() { return BF ? 8 : 4; }
+
+template <bool BF>
+__device__ __forceinline__ int tile_token(int c, int i) { return BF ? c * 8 + i : c * 4 + i; }
+
+template <bool BF, int D>
+struct KTile;
+
+template <int D>
+struct KTile<true, D> {
+  u32x4 f[2][D / 32];
+  template <bool kStream>
+  __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0, int lane) {
+    const int m = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const char* r = row_ptr<true, D>(v, p, t0, ((m >> 2) << 3) + u * 4 + (m & 3)) + c * 16;
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) f[u][s] = load_vec<kStream, u32x4>(r + s * 64);
+    }
+  }
+  template <int PARTS>
+  __device__ __forceinline__ void scores(const QFrag<true, D, PARTS>& q, float (&z)[8]) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = PARTS - 1; k >= 0; --k)
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s)
+          a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(f[u][s]), as_bf(q.f[k][s]), a, 0, 0,
+                                                      0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[u * 4 + i] = a[i];
+    }
+  }
+};
+
+template <int D>
+struct KTile<false, D> {
+  f32x4 f[D / 16];
+  template <bool kStream>
+  __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0, int lane) {
+    const char* r = row_ptr<false, D>(v, p, t0, lane & 15) + (lane >> 4) * 16;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) f[s] = load_vec<kStream, f32x4>(r + s * 64);
+  }
+  template <int PARTS>
+  __device__ __forceinline__ void scores(const QFrag<false, D, PARTS>& q, float (&z)[4]) const {
+    // four sums of D/4 products each: shorter chains round less (one chain:
+    // 1.8 times the error at D = 128) and do not wait for each other
+    f32x4 a[4] = {{0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        a[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[s][e], q.f[s][e], a[e], 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = (a[0][i] + a[1][i]) + (a[2][i] + a[3][i]);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Output accumulator: rows x D, spread as acc[n][i]; `first(c, n, i)` below
+// says which coordinates a lane holds.
+
+template <bool BF, int D>
+struct VTile;
+
+// Each lane loads D/16 neighbouring coordinates of the 8 tokens of its group
+// (a whole row per 16 lanes) and transposes them in registers: instruction n
+// takes coordinate n of every lane, so its 16 A rows are d = (D/16) m + n.
+template <int D>
+struct VTile<true, D> {
+  static constexpr int kAcc = D / 16;
+  typedef typename std::conditional<D == 128, u32x4, u32x2>::type vec;
+  vec f[8];
+  template <bool kStream>
+  __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0, int lane) {
+    const int m = lane & 15, c = lane >> 4;
+    const char* r = row_ptr<true, D>(v, p, t0, c * 8) + m * (D / 8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = load_vec<kStream, vec>(r + j * (D * 2));
+  }
+  __device__ __forceinline__ void clear(int j) { f[j] = vec(0); }
+  // An infinity or NaN among the values held?
+  __device__ __forceinline__ bool any_nonfinite() const {
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        bad |= (f[j][e] & 0x7f800000u) == 0x7f800000u || (f[j][e] & 0x7f80u) == 0x7f80u;
+    return bad;
+  }
+  // acc += V^T P^T with P in PP bf16 parts: 3 (p exact), 2 (p to 16
+  // significant bits) or 1 (rounded to nearest even)
+  // kMine: only lanes with `mine` take the sums
+  template <int PP, bool kMine = false>
+  __device__ __forceinline__ void pv(const float (&p)[8], f32x4 (&acc)[kAcc],
+                                     bool mine = true) const {
+    u32x4 b[PP];
+    if constexpr (PP == 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        b[0][k] = bf16_round(p[2 * k]) | (bf16_round(p[2 * k + 1]) << 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t x[3], y[3];
+        split3(p[2 * k], x);
+        split3(p[2 * k + 1], y);
+#pragma unroll
+        for (int s = 0; s < PP; ++s) b[s][k] = pack_hi(x[s], y[s]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kAcc; ++n) {
+      u32x4 a;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        a[k] = (n & 1) ? pack_hi(f[2 * k][n / 2], f[2 * k + 1][n / 2])
+                       : pack_lo(f[2 * k][n / 2], f[2 * k + 1][n / 2]);
+      f32x4 o = kMine ? f32x4{0, 0, 0, 0} : acc[n];
+#pragma unroll
+      for (int s = PP - 1; s >= 0; --s)
+        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(a), as_bf(b[s]), o, 0, 0, 0);
+      if constexpr (kMine) {
+        if (mine) acc[n] += o;
+      } else {
+        acc[n] = o;
+      }
+    }
+  }
+  // coordinate of acc[n][i]
+  __device__ __forceinline__ static int coord(int c, int n, int i) {
+    return (c * 4 + i) * (D / 16) + n;
+  }
+};
+
+template <int D>
+struct VTile<false, D> {
+  static constexpr int kAcc = D / 16;
+  f32x4 f[4][D / 64];
+  template <bool kStream>
+  __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0, int lane) {
+    const int m = lane & 15, c = lane >> 4;
+    const char* r = row_ptr<false, D>(v, p, t0, c * 4) + m * 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        f[j][h] = load_vec<kStream, f32x4>(r + j * (D * 4) + h * 256);
+  }
+  __device__ __forceinline__ void clear(int j) {
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) f[j][h] = f32x4{0, 0, 0, 0};
+  }
+  __device__ __forceinline__ bool any_nonfinite() const {
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          bad |= (__float_as_uint(f[j][h][e]) & 0x7f800000u) == 0x7f800000u;
+    return bad;
+  }
+  template <int PP, bool kMine = false>
+  __device__ __forceinline__ void pv(const float (&p)[4], f32x4 (&acc)[kAcc],
+                                     bool mine = true) const {
+#pragma unroll
+    for (int n = 0; n < kAcc; ++n) {
+      f32x4 o = kMine ? f32x4{0, 0, 0, 0} : acc[n];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o = __builtin_amdgcn_mfma_f32_16x16x4f32(f[j][n >> 2][n & 3], p[j], o, 0, 0, 0);
+      if constexpr (kMine) {
+        if (mine) acc[n] += o;
+      } else {
+        acc[n] = o;
+      }
+    }
+  }
+  __device__ __forceinline__ static int coord(int c, int n, int i) {
+    return (n >> 2) * 64 + (c * 4 + i) * 4 + (n & 3);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// The tokens a block of rows sees
+
+// Row r sees tokens t < hi_r with t >= lo_r or t < sinks. A block's tiles are
+// those of [0, sinks) and of [lo, hi) (lo the least lo_r, hi the largest
+// hi_r), each once: ordinal v is tile v below ns, else tile v - ns + mt0.
+struct TileSpan {
+  int ns, mt0, n;
+  __device__ __forceinline__ int tile(int v) const { return v < ns ? v : v - ns + mt0; }
+};
+
+template <int TT>
+__device__ __forceinline__ TileSpan tile_span(int lo, int hi, int sinks) {
+  TileSpan s;
+  if (hi <= 0) {
+    s.ns = s.mt0 = s.n = 0;
+    return s;
+  }
+  s.mt0 = min(lo, hi) / TT;
+  s.ns = min((min(sinks, hi) + TT - 1) / TT, s.mt0);
+  s.n = s.ns + (hi + TT - 1) / TT - s.mt0;
+  return s;
+}
+
+// max over the four lanes that share lane % 16
+__device__ __forceinline__ float group_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16, kWave));
+  return fmaxf(x, __shfl_xor(x, 32, kWave));
+}
+__device__ __forceinline__ float group_sum(float x) {
+  x += __shfl_xor(x, 16, kWave);
+  return x + __shfl_xor(x, 32, kWave);
+}
+
+}  // namespace ekv

@@ -9,7 +9,9 @@ The function names match the C ABI:
     entmaxkv_build_page_meta, entmaxkv_append_page_meta, entmaxkv_score_select,
     entmaxkv_score_select_noalloc, entmaxkv_decode_sparse, entmaxkv_decode_topk,
     entmaxkv_decode_full, entmaxkv_build_page_moments,
-    entmaxkv_append_page_moments, entmaxkv_gauss_select, entmaxkv_workspace_bytes,
+    entmaxkv_append_page_moments, entmaxkv_gauss_select, entmaxkv_softmax_window,
+    entmaxkv_softmax_prefix, entmaxkv_accumulate_weights, entmaxkv_evict,
+    entmaxkv_workspace_bytes, entmaxkv_softmax_window_ws, entmaxkv_softmax_prefix_ws,
     entmaxkv_topk_kernels, entmaxkv_strerror
 """
 from __future__ import annotations
@@ -40,7 +42,10 @@ ENTMAXKV_WS_TOPK = 4
 KERNELS = {"build_page_meta": 1, "append_page_meta": 1, "score_select": 2,
            "score_select_noalloc": 2, "decode_sparse": 2, "decode_topk": 4,
            "decode_full": 2, "build_page_moments": 1, "append_page_moments": 1,
-           "gauss_select": 2}
+           "gauss_select": 2, "softmax_window": 2, "softmax_prefix": 2, "accumulate_weights": 1,
+           "evict": 2}
+
+FULL_WINDOW = 2**31 - 1  # a window that hides no token
 
 
 class Shape(ctypes.Structure):
@@ -80,6 +85,14 @@ def _load() -> ctypes.CDLL:
     lib.entmaxkv_build_page_moments.argtypes = [SP, P, P, P, P, P, P]
     lib.entmaxkv_append_page_moments.argtypes = [SP, P, P, P, P, I32, P, P, P]
     lib.entmaxkv_gauss_select.argtypes = [SP, P, P, P, P, F32, F32, I32, P, P, P, SZ, P, P]
+    lib.entmaxkv_softmax_window.argtypes = [SP, P, I32, I32, P, P, P, P, I32, I32, P, P, P, SZ, P,
+                                            P]
+    lib.entmaxkv_softmax_window_ws.argtypes = [SP, I32, I32, I32, ctypes.POINTER(SZ)]
+    lib.entmaxkv_softmax_prefix.argtypes = [SP, P, I32, P, P, P, I32, P, P, P, P, P, SZ, P, P]
+    lib.entmaxkv_softmax_prefix_ws.argtypes = [SP, I32, ctypes.POINTER(SZ)]
+    lib.entmaxkv_accumulate_weights.argtypes = [SP, P, I32, P, P, P, F32, P, I32, I32, F32, P, P,
+                                                P, P]
+    lib.entmaxkv_evict.argtypes = [SP, P, P, P, P, P, I32, I32, I32, P, P, P, P, P, P]
     lib.entmaxkv_workspace_bytes.argtypes = [SP, I32, I32, ctypes.POINTER(SZ)]
     lib.entmaxkv_topk_kernels.argtypes = [SP, I32, ctypes.POINTER(I32)]
     lib.entmaxkv_strerror.argtypes = [ctypes.c_int]
@@ -89,8 +102,10 @@ def _load() -> ctypes.CDLL:
                  "entmaxkv_score_select", "entmaxkv_score_select_noalloc",
                  "entmaxkv_decode_sparse", "entmaxkv_decode_topk", "entmaxkv_decode_full",
                  "entmaxkv_build_page_moments", "entmaxkv_append_page_moments",
-                 "entmaxkv_gauss_select", "entmaxkv_workspace_bytes", "entmaxkv_topk_kernels",
-                 "entmaxkv_version"):
+                 "entmaxkv_gauss_select", "entmaxkv_softmax_window",
+                 "entmaxkv_softmax_window_ws", "entmaxkv_softmax_prefix",
+                 "entmaxkv_softmax_prefix_ws", "entmaxkv_accumulate_weights", "entmaxkv_evict",
+                 "entmaxkv_workspace_bytes", "entmaxkv_topk_kernels", "entmaxkv_version"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -371,12 +386,159 @@ def _args_decode_full(shape: Shape, q, k_pool, v_pool, block_table, seq_lens, al
         _stream(stream, q.device), None], ws
 
 
+def _one_device(**tensors):
+    """As _on_device, and all of them on the same device."""
+    _on_device(**tensors)
+    devices = {t.device for t in tensors.values() if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"tensors are on several devices: {sorted(map(str, devices))}")
+
+
+def _q_dtype(shape: Shape, q) -> int:
+    """Query type of the softmax calls: float32, or bfloat16 with a bf16 cache."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch tensor")
+    if q.dtype == torch.float32:
+        return ENTMAXKV_F32
+    if q.dtype == torch.bfloat16 and shape.kv_dtype == ENTMAXKV_BF16:
+        return ENTMAXKV_BF16
+    raise TypeError(f"q has dtype {q.dtype}; the softmax calls take float32, or bfloat16 with a "
+                    "bf16 cache")
+
+
+def _max_tokens(shape: Shape) -> int:
+    return shape.max_pages_per_seq * shape.page_size
+
+
+def entmaxkv_softmax_window_ws(shape: Shape, q_tokens: int, window: int, sinks: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib.entmaxkv_softmax_window_ws(ctypes.byref(shape), int(q_tokens), int(window),
+                                          int(sinks), ctypes.byref(out)),
+           "entmaxkv_softmax_window_ws")
+    return int(out.value)
+
+
+def entmaxkv_softmax_prefix_ws(shape: Shape, prefix_pages: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib.entmaxkv_softmax_prefix_ws(ctypes.byref(shape), int(prefix_pages),
+                                          ctypes.byref(out)), "entmaxkv_softmax_prefix_ws")
+    return int(out.value)
+
+
+def _given_or_new(ws, nbytes, q, stream):
+    """(pointer, bytes, tensor) of a workspace of `nbytes`. One allocated here
+    is the allocator's again when the call returns, so it is marked as in use
+    by the stream that the kernels run on."""
+    if ws is None:
+        if nbytes == 0:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+                stream = torch.cuda.ExternalStream(raw, device=q.device)
+            ws.record_stream(stream)
+    else:
+        _ptr(ws, "ws")
+        _one_device(q=q, ws=ws)
+    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), ws
+
+
+def _softmax_ptrs(shape: Shape, q, q_tokens, k_pool, v_pool, block_table, seq_lens, out, lse):
+    n = _Sizes(shape)
+    qd = _q_dtype(shape, q)
+    q_tokens = max(int(q_tokens), 0)
+    return qd, (_ptr(q, "q", numel=n.q * q_tokens),
+                _ptr(k_pool, "k_pool", _kv_dtypes(shape), numel=n.pool),
+                _ptr(v_pool, "v_pool", _kv_dtypes(shape), numel=n.pool),
+                _ptr(block_table, "block_table", (torch.int32,), numel=n.block_table),
+                _ptr(seq_lens, "seq_lens", (torch.int32,), numel=n.batch),
+                _ptr(out, "out", (q.dtype,), numel=n.out * q_tokens),
+                _ptr(lse, "lse", (torch.float32,), nullable=True, numel=n.heads * q_tokens))
+
+
+def _args_softmax_window(shape: Shape, q, k_pool, v_pool, block_table, seq_lens, window, sinks,
+                         out, lse=None, q_tokens=1, ws=None, stream=None):
+    qd, (pq, pk, pv, pbt, pl, po, pe) = _softmax_ptrs(shape, q, q_tokens, k_pool, v_pool,
+                                                      block_table, seq_lens, out, lse)
+    _one_device(q=q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, seq_lens=seq_lens,
+                out=out, lse=lse)
+    need = 0 if ws is not None else entmaxkv_softmax_window_ws(shape, q_tokens, window, sinks)
+    pw, nw, ws = _given_or_new(ws, need, q, stream)
+    return lib.entmaxkv_softmax_window, [
+        ctypes.byref(shape), pq, qd, int(q_tokens), pk, pv, pbt, pl, int(window), int(sinks), po,
+        pe, pw, nw, _stream(stream, q.device), None], ws
+
+
+def _args_softmax_prefix(shape: Shape, q, k_pool, v_pool, prefix_table, prefix_pages,
+                         block_table, seq_lens, out, lse=None, ws=None, stream=None):
+    qd, (pq, pk, pv, pbt, pl, po, pe) = _softmax_ptrs(shape, q, 1, k_pool, v_pool, block_table,
+                                                      seq_lens, out, lse)
+    ppt = _ptr(prefix_table, "prefix_table", (torch.int32,), numel=max(int(prefix_pages), 0))
+    _one_device(q=q, k_pool=k_pool, v_pool=v_pool, prefix_table=prefix_table,
+                block_table=block_table, seq_lens=seq_lens, out=out, lse=lse)
+    need = 0 if ws is not None else entmaxkv_softmax_prefix_ws(shape, prefix_pages)
+    pw, nw, ws = _given_or_new(ws, need, q, stream)
+    return lib.entmaxkv_softmax_prefix, [
+        ctypes.byref(shape), pq, qd, pk, pv, ppt, int(prefix_pages), pbt, pl, po, pe, pw, nw,
+        _stream(stream, q.device), None], ws
+
+
+def _args_accumulate_weights(shape: Shape, q, k_pool, block_table, seq_lens, alpha, tau, decay,
+                             weights_in, weights_out, window=FULL_WINDOW, sinks=0, stream=None):
+    n = _Sizes(shape)
+    cells = shape.batch * shape.num_kv_heads * _max_tokens(shape)
+    qd = _q_dtype(shape, q)
+    pq = _ptr(q, "q", numel=n.q)
+    pk = _ptr(k_pool, "k_pool", _kv_dtypes(shape), numel=n.pool)
+    pbt = _ptr(block_table, "block_table", (torch.int32,), numel=n.block_table)
+    pl = _ptr(seq_lens, "seq_lens", (torch.int32,), numel=n.batch)
+    pt = _ptr(tau, "tau", (torch.float32,), numel=n.heads)
+    pi = _ptr(weights_in, "weights_in", (torch.float32,), nullable=True, numel=cells)
+    po = _ptr(weights_out, "weights_out", (torch.float32,), numel=cells)
+    _one_device(q=q, k_pool=k_pool, block_table=block_table, seq_lens=seq_lens, tau=tau,
+                weights_in=weights_in, weights_out=weights_out)
+    return lib.entmaxkv_accumulate_weights, [
+        ctypes.byref(shape), pq, qd, pk, pbt, pl, float(alpha), pt, int(window), int(sinks),
+        float(decay), pi, po, _stream(stream, q.device), None]
+
+
+def _args_evict(shape: Shape, k_pool, v_pool, block_table, seq_lens, weights, keep, sinks, recent,
+                new_table, kept, new_lens, new_weights=None, stream=None):
+    n = _Sizes(shape)
+    rows = shape.batch * shape.num_kv_heads
+    cells = rows * _max_tokens(shape)
+    ptrs = [_ptr(k_pool, "k_pool", _kv_dtypes(shape), numel=n.pool),
+            _ptr(v_pool, "v_pool", _kv_dtypes(shape), numel=n.pool),
+            _ptr(block_table, "block_table", (torch.int32,), numel=n.block_table),
+            _ptr(seq_lens, "seq_lens", (torch.int32,), numel=n.batch),
+            _ptr(weights, "weights", (torch.float32,), numel=cells)]
+    outs = [_ptr(new_table, "new_table", (torch.int32,), numel=n.block_table),
+            _ptr(kept, "kept", (torch.int32,), numel=rows * max(int(keep), 0)),
+            _ptr(new_lens, "new_lens", (torch.int32,), numel=n.batch),
+            _ptr(new_weights, "new_weights", (torch.float32,), nullable=True, numel=cells)]
+    _one_device(k_pool=k_pool, v_pool=v_pool, block_table=block_table, seq_lens=seq_lens,
+                weights=weights, new_table=new_table, kept=kept, new_lens=new_lens,
+                new_weights=new_weights)
+    return lib.entmaxkv_evict, [ctypes.byref(shape), *ptrs, int(keep), int(sinks), int(recent),
+                                *outs, _stream(stream, k_pool.device), None]
+
+
 def _run(name, fn, args, events):
     if events is not None:
         ev = _events(events)
         args = list(args)
         args[-1] = ev[0]
     _check(fn(*args), name)
+
+
+def _run_on(device, name, fn, args, events):
+    """_run with `device` as the current one (the library launches there)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        _run(name, fn, args, events)
+    else:
+        with torch.cuda.device(device):
+            _run(name, fn, args, events)
 
 
 def entmaxkv_build_page_meta(shape: Shape, k_pool, block_table, seq_lens, meta, stream=None,
@@ -453,6 +615,47 @@ def entmaxkv_decode_full(shape: Shape, q, k_pool, v_pool, block_table, seq_lens,
     _run("entmaxkv_decode_full", fn, args, events)
 
 
+def entmaxkv_softmax_window(shape: Shape, q, k_pool, v_pool, block_table, seq_lens, window, sinks,
+                            out, lse=None, q_tokens=1, ws=None, stream=None, events=None):
+    """Softmax attention of every sequence's last q_tokens tokens over a
+    window and the first `sinks` tokens. q and out: [batch, q_tokens,
+    num_q_heads, head_dim], float32 or (with a bf16 cache) bfloat16; window:
+    FULL_WINDOW for all tokens."""
+    fn, args, _ = _args_softmax_window(shape, q, k_pool, v_pool, block_table, seq_lens, window,
+                                       sinks, out, lse, q_tokens, ws, stream)
+    _run_on(q.device, "entmaxkv_softmax_window", fn, args, events)
+
+
+def entmaxkv_softmax_prefix(shape: Shape, q, k_pool, v_pool, prefix_table, prefix_pages,
+                            block_table, seq_lens, out, lse=None, ws=None, stream=None,
+                            events=None):
+    """Softmax attention of one token per sequence over sequences that share
+    their first prefix_pages pages, listed in prefix_table."""
+    fn, args, _ = _args_softmax_prefix(shape, q, k_pool, v_pool, prefix_table, prefix_pages,
+                                       block_table, seq_lens, out, lse, ws, stream)
+    _run_on(q.device, "entmaxkv_softmax_prefix", fn, args, events)
+
+
+def entmaxkv_accumulate_weights(shape: Shape, q, k_pool, block_table, seq_lens, alpha, tau, decay,
+                                weights_in, weights_out, window=FULL_WINDOW, sinks=0, stream=None,
+                                events=None):
+    """weights_out = decay * weights_in (None: 0) + every cached token's
+    attention weight, summed over the query heads of its KV head. tau: the lse
+    of a softmax decode (alpha 1) or the tau of an alpha-entmax decode."""
+    fn, args = _args_accumulate_weights(shape, q, k_pool, block_table, seq_lens, alpha, tau,
+                                        decay, weights_in, weights_out, window, sinks, stream)
+    _run_on(q.device, "entmaxkv_accumulate_weights", fn, args, events)
+
+
+def entmaxkv_evict(shape: Shape, k_pool, v_pool, block_table, seq_lens, weights, keep, sinks,
+                   recent, new_table, kept, new_lens, new_weights=None, stream=None, events=None):
+    """Keeps `keep` tokens of every (sequence, KV head) by accumulated weight
+    and copies them to the pages of new_table."""
+    fn, args = _args_evict(shape, k_pool, v_pool, block_table, seq_lens, weights, keep, sinks,
+                           recent, new_table, kept, new_lens, new_weights, stream)
+    _run_on(k_pool.device, "entmaxkv_evict", fn, args, events)
+
+
 class Prepared:
     """An entry point with its arguments marshalled once, for tight loops.
     The tensors must stay alive and unchanged in place while it is used.
@@ -467,16 +670,24 @@ class Prepared:
                "decode_full": _args_decode_full,
                "build_page_moments": _args_build_page_moments,
                "append_page_moments": _args_append_page_moments,
-               "gauss_select": _args_gauss_select}
+               "gauss_select": _args_gauss_select,
+               "softmax_window": _args_softmax_window,
+               "softmax_prefix": _args_softmax_prefix,
+               "accumulate_weights": _args_accumulate_weights, "evict": _args_evict}
 
     def __init__(self, name: str, *args, **kwargs):
         r = Prepared._makers[name](*args, **kwargs)
         self.name = "entmaxkv_" + name
         self.fn, self.args = r[0], r[1]
         self.keep = (args, kwargs, r[2:] if len(r) > 2 else ())  # keep tensors alive
+        tensors = [t for t in args if isinstance(t, torch.Tensor)]
+        self.device = tensors[0].device.index  # the device that the kernels are launched on
         self._ev_cache = {}
 
     def __call__(self, events=None):
+        if self.device is not None and self.device != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                return self(events)
         if events is None:
             rc = self.fn(*self.args)
         else:
