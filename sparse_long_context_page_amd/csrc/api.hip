@@ -321,24 +321,34 @@ int check_plan(const AttendPlan& p) {
   return p.items > 0x7fffffffLL ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
 }
 
-int window_plan(const entmaxkv_shape* shape, int32_t q_tokens, int32_t* window, int32_t* sinks,
-                LaunchShape* s, AttendPlan* p) {
+// The plan of a call; q_dtype < 0: of whichever query type needs the larger
+// workspace.
+AttendPlan plan_either(const LaunchShape& s, int32_t q_dtype, int n, int window, int sinks,
+                       int prefix_pages) {
+  const AttendPlan f = plan_attend(s, false, n, window, sinks, prefix_pages);
+  if (q_dtype == ENTMAXKV_F32 || !s.bf16) return f;
+  const AttendPlan b = plan_attend(s, true, n, window, sinks, prefix_pages);
+  return q_dtype == ENTMAXKV_BF16 || b.ws_bytes > f.ws_bytes ? b : f;
+}
+
+int window_plan(const entmaxkv_shape* shape, int32_t q_dtype, int32_t q_tokens, int32_t* window,
+                int32_t* sinks, LaunchShape* s, AttendPlan* p) {
   int rc = check_shape(shape, s);
   if (rc) return rc;
   if (q_tokens <= 0) return ENTMAXKV_ERR_INVALID;
   if ((rc = check_window(window, sinks))) return rc;
   if ((long long)s->batch * s->num_q_heads * q_tokens > (1LL << 24))
     return ENTMAXKV_ERR_UNSUPPORTED;
-  *p = plan_attend(*s, q_tokens, *window, *sinks, 0);
+  *p = plan_either(*s, q_dtype, q_tokens, *window, *sinks, 0);
   return check_plan(*p);
 }
 
-int prefix_plan(const entmaxkv_shape* shape, int32_t prefix_pages, LaunchShape* s,
-                AttendPlan* p) {
+int prefix_plan(const entmaxkv_shape* shape, int32_t q_dtype, int32_t prefix_pages,
+                LaunchShape* s, AttendPlan* p) {
   int rc = check_shape(shape, s);
   if (rc) return rc;
   if (prefix_pages <= 0 || prefix_pages > s->max_pages) return ENTMAXKV_ERR_INVALID;
-  *p = plan_attend(*s, 1, kMaxWindow, 0, prefix_pages);
+  *p = plan_either(*s, q_dtype, 1, kMaxWindow, 0, prefix_pages);
   return check_plan(*p);
 }
 
@@ -669,7 +679,7 @@ int entmaxkv_softmax_window_ws(const entmaxkv_shape* shape, int32_t q_tokens, in
                                int32_t sinks, size_t* bytes) {
   LaunchShape s;
   AttendPlan p;
-  if (int rc = window_plan(shape, q_tokens, &window, &sinks, &s, &p)) return rc;
+  if (int rc = window_plan(shape, -1, q_tokens, &window, &sinks, &s, &p)) return rc;
   if (!bytes) return ENTMAXKV_ERR_INVALID;
   *bytes = p.ws_bytes;
   return ENTMAXKV_OK;
@@ -682,7 +692,7 @@ int entmaxkv_softmax_window(const entmaxkv_shape* shape, const void* q, int32_t 
                             hipStream_t stream, hipEvent_t* events) {
   LaunchShape s;
   AttendPlan p;
-  if (int rc = window_plan(shape, q_tokens, &window, &sinks, &s, &p)) return rc;
+  if (int rc = window_plan(shape, q_dtype, q_tokens, &window, &sinks, &s, &p)) return rc;
   return attend_common(s, p, q, q_dtype, q_tokens, k_pool, v_pool, nullptr, 0, block_table,
                        seq_lens, window, sinks, out, lse, ws, ws_bytes, stream, events);
 }
@@ -690,7 +700,7 @@ int entmaxkv_softmax_window(const entmaxkv_shape* shape, const void* q, int32_t 
 int entmaxkv_softmax_prefix_ws(const entmaxkv_shape* shape, int32_t prefix_pages, size_t* bytes) {
   LaunchShape s;
   AttendPlan p;
-  if (int rc = prefix_plan(shape, prefix_pages, &s, &p)) return rc;
+  if (int rc = prefix_plan(shape, -1, prefix_pages, &s, &p)) return rc;
   if (!bytes) return ENTMAXKV_ERR_INVALID;
   *bytes = p.ws_bytes;
   return ENTMAXKV_OK;
@@ -703,7 +713,7 @@ int entmaxkv_softmax_prefix(const entmaxkv_shape* shape, const void* q, int32_t 
                             size_t ws_bytes, hipStream_t stream, hipEvent_t* events) {
   LaunchShape s;
   AttendPlan p;
-  if (int rc = prefix_plan(shape, prefix_pages, &s, &p)) return rc;
+  if (int rc = prefix_plan(shape, q_dtype, prefix_pages, &s, &p)) return rc;
   if (!prefix_table) return ENTMAXKV_ERR_INVALID;
   return attend_common(s, p, q, q_dtype, 1, k_pool, v_pool, prefix_table, prefix_pages,
                        block_table, seq_lens, kMaxWindow, 0, out, lse, ws, ws_bytes, stream,

@@ -278,18 +278,22 @@ hipError_t launch_tau_pv_f32(const LaunchShape& s, const SplitPlan& p, const voi
                              int budget, float alpha, float window, float* out, float* tau,
                              int32_t* support, void* ws, const DecodeWs& L, hipStream_t st);
 
-// Softmax attention (softmax.hip). A row block is 16 query rows of one KV
-// head; its tokens are split over `splits` workgroups (`pre_splits` over the
-// shared prefix), whose parts are joined by a second kernel when there is
-// more than one per row.
+// Softmax attention (softmax.hip). The query rows of one KV head, of one
+// sequence or of a whole batch over its shared prefix, go in blocks (16 rows,
+// or one block of the many-rows form); a block's tokens are split over
+// `splits` workgroups (`pre_splits` over the prefix), whose parts are joined
+// by a second kernel when there is more than one per row.
 constexpr int kAttWgsPerCU = 2;     // workgroups a CU holds at the kernel's register use
 constexpr int kAttMaxSplits = 256;  // parts of a row block
+constexpr int kAttManyRows = 33;    // rows of a KV head from which the many-rows form runs
 struct AttendPlan {
   long long rows = 0, items = 0, pre_items = 0;
-  int pre_tiles = 0, pre_splits = 0, row_tiles = 0, splits = 0, slots = 0;
+  int pre_block = 0, pre_splits = 0, row_block = 0, row_blocks = 0, splits = 0, slots = 0;
+  bool pre_rows = false, own_rows = false;  // the many-rows form, per part
   size_t ml_off = 0, ws_bytes = 0;
 };
-AttendPlan plan_attend(const LaunchShape& s, int n, int window, int sinks, int prefix_pages);
+AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int sinks,
+                       int prefix_pages);
 hipError_t launch_attend(const LaunchShape& s, const AttendPlan& p, const void* q, bool q_bf16,
                          int n, const void* k_pool, const void* v_pool,
                          const int32_t* prefix_table, int prefix_pages,

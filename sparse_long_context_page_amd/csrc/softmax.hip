@@ -5,15 +5,25 @@
 //   out = sum exp(z_t - m) v_t / l,  lse = m + ln l
 //
 // over the tokens a query sees. One pass over K and V: a wave holds 16 query
-// rows (the heads of one KV group, times query tokens or sequences), the
-// reference m, the sum l and the output in registers, and walks its tiles
+// rows a tile (the heads of one KV group, times query tokens or sequences),
+// their reference m, sum l and output in registers, and walks tiles of tokens
 // (softmax_impl.hpp). Any reference m gives the same quotient, so m follows
 // the running maximum only when that has grown by more than kSlack: the sum
 // stays below e^kSlack * tokens, far inside float32, and almost no tile pays
 // for a rescale or a reduction across lanes.
 //
-// Work is split over the tokens of a row block; the parts (m_s, l_s, o_s) are
-// joined by a second kernel: out = sum e^(m_s - M) o_s / sum e^(m_s - M) l_s.
+// Two forms of a workgroup:
+//  - few rows (attend_tokens): the waves share at most 16 rows and take turns
+//    at the tiles, loaded from memory straight into the operands' registers;
+//    bound by reading K and V.
+//  - many rows (attend_rows): each wave has row tiles of its own and all walk
+//    the same tokens, staged once per workgroup in LDS by direct loads, one
+//    stage ahead; bound by the matrix cores and the exponentials.
+// The tokens of a row block are split over workgroups; the parts (m_s, l_s,
+// o_s) are joined by a second kernel: out = sum e^(m_s - M) o_s / sum e^(m_s -
+// M) l_s.
+#include <atomic>
+
 #include "softmax_impl.hpp"
 
 namespace ekv {
@@ -36,13 +46,16 @@ struct AttendArgs {
   float* part_ml; // [rows, slots, 2]
   int batch, H, Hkv, G, n, ps, max_pages, num_phys;
   int window, sinks;
-  int prefix;            // tokens of the shared prefix (0: none)
-  int pre_tiles, pre_splits, pre_items;  // row tiles and splits of the prefix part
-  int row_tiles, splits;                 // of the other part
-  int slots;                             // parts per row
+  int prefix;                                  // tokens of the shared prefix (0: none)
+  int pre_block, pre_splits, pre_items;        // rows per block and splits of the prefix part
+  int row_block, row_blocks, splits;           // of the sequences' own part
+  int slots;                                   // parts per row
+  bool pre_rows, own_rows;                     // parts of the many-rows form
 };
 
-// What one workgroup works on.
+// What one workgroup works on. Items go over the KV heads first: the blocks
+// that read the same head's tokens are a multiple of num_kv_heads apart, so
+// that with 8 heads they share an XCD and its L2.
 struct Block {
   int b, g;       // sequence (prefix part: none) and KV head
   int r0, nrows;  // first row of the block among its rows, rows of it
@@ -52,127 +65,228 @@ struct Block {
 
 __device__ __forceinline__ Block block_of(const AttendArgs& a, int item) {
   Block w;
-  if (item < a.pre_items) {
-    w.pre = true;
+  w.pre = item < a.pre_items;
+  if (!w.pre) item -= a.pre_items;
+  w.g = item % a.Hkv;
+  int x = item / a.Hkv;
+  if (w.pre) {
     w.b = 0;
-    w.split = item % a.pre_splits;
-    const int x = item / a.pre_splits;
-    w.g = x % a.Hkv;
-    w.r0 = x / a.Hkv * 16;
-    w.nrows = min(16, a.batch * a.G - w.r0);
+    w.split = x % a.pre_splits;
+    w.r0 = x / a.pre_splits * a.pre_block;
+    w.nrows = min(a.pre_block, a.batch * a.G - w.r0);
     w.splits = a.pre_splits;
     w.slot = w.split;
   } else {
-    item -= a.pre_items;
-    w.pre = false;
-    w.split = item % a.splits;
-    int x = item / a.splits;
-    w.g = x % a.Hkv;
-    x /= a.Hkv;
-    w.r0 = x % a.row_tiles * 16;
-    w.b = x / a.row_tiles;
-    w.nrows = min(16, a.n * a.G - w.r0);
+    w.split = x % a.splits;
+    x /= a.splits;
+    w.r0 = x % a.row_blocks * a.row_block;
+    w.b = x / a.row_blocks;
+    w.nrows = min(a.row_block, a.n * a.G - w.r0);
     w.splits = a.splits;
     w.slot = a.pre_items ? a.pre_splits + w.split : w.split;
   }
   return w;
 }
 
-// Index of row r of the block among all [batch, n, H] rows, and the tokens it
-// sees.
+// Index of row r of the block's part among all [batch, n, H] rows, and the
+// tokens it sees.
 __device__ __forceinline__ void row_of(const AttendArgs& a, const Block& w, int L, int r,
-                                       size_t* row, int* lo, int* hi) {
+                                       int* row, int* lo, int* hi) {
   if (w.pre) {
     const int b = r / a.G;
-    *row = (size_t)b * a.H + w.g * a.G + (r - b * a.G);
+    *row = b * a.H + w.g * a.G + (r - b * a.G);
     *lo = 0;
     *hi = min(clamp_len(a.seq_lens[b], a.max_pages * a.ps), a.prefix);
   } else {
     const int i = r / a.G;
-    *row = ((size_t)w.b * a.n + i) * a.H + w.g * a.G + (r - i * a.G);
+    *row = (w.b * a.n + i) * a.H + w.g * a.G + (r - i * a.G);
     const int pos = L - a.n + i;
     *hi = max(pos + 1, 0);
     *lo = max(max(pos - a.window + 1, a.prefix), 0);
   }
 }
 
+// Tokens [lo, hi) that some of the rows r0 .. r0 + nrows - 1 sees and [flo,
+// fhi) that all of them see (besides the sinks).
+struct Span {
+  int lo, hi, flo, fhi;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int L, int r0, int nrows) {
+  const int p0 = L - a.n + r0 / a.G, p1 = L - a.n + (r0 + nrows - 1) / a.G;
+  Span s;
+  s.lo = max(max(p0 - a.window + 1, a.prefix), 0);
+  s.hi = max(p1 + 1, 0);
+  s.flo = max(max(p1 - a.window + 1, a.prefix), 0);
+  s.fhi = max(p0 + 1, 0);
+  return s;
+}
+// The same of prefix rows, from the lanes' own hi (rows that are none: 0).
+__device__ __forceinline__ Span span_of_prefix(int hi, bool live) {
+  int u = hi, f = live ? hi : INT32_MAX;
+#pragma unroll
+  for (int s = 1; s < 16; s <<= 1) {
+    u = max(u, __shfl_xor(u, s, kWave));
+    f = min(f, __shfl_xor(f, s, kWave));
+  }
+  return Span{0, __builtin_amdgcn_readfirstlane(u), 0, __builtin_amdgcn_readfirstlane(f)};
+}
+
+struct Views {
+  KvView k, v;
+  const int32_t* table;
+};
+template <bool BF, int D>
+__device__ __forceinline__ Views views_of(const AttendArgs& a, const Block& w) {
+  constexpr int kElem = BF ? 2 : 4;
+  Views x;
+  const size_t head_off = (size_t)w.g * a.ps * D * kElem;
+  x.k.base = static_cast<const char*>(a.k_pool) + head_off;
+  x.v.base = static_cast<const char*>(a.v_pool) + head_off;
+  x.k.page_bytes = x.v.page_bytes = (size_t)a.Hkv * a.ps * D * kElem;
+  x.k.page_size = x.v.page_size = a.ps;
+  x.table = w.pre ? a.prefix_table : a.block_table + (size_t)w.b * a.max_pages;
+  return x;
+}
+
+// Table entry j, -1 past npages and where it is no physical page.
+__device__ __forceinline__ int page_at(const AttendArgs& a, const int32_t* table, int npages,
+                                       int j) {
+  const int p = j < npages ? table[j] : -1;
+  return p < a.num_phys ? p : -1;
+}
+
+// m before any token: below every score, and finite, also times log2(e)
+// where weight() forms that product alone.
+template <int PARTS>
+constexpr float kLowest = PARTS == 1 ? -FLT_MAX / 2 : -FLT_MAX;
+
+// exp(z - m). float32 queries: the difference first (no rounding near the
+// maximum); bf16 ones: one multiply-add, |z| 2^-24 off.
+template <int PARTS>
+__device__ __forceinline__ float weight(float z, float m) {
+  if constexpr (PARTS == 1) return __builtin_amdgcn_exp2f(fmaf(z, kLog2e, -m * kLog2e));
+  return __builtin_amdgcn_exp2f((z - m) * kLog2e);
+}
+
+// The reference m follows the maximum of a tile's scores.
+template <int N>
+__device__ __forceinline__ void raise(float tmax, float& m, float& l, f32x4 (&acc)[N]) {
+  const float mn = fmaxf(m, group_max(tmax));
+  const float f = exp2f((m - mn) * kLog2e);
+  l *= f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) acc[n] *= f;
+  m = mn;
+}
+
+// A tile in which the rows see different tokens and some value is not finite,
+// which must not meet the zero weight of a row that does not see it: one row
+// at a time, on the values that it sees. (The weights are in l already.)
+template <bool BF, int D, int PARTS, int PP, int N>
+__device__ __forceinline__ void late_tile(const Views& x, TilePages pg, int t0, int lane,
+                                          const QFrag<BF, D, PARTS>& q, int lo, int hi, int sinks,
+                                          float m, f32x4 (&acc)[N]) {
+  constexpr int NZ = scores_per_lane<BF>();
+  const int c = lane >> 4, rl = lane & 15;
+  const bool page_ok = (!BF || c < 2 ? pg.p0 : pg.p1) >= 0;
+  KTile<BF, D> kt;
+  float p[NZ];
+  kt.template load<true>(x.k, pg, t0, lane);
+  kt.template scores<PARTS>(q, p);
+#pragma unroll
+  for (int i = 0; i < NZ; ++i) {
+    const int t = t0 + tile_token<BF>(c, i);
+    const bool see = page_ok && t < hi && (t >= lo || t < sinks);
+    p[i] = see ? weight<PARTS>(p[i], m) : 0.0f;
+  }
+  PFrag<BF, PP> pf;
+  pf.set(p);
+  VTile<BF, D> vt;
+#pragma unroll 1
+  for (int r = 0; r < 16; ++r) {
+    const int rlo = __shfl(lo, r, kWave), rhi = __shfl(hi, r, kWave);
+    vt.template load<true>(x.v, pg, t0, lane);
+#pragma unroll
+    for (int i = 0; i < NZ; ++i) {
+      const int t = t0 + tile_token<BF>(c, i);
+      if (!(page_ok && t < rhi && (t >= rlo || t < sinks))) vt.clear(i);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const f32x4 o = vt.template mul<PP>(n, pf, f32x4{0, 0, 0, 0});
+      if (rl == r) acc[n] += o;
+    }
+  }
+}
+
+// Four finished coordinates of a row.
+template <int PARTS>
+__device__ __forceinline__ void store_out(void* out, size_t at, f32x4 o) {
+  if constexpr (PARTS == 1) {
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = bf16_round(o[e]);
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) =
+        u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = o;
+  }
+}
+__device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.0f ? -INFINITY : m + kLn2 * log2f(l);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+
+template <bool BF, int D>
+struct TokensLds {
+  float o[kAttWaves][16][D + 4];
+  float ml[kAttWaves][16][2];
+};
+
 template <bool BF, int D, int PARTS>
-__global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
+__device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& w, char* smem) {
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
+  // bf16 queries: weights to 16 bits (the instructions are free here)
   constexpr int PP = PARTS == 3 ? 3 : 2;
-  constexpr int PITCH = D + 4;
   constexpr int QB = PARTS == 1 ? 2 : 4;
   constexpr int kAcc = VTile<BF, D>::kAcc;
-  __shared__ float so[kAttWaves][16][PITCH];
-  __shared__ float sml[kAttWaves][16][2];
+  TokensLds<BF, D>& sh = *reinterpret_cast<TokensLds<BF, D>*>(smem);
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane >> 4, rl = lane & 15;
-  const Block w = block_of(a, blockIdx.x);
 
   const int L = w.pre ? a.prefix : clamp_len(a.seq_lens[w.b], a.max_pages * a.ps);
-  int lo = 0, hi = 0;
-  size_t row = 0;
+  int lo = 0, hi = 0, row = 0;
   if (rl < w.nrows) row_of(a, w, L, w.r0 + rl, &row, &lo, &hi);
-  const int sinks = w.pre ? 0 : a.sinks;
-
-  // tokens that some row sees, and that every row sees
-  int ulo, uhi, flo, fhi;
-  if (w.pre) {
-    ulo = 0;
-    uhi = hi;
-    fhi = rl < w.nrows ? hi : INT32_MAX;
-#pragma unroll
-    for (int s = 1; s < 16; s <<= 1) {
-      uhi = max(uhi, __shfl_xor(uhi, s, kWave));
-      fhi = min(fhi, __shfl_xor(fhi, s, kWave));
-    }
-    uhi = __builtin_amdgcn_readfirstlane(uhi);
-    fhi = __builtin_amdgcn_readfirstlane(fhi);
-    flo = 0;
-  } else {
-    const int p0 = L - a.n + w.r0 / a.G, p1 = L - a.n + (w.r0 + w.nrows - 1) / a.G;
-    ulo = max(max(p0 - a.window + 1, a.prefix), 0);
-    uhi = max(p1 + 1, 0);
-    flo = max(max(p1 - a.window + 1, a.prefix), 0);
-    fhi = max(p0 + 1, 0);
-  }
-  const TileSpan span = tile_span<TT>(ulo, uhi, sinks);
+  const int sinks = a.sinks;
+  const Span u = w.pre ? span_of_prefix(hi, rl < w.nrows) : span_of(a, L, w.r0, w.nrows);
+  const TileSpan span = tile_span<TT>(u.lo, u.hi, sinks);
   const int per = (span.n + w.splits - 1) / w.splits;
   const int v0 = min(w.split * per, span.n), v1 = min(v0 + per, span.n);
-
-  const int32_t* table =
-      w.pre ? a.prefix_table : a.block_table + (size_t)w.b * a.max_pages;
-  const int npages = (uhi + a.ps - 1) / a.ps;
-  KvView kv, vv;
-  const size_t head_off = (size_t)w.g * a.ps * D * (BF ? 2 : 4);
-  kv.base = static_cast<const char*>(a.k_pool) + head_off;
-  vv.base = static_cast<const char*>(a.v_pool) + head_off;
-  kv.page_bytes = vv.page_bytes = (size_t)a.Hkv * a.ps * D * (BF ? 2 : 4);
-  kv.page_size = vv.page_size = a.ps;
+  const int npages = (u.hi + a.ps - 1) / a.ps;
+  const Views x = views_of<BF, D>(a, w);
 
   QFrag<BF, D, PARTS> q;
-  q.load(rl < w.nrows ? static_cast<const char*>(a.q) + row * (D * QB) : nullptr, c);
+  q.load(rl < w.nrows ? static_cast<const char*>(a.q) + (size_t)row * (D * QB) : nullptr, c);
 
   f32x4 acc[kAcc];
 #pragma unroll
   for (int n = 0; n < kAcc; ++n) acc[n] = f32x4{0, 0, 0, 0};
-  float m = -FLT_MAX, l = 0.0f;
+  float m = kLowest<PARTS>, l = 0.0f;
 
   for (int base = v0 + wave; base < v1; base += kAttWaves * kWave) {
     // pages of this wave's next 64 tiles, one tile per lane
     const int nt = min(kWave, (v1 - base + kAttWaves - 1) / kAttWaves);
     int pg0 = -1, pg1 = -1;
     if (lane < nt) {
-      const int t0 = span.tile(base + lane * kAttWaves) * TT;
-      const int j = t0 / a.ps;
-      pg0 = j < npages ? table[j] : -1;
-      pg1 = pg0;
-      if (BF && a.ps == 16) pg1 = j + 1 < npages ? table[j + 1] : -1;
-      if (pg0 >= a.num_phys) pg0 = -1;
-      if (pg1 >= a.num_phys) pg1 = -1;
+      const int j = span.tile(base + lane * kAttWaves) * TT / a.ps;
+      pg0 = pg1 = page_at(a, x.table, npages, j);
+      if (BF && a.ps == 16) pg1 = page_at(a, x.table, npages, j + 1);
     }
     KTile<BF, D> kt;
     VTile<BF, D> vt;
@@ -182,8 +296,8 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
     auto start = [&](int j) { return span.tile(base + j * kAttWaves) * TT; };
     TilePages pc = pages(0);
     int t0 = start(0);
-    kt.template load<true>(kv, pc, t0, lane);
-    vt.template load<true>(vv, pc, t0, lane);
+    kt.template load<true>(x.k, pc, t0, lane);
+    vt.template load<true>(x.v, pc, t0, lane);
     uint64_t put_off = 0;
     for (int j = 0; j < nt; ++j) {
       float z[NZ];
@@ -193,10 +307,10 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
       if (j + 1 < nt) {
         pn = pages(j + 1);
         tn = start(j + 1);
-        kt.template load<true>(kv, pn, tn, lane);
+        kt.template load<true>(x.k, pn, tn, lane);
       }
       const bool full = pc.p0 >= 0 && pc.p1 >= 0 &&
-                        (t0 + TT <= fhi && (t0 >= flo || t0 + TT <= sinks));
+                        (t0 + TT <= u.fhi && (t0 >= u.flo || t0 + TT <= sinks));
       const bool page_ok = (!BF || c < 2 ? pc.p0 : pc.p1) >= 0;
       if (!full) {
 #pragma unroll
@@ -208,67 +322,39 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
       float tmax = z[0];
 #pragma unroll
       for (int i = 1; i < NZ; ++i) tmax = fmaxf(tmax, z[i]);
-      if (__any(tmax > m + kSlack)) {
-        const float mn = fmaxf(m, group_max(tmax));
-        const float f = exp2f((m - mn) * kLog2e);
-        l *= f;
-#pragma unroll
-        for (int n = 0; n < kAcc; ++n) acc[n] *= f;
-        m = mn;
-      }
+      if (__any(tmax > m + kSlack)) raise(tmax, m, l, acc);
       float p[NZ];
 #pragma unroll
       for (int i = 0; i < NZ; ++i) {
-        p[i] = __builtin_amdgcn_exp2f((z[i] - m) * kLog2e);
+        p[i] = weight<PARTS>(z[i], m);
         l += p[i];
       }
       bool later = false;
       if (!full) {
-        // tokens no row sees take no part, whatever their rows hold; where
-        // the rows differ in what they see, a value that is not finite must
-        // not meet the zero weight of a row that does not see it: such a
-        // tile's values wait
+        // tokens that no row sees take no part, whatever their rows hold
 #pragma unroll
         for (int i = 0; i < NZ; ++i) {
           const int t = t0 + tile_token<BF>(c, i);
-          if (!(page_ok && t < uhi && (t >= ulo || t < sinks))) vt.clear(i);
+          if (!(page_ok && t < u.hi && (t >= u.lo || t < sinks))) vt.clear(i);
         }
         later = __any(vt.any_nonfinite());
       }
-      if (later) put_off |= 1ull << j;
-      else vt.template pv<PP>(p, acc);
-      if (j + 1 < nt) vt.template load<true>(vv, pn, tn, lane);
+      if (later) {
+        put_off |= 1ull << j;
+      } else {
+        PFrag<BF, PP> pf;
+        pf.set(p);
+#pragma unroll
+        for (int n = 0; n < kAcc; ++n) acc[n] = vt.template mul<PP>(n, pf, acc[n]);
+      }
+      if (j + 1 < nt) vt.template load<true>(x.v, pn, tn, lane);
       pc = pn;
       t0 = tn;
     }
-    // the tiles put off: one row at a time, on the values that it sees (their
-    // weights are in l already)
     while (put_off) {
       const int j = __builtin_ctzll(put_off);
       put_off &= put_off - 1;
-      pc = pages(j);
-      t0 = start(j);
-      const bool page_ok = (!BF || c < 2 ? pc.p0 : pc.p1) >= 0;
-      float p[NZ];
-      kt.template load<true>(kv, pc, t0, lane);
-      kt.template scores<PARTS>(q, p);
-#pragma unroll
-      for (int i = 0; i < NZ; ++i) {
-        const int t = t0 + tile_token<BF>(c, i);
-        const bool see = page_ok && t < hi && (t >= lo || t < sinks);
-        p[i] = see ? __builtin_amdgcn_exp2f((p[i] - m) * kLog2e) : 0.0f;
-      }
-#pragma unroll 1
-      for (int r = 0; r < 16; ++r) {
-        const int rlo = __shfl(lo, r, kWave), rhi = __shfl(hi, r, kWave);
-        vt.template load<true>(vv, pc, t0, lane);
-#pragma unroll
-        for (int i = 0; i < NZ; ++i) {
-          const int t = t0 + tile_token<BF>(c, i);
-          if (!(page_ok && t < rhi && (t >= rlo || t < sinks))) vt.clear(i);
-        }
-        vt.template pv<PP, true>(p, acc, rl == r);
-      }
+      late_tile<BF, D, PARTS, PP>(x, pages(j), start(j), lane, q, lo, hi, sinks, m, acc);
     }
   }
 
@@ -276,13 +362,13 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
   l = group_sum(l);
   if (rl < w.nrows) {
     if (c == 0) {
-      sml[wave][rl][0] = m;
-      sml[wave][rl][1] = l;
+      sh.ml[wave][rl][0] = m;
+      sh.ml[wave][rl][1] = l;
     }
 #pragma unroll
     for (int n = 0; n < kAcc; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) so[wave][rl][VTile<BF, D>::coord(c, n, i)] = acc[n][i];
+      for (int i = 0; i < 4; ++i) sh.o[wave][rl][VTile<BF, D>::coord(c, n, i)] = acc[n][i];
   }
   __syncthreads();
   constexpr int TPR = D / 4;  // threads per row, 4 coordinates each
@@ -291,119 +377,435 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
     float M = -FLT_MAX;
 #pragma unroll
     for (int v = 0; v < kAttWaves; ++v)
-      if (!(sml[v][r][1] == 0.0f)) M = fmaxf(M, sml[v][r][0]);
+      if (!(sh.ml[v][r][1] == 0.0f)) M = fmaxf(M, sh.ml[v][r][0]);
     float ls = 0.0f;
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
     for (int v = 0; v < kAttWaves; ++v) {
-      const float lv = sml[v][r][1];
+      const float lv = sh.ml[v][r][1];
       if (lv == 0.0f) continue;
-      const float f = exp2f((sml[v][r][0] - M) * kLog2e);
+      const float f = exp2f((sh.ml[v][r][0] - M) * kLog2e);
       ls += f * lv;
-      o += f * *reinterpret_cast<const f32x4*>(&so[v][r][d]);
+      o += f * *reinterpret_cast<const f32x4*>(&sh.o[v][r][d]);
     }
-    size_t grow;
-    int dlo, dhi;
+    int grow, dlo, dhi;
     row_of(a, w, L, w.r0 + r, &grow, &dlo, &dhi);
     if (a.slots > 1) {
-      const size_t part = grow * a.slots + w.slot;
+      const size_t part = (size_t)grow * a.slots + w.slot;
       *reinterpret_cast<f32x4*>(a.part_o + part * D + d) = o;
       if (d == 0) {
         a.part_ml[2 * part] = M;
         a.part_ml[2 * part + 1] = ls;
       }
     } else {
-      const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-      if constexpr (PARTS == 1) {
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = bf16_round(o[e] * inv);
-        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + grow * D + d) =
-            u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-      } else {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + grow * D + d) = o * inv;
-      }
-      if (d == 0 && a.lse) a.lse[grow] = ls == 0.0f ? -INFINITY : M + kLn2 * log2f(ls);
+      store_out<PARTS>(a.out, (size_t)grow * D + d, o * inverse(ls));
+      if (d == 0 && a.lse) a.lse[grow] = log_sum(M, ls);
     }
   }
 }
 
-// Joins the parts of each row: D/4 threads a row, 4 coordinates each.
-template <int D, int PARTS>
-__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part_o,
-                                                   const float* __restrict__ part_ml, int slots,
-                                                   int rows, void* __restrict__ out,
-                                                   float* __restrict__ lse) {
-  constexpr int TPR = D / 4;
-  const int r = blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-  if (r >= rows) return;
-  const int d = (threadIdx.x % TPR) * 4;
-  const float* ml = part_ml + (size_t)r * slots * 2;
-  const float* po = part_o + (size_t)r * slots * D + d;
-  float M = -FLT_MAX;
-  for (int s = 0; s < slots; ++s)
-    if (!(ml[2 * s + 1] == 0.0f)) M = fmaxf(M, ml[2 * s]);
-  float l = 0.0f;
-  f32x4 o = {0, 0, 0, 0};
-  for (int s = 0; s < slots; ++s) {
-    const float ls = ml[2 * s + 1];
-    if (ls == 0.0f) continue;
-    const float f = exp2f((ml[2 * s] - M) * kLog2e);
-    l += f * ls;
-    o += f * *reinterpret_cast<const f32x4*>(po + (size_t)s * D);
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if constexpr (PARTS == 1) {
-    uint32_t h[4];
+// ---------------------------------------------------------------------------
+// Many rows
+
+// Row tiles a wave holds: two with bf16 queries (32 rows share each K and V
+// operand); one with float32 ones, whose three parts fill the registers.
+template <bool BF, int PARTS>
+constexpr int kRowTiles = BF && PARTS == 1 ? 2 : 1;
+
+template <bool BF, int D>
+struct RowsLds {
+  char st[2][2][Stage<BF, D>::kBytes];  // [buffer][K, V]
+  int ok[2][kAttWaves];                 // is that quarter of the stage in a physical page?
+};
+
+template <bool BF, int D, int PARTS>
+__device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w, char* smem) {
+  constexpr int TT = kTile<BF>;
+  constexpr int NZ = scores_per_lane<BF>();
+  // bf16 queries: weights rounded to bf16, half a step of at most 2^-8 of
+  // each, as the output's own rounding; the sum l is of the unrounded ones
+  constexpr int PP = PARTS;
+  constexpr int QB = PARTS == 1 ? 2 : 4;
+  constexpr int RT = kRowTiles<BF, PARTS>;
+  constexpr int kAcc = VTile<BF, D>::kAcc;
+  typedef Stage<BF, D> St;
+  constexpr int ST = St::kTokens;
+  constexpr int kChunk = 32;                          // stages between two looks at the table
+  constexpr int kLoads = St::kBytes / kAttWaves / 1024;  // of K a wave and stage, and of V
+  RowsLds<BF, D>& sh = *reinterpret_cast<RowsLds<BF, D>*>(smem);
+
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane >> 4, rl = lane & 15;
+
+  const int L = w.pre ? a.prefix : clamp_len(a.seq_lens[w.b], a.max_pages * a.ps);
+  const int sinks = a.sinks;
+  const int wr = wave * (16 * RT);                      // first row of this wave in the block
+  const int wrows = max(min(16 * RT, w.nrows - wr), 0);  // its rows
+  int lo[RT], hi[RT], row[RT];
+  QFrag<BF, D, PARTS> q[RT];
+  Span u = {INT32_MAX, 0, 0, INT32_MAX};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = bf16_round(o[e] * inv);
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + (size_t)r * D + d) =
-        u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-  } else {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + (size_t)r * D + d) = o * inv;
+  for (int t = 0; t < RT; ++t) {
+    lo[t] = hi[t] = row[t] = 0;
+    const int r = t * 16 + rl;
+    if (r < wrows) row_of(a, w, L, w.r0 + wr + r, &row[t], &lo[t], &hi[t]);
+    q[t].load(r < wrows ? static_cast<const char*>(a.q) + (size_t)row[t] * (D * QB) : nullptr, c);
+    if (w.pre) {
+      const Span s = span_of_prefix(hi[t], r < wrows);
+      u = Span{0, max(u.hi, s.hi), 0, min(u.fhi, s.fhi)};
+    }
   }
-  if (d == 0 && lse) lse[r] = l == 0.0f ? -INFINITY : M + kLn2 * log2f(l);
+  if (!w.pre && wrows > 0) u = span_of(a, L, w.r0 + wr, wrows);
+  // the workgroup's stages: those that any of its rows sees
+  Span all = {0, a.prefix, 0, 0};
+  if (!w.pre) all = span_of(a, L, w.r0, w.nrows);
+  const TileSpan span = tile_span<ST>(all.lo, all.hi, sinks);
+  const int per = (span.n + w.splits - 1) / w.splits;
+  const int v0 = min(w.split * per, span.n), v1 = min(v0 + per, span.n);
+  const int npages = (all.hi + a.ps - 1) / a.ps;
+  const Views x = views_of<BF, D>(a, w);
+
+  // where this lane's 16 bytes of each direct load come from, past the row
+  // that the wave's quarter of the stage starts with
+  int from[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = i * 1024 + lane * 16;
+    const int r = at / St::kRow, slot = at % St::kRow / 16;
+    from[i] = r * St::kRow + ((slot ^ St::swizzle(wave * (ST / kAttWaves) + r)) << 4);
+  }
+
+  f32x4 acc[RT][kAcc];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+#pragma unroll
+    for (int n = 0; n < kAcc; ++n) acc[t][n] = f32x4{0, 0, 0, 0};
+    m[t] = kLowest<PARTS>;
+    l[t] = 0.0f;
+  }
+
+  for (int base = v0; base < v1; base += kChunk) {
+    const int ns = min(kChunk, v1 - base);
+    // page of this wave's quarter of each stage, one stage per lane
+    int pg = -1;
+    if (lane < ns)
+      pg = page_at(a, x.table, npages,
+                   (span.tile(base + lane) * ST + wave * (ST / kAttWaves)) / a.ps);
+    auto stage = [&](int j) {
+      const int p = __builtin_amdgcn_readlane(pg, j);
+      const int t = span.tile(base + j) * ST + wave * (ST / kAttWaves);
+      const size_t off =
+          (size_t)max(p, 0) * x.k.page_bytes + (size_t)(t & (a.ps - 1)) * St::kRow;
+      char* dst = sh.st[j & 1][0] + wave * (St::kBytes / kAttWaves);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        __builtin_amdgcn_global_load_lds(x.k.base + off + from[i], dst + i * 1024, 16, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        __builtin_amdgcn_global_load_lds(x.v.base + off + from[i], dst + St::kBytes + i * 1024, 16,
+                                         0, 0);
+      if (lane == 0) sh.ok[j & 1][wave] = p >= 0;
+    };
+    stage(0);
+    wait_vmcnt<0>();
+    __syncthreads();
+    uint64_t put_off = 0;  // two tiles a stage
+    for (int j = 0; j < ns; ++j) {
+      if (j + 1 < ns) stage(j + 1);
+      const int ts = span.tile(base + j) * ST;
+      const char* kst = sh.st[j & 1][0];
+      const char* vst = sh.st[j & 1][1];
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const int t0 = ts + sub * TT;
+        // a tile none of this wave's rows sees
+        if (t0 >= u.hi || (t0 + TT <= u.lo && t0 >= sinks)) continue;
+        const bool ok0 = sh.ok[j & 1][2 * sub] != 0, ok1 = sh.ok[j & 1][2 * sub + 1] != 0;
+        const bool full = __builtin_amdgcn_readfirstlane(ok0 && ok1) &&
+                          t0 + TT <= u.fhi && (t0 >= u.flo || t0 + TT <= sinks);
+        const bool page_ok = c < 2 ? ok0 : ok1;
+        KTile<BF, D> kt;
+        kt.read(kst, sub, lane);
+        float p[RT][NZ];
+        float tmax[RT];
+        bool rise = false;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          kt.template scores<PARTS>(q[t], p[t]);
+          if (!full) {
+#pragma unroll
+            for (int i = 0; i < NZ; ++i) {
+              const int tt = t0 + tile_token<BF>(c, i);
+              if (!(page_ok && tt < hi[t] && (tt >= lo[t] || tt < sinks))) p[t][i] = -INFINITY;
+            }
+          }
+          tmax[t] = p[t][0];
+#pragma unroll
+          for (int i = 1; i < NZ; ++i) tmax[t] = fmaxf(tmax[t], p[t][i]);
+          rise |= tmax[t] > m[t] + kSlack;
+        }
+        if (__any(rise)) {
+#pragma unroll
+          for (int t = 0; t < RT; ++t) raise(tmax[t], m[t], l[t], acc[t]);
+        }
+        PFrag<BF, PP> pf[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+#pragma unroll
+          for (int i = 0; i < NZ; ++i) {
+            p[t][i] = weight<PARTS>(p[t][i], m[t]);
+            l[t] += p[t][i];
+          }
+          pf[t].set(p[t]);
+        }
+        VTile<BF, D> vt;
+        vt.read(vst, sub, lane);
+        bool later = false;
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < NZ; ++i) {
+            const int tt = t0 + tile_token<BF>(c, i);
+            if (!(page_ok && tt < u.hi && (tt >= u.lo || tt < sinks))) vt.clear(i);
+          }
+          later = __any(vt.any_nonfinite());
+        }
+        if (later) {
+          put_off |= 1ull << (2 * j + sub);
+        } else {
+#pragma unroll
+          for (int n = 0; n < kAcc; ++n)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[t][n] = vt.template mul<PP>(n, pf[t], acc[t][n]);
+        }
+      }
+      wait_vmcnt<0>();
+      __syncthreads();
+    }
+    while (put_off) {
+      const int j = __builtin_ctzll(put_off);
+      put_off &= put_off - 1;
+      const int t0 = span.tile(base + j / 2) * ST + (j & 1) * TT;
+      TilePages pp;
+      pp.p0 = pp.p1 = page_at(a, x.table, npages, t0 / a.ps);
+      if (BF && a.ps == 16) pp.p1 = page_at(a, x.table, npages, t0 / a.ps + 1);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        late_tile<BF, D, PARTS, PP>(x, pp, t0, lane, q[t], lo[t], hi[t], sinks, m[t], acc[t]);
+    }
+  }
+
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const float ls = group_sum(l[t]);
+    if (t * 16 + rl >= wrows) continue;
+    if (a.slots > 1) {
+      const size_t part = (size_t)row[t] * a.slots + w.slot;
+      if (c == 0) {
+        a.part_ml[2 * part] = m[t];
+        a.part_ml[2 * part + 1] = ls;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < kAcc; n += 4)
+          *reinterpret_cast<f32x4*>(a.part_o + part * D + VTile<BF, D>::coord(c, n, i)) =
+              f32x4{acc[t][n][i], acc[t][n + 1][i], acc[t][n + 2][i], acc[t][n + 3][i]};
+    } else {
+      const float inv = inverse(ls);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < kAcc; n += 4)
+          store_out<PARTS>(a.out, (size_t)row[t] * D + VTile<BF, D>::coord(c, n, i),
+                           f32x4{acc[t][n][i], acc[t][n + 1][i], acc[t][n + 2][i],
+                                 acc[t][n + 3][i]} * inv);
+      if (c == 0 && a.lse) a.lse[row[t]] = log_sum(m[t], ls);
+    }
+  }
+}
+
+template <bool BF, int D, int PARTS, bool ROWS>
+__global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  const Block w = block_of(a, blockIdx.x);
+  if constexpr (ROWS) {
+    if (w.pre ? a.pre_rows : a.own_rows) {
+      attend_rows<BF, D, PARTS>(a, w, smem);
+      return;
+    }
+  }
+  attend_tokens<BF, D, PARTS>(a, w, smem);
+}
+
+// Joins the parts of each row. D/4 threads hold 4 coordinates each of a row's
+// parts s, s + SG, ...; the SG groups are joined through LDS.
+constexpr int kJoinThreads = 256;
+
+template <int D, int PARTS, int SG>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const float* __restrict__ part_o,
+                                                            const float* __restrict__ part_ml,
+                                                            int slots, int rows,
+                                                            void* __restrict__ out,
+                                                            float* __restrict__ lse) {
+  constexpr int TPR = D / 4;
+  constexpr int kRows = kJoinThreads / (TPR * SG);
+  constexpr int U = 4;  // parts of a thread in flight
+  __shared__ f32x4 so[kRows][SG][TPR];
+  __shared__ float sml[kRows][SG][2];
+  const int tid = threadIdx.x, d4 = tid % TPR, sg = tid / TPR % SG, rr = tid / (TPR * SG);
+  const int r = blockIdx.x * kRows + rr;
+  float M = -FLT_MAX, l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+  if (r < rows) {
+    const f32x2* ml = reinterpret_cast<const f32x2*>(part_ml) + (size_t)r * slots;
+    const f32x4* po = reinterpret_cast<const f32x4*>(part_o) + (size_t)r * slots * TPR + d4;
+    for (int s0 = sg; s0 < slots; s0 += U * SG) {
+      f32x2 x[U];
+      f32x4 y[U];
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        const int s = min(s0 + e * SG, slots - 1);
+        x[e] = ml[s];
+        y[e] = po[(size_t)s * TPR];
+      }
+      float mn = M;
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        if (s0 + e * SG >= slots) x[e] = f32x2{-FLT_MAX, 0.0f};
+        if (!(x[e][1] == 0.0f)) mn = fmaxf(mn, x[e][0]);
+      }
+      const float f = exp2f((M - mn) * kLog2e);
+      l *= f;
+      o *= f;
+      M = mn;
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        if (x[e][1] == 0.0f) continue;
+        const float g = exp2f((x[e][0] - M) * kLog2e);
+        l += g * x[e][1];
+        o += g * y[e];
+      }
+    }
+  }
+  if constexpr (SG > 1) {
+    so[rr][sg][d4] = o;
+    if (d4 == 0) {
+      sml[rr][sg][0] = M;
+      sml[rr][sg][1] = l;
+    }
+    __syncthreads();
+    if (sg != 0) return;
+    float mn = -FLT_MAX;
+#pragma unroll
+    for (int e = 0; e < SG; ++e)
+      if (!(sml[rr][e][1] == 0.0f)) mn = fmaxf(mn, sml[rr][e][0]);
+    l = 0.0f;
+    o = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < SG; ++e) {
+      const float le = sml[rr][e][1];
+      if (le == 0.0f) continue;
+      const float g = exp2f((sml[rr][e][0] - mn) * kLog2e);
+      l += g * le;
+      o += g * so[rr][e][d4];
+    }
+    M = mn;
+  }
+  if (r >= rows) return;
+  store_out<PARTS>(out, (size_t)r * D + d4 * 4, o * inverse(l));
+  if (d4 == 0 && lse) lse[r] = log_sum(M, l);
+}
+
+// Raises a kernel's LDS limit on the current device, once (a repeat by two
+// threads at the same time does no harm).
+hipError_t raise_lds(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (hipError_t e = hipGetDevice(&dev)) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load() & bit) return hipSuccess;
+  if (hipError_t e =
+          hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes))
+    return e;
+  done.fetch_or(bit);
+  return hipSuccess;
 }
 
 template <bool BF, int D, int PARTS>
 hipError_t launch(const AttendArgs& a, long long items, hipStream_t st) {
-  hipLaunchKernelGGL((attend_kernel<BF, D, PARTS>), dim3((unsigned)items), dim3(kAttThreads), 0, st,
-                     a);
+  constexpr size_t few = sizeof(TokensLds<BF, D>), many = sizeof(RowsLds<BF, D>);
+  if (a.pre_rows || a.own_rows) {
+    auto* f = attend_kernel<BF, D, PARTS, true>;
+    constexpr size_t lds = few > many ? few : many;
+    static std::atomic<uint64_t> raised{0};  // devices whose kernel has the limit
+    if (hipError_t e = raise_lds(reinterpret_cast<const void*>(f), lds, raised)) return e;
+    hipLaunchKernelGGL(f, dim3((unsigned)items), dim3(kAttThreads), lds, st, a);
+  } else {
+    hipLaunchKernelGGL((attend_kernel<BF, D, PARTS, false>), dim3((unsigned)items),
+                       dim3(kAttThreads), few, st, a);
+  }
+  return hipGetLastError();
+}
+
+template <int D, int PARTS>
+hipError_t join(const AttendPlan& p, const float* o, const float* ml, void* out, float* lse,
+                hipStream_t st) {
+  const int rows = (int)p.rows;
+  constexpr int TPR = D / 4, kMost = kJoinThreads / TPR;
+  const auto grid = [&](int sg) { return dim3((unsigned)((rows * (long long)sg * TPR + kJoinThreads - 1) / kJoinThreads)); };
+  // up to 8 parts: two groups of 4 in flight; more: the whole workgroup on a row
+  if (p.slots <= 8)
+    hipLaunchKernelGGL((join_kernel<D, PARTS, 2>), grid(2), dim3(kJoinThreads), 0, st, o, ml,
+                       p.slots, rows, out, lse);
+  else
+    hipLaunchKernelGGL((join_kernel<D, PARTS, kMost>), grid(kMost), dim3(kJoinThreads), 0, st, o,
+                       ml, p.slots, rows, out, lse);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Parts of a row block's tokens: enough workgroups for kAttWgsPerCU a CU, of
-// at least one tile per wave.
-static int splits_for(long long blocks, long long tiles) {
-  const long long want = (kAttWgsPerCU * kNumCUs + blocks - 1) / blocks;
-  const long long most = (tiles + kAttWaves - 1) / kAttWaves;
-  long long s = want < most ? want : most;
-  if (s < 1) s = 1;
+// Parts of a row block's tokens: enough workgroups for `want` in all, each of
+// at least `least` tiles.
+static int splits_for(long long blocks, long long tiles, long long want, int least) {
+  long long s = (want + blocks - 1) / blocks;
+  const long long most = (tiles + least - 1) / least;
+  if (s > most) s = most;
   if (s > kAttMaxSplits) s = kAttMaxSplits;
-  return (int)s;
+  return s < 1 ? 1 : (int)s;
 }
 
-AttendPlan plan_attend(const LaunchShape& s, int n, int window, int sinks, int prefix_pages) {
+AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int sinks,
+                       int prefix_pages) {
   AttendPlan p;
   const int TT = s.bf16 ? kTile<true> : kTile<false>;
   const long long total = (long long)s.max_pages * s.page_size;
   const long long prefix = (long long)prefix_pages * s.page_size;
+  const int many = kAttWaves * 16 * (s.bf16 && q_bf16 ? kRowTiles<true, 1> : kRowTiles<true, 3>);
+  const long long want = (long long)kAttWgsPerCU * kNumCUs;
   p.rows = (long long)s.batch * n * s.num_q_heads;
-  p.row_tiles = (n * s.group + 15) / 16;
+  const int own = n * s.group, pre = s.batch * s.group;
+  p.own_rows = own >= kAttManyRows;
+  p.row_block = p.own_rows ? many : 16;
+  p.row_blocks = (own + p.row_block - 1) / p.row_block;
   // tokens a row block of the sequences' own part can see
-  const long long span = (long long)window + 16 / s.group + 1;
+  const long long span = (long long)window + p.row_block / s.group + 1;
   const long long seen = total - prefix < span ? total - prefix : span;
   const long long tiles = (seen + TT - 1) / TT + 1 + (sinks + TT - 1) / TT;
-  const long long blocks = (long long)s.batch * s.num_kv_heads * p.row_tiles;
+  const long long blocks = (long long)s.batch * s.num_kv_heads * p.row_blocks;
+  // a workgroup's tokens: at least one tile a wave, or four stages
+  const int least = p.own_rows ? 8 : kAttWaves;
   if (prefix_pages > 0) {
-    p.pre_tiles = (s.batch * s.group + 15) / 16;
-    const long long pre_blocks = (long long)s.num_kv_heads * p.pre_tiles;
-    p.pre_splits = splits_for(pre_blocks, (prefix + TT - 1) / TT);
+    p.pre_rows = pre >= kAttManyRows;
+    p.pre_block = p.pre_rows ? many : 16;
+    const long long pre_blocks =
+        (long long)s.num_kv_heads * ((pre + p.pre_block - 1) / p.pre_block);
+    p.pre_splits = splits_for(pre_blocks, (prefix + TT - 1) / TT, want,
+                              p.pre_rows ? 8 : kAttWaves);
+    p.pre_items = pre_blocks * p.pre_splits;
   }
-  p.pre_items = (long long)s.num_kv_heads * p.pre_tiles * p.pre_splits;
-  p.splits = total > prefix ? splits_for(blocks, tiles) : 0;
+  p.splits = total > prefix ? splits_for(blocks, tiles, want, least) : 0;
   p.items = p.pre_items + blocks * p.splits;
   p.slots = p.pre_splits + p.splits;
   if (p.slots > 1) {
@@ -441,12 +843,15 @@ hipError_t launch_attend(const LaunchShape& s, const AttendPlan& p, const void* 
   a.window = window;
   a.sinks = sinks;
   a.prefix = prefix_pages * s.page_size;
-  a.pre_tiles = p.pre_tiles;
+  a.pre_block = p.pre_block;
   a.pre_splits = p.pre_splits;
   a.pre_items = (int)p.pre_items;
-  a.row_tiles = p.row_tiles;
+  a.row_block = p.row_block;
+  a.row_blocks = p.row_blocks;
   a.splits = p.splits;
   a.slots = p.slots;
+  a.pre_rows = p.pre_rows;
+  a.own_rows = p.own_rows;
   if (!s.bf16) return s.head_dim == 64 ? launch<false, 64, 3>(a, p.items, st)
                                        : launch<false, 128, 3>(a, p.items, st);
   if (q_bf16) return s.head_dim == 64 ? launch<true, 64, 1>(a, p.items, st)
@@ -459,16 +864,9 @@ hipError_t launch_join(const LaunchShape& s, const AttendPlan& p, bool q_bf16, v
                        float* lse, void* ws, hipStream_t st) {
   const float* o = static_cast<const float*>(ws);
   const float* ml = reinterpret_cast<const float*>(static_cast<const char*>(ws) + p.ml_off);
-  const int rows = (int)p.rows, per = 256 / (s.head_dim / 4);
-  const dim3 grid((unsigned)((rows + per - 1) / per));
-  if (s.head_dim == 64) {
-    if (q_bf16) hipLaunchKernelGGL((join_kernel<64, 1>), grid, dim3(256), 0, st, o, ml, p.slots, rows, out, lse);
-    else hipLaunchKernelGGL((join_kernel<64, 3>), grid, dim3(256), 0, st, o, ml, p.slots, rows, out, lse);
-  } else {
-    if (q_bf16) hipLaunchKernelGGL((join_kernel<128, 1>), grid, dim3(256), 0, st, o, ml, p.slots, rows, out, lse);
-    else hipLaunchKernelGGL((join_kernel<128, 3>), grid, dim3(256), 0, st, o, ml, p.slots, rows, out, lse);
-  }
-  return hipGetLastError();
+  if (s.head_dim == 64)
+    return q_bf16 ? join<64, 1>(p, o, ml, out, lse, st) : join<64, 3>(p, o, ml, out, lse, st);
+  return q_bf16 ? join<128, 1>(p, o, ml, out, lse, st) : join<128, 3>(p, o, ml, out, lse, st);
 }
 
 }  // namespace ekv

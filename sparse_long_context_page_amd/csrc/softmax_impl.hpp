@@ -92,6 +92,27 @@ __device__ __forceinline__ uint32_t bf16_round(float x) {
 __device__ __forceinline__ bf16x8 as_bf(const u32x4& v) { return __builtin_bit_cast(bf16x8, v); }
 
 // ---------------------------------------------------------------------------
+// Tiles staged in LDS for several waves
+
+// A stage is two tiles of K and the same of V. Row r of 16-byte chunks lies at
+// r * row bytes, chunk ch at slot ch ^ swizzle(r): the 16 tokens that a score
+// operand reads at one chunk fall on different banks (without it all 16 hit
+// the same ones), and a value row is still read whole.
+template <bool BF, int D>
+struct Stage {
+  static constexpr int kTokens = 2 * kTile<BF>;
+  static constexpr int kRow = D * (BF ? 2 : 4);
+  static constexpr int kChunks = kRow / 16;
+  static constexpr int kBytes = kTokens * kRow;  // of K, and of V
+  __device__ __forceinline__ static int swizzle(int r) {
+    return (BF ? ((r >> 3) & 3) << 2 | (r & 3) : r & 15) & (kChunks - 1);
+  }
+  __device__ __forceinline__ static int at(int r, int ch) {
+    return r * kRow + ((ch ^ swizzle(r)) << 4);
+  }
+};
+
+// ---------------------------------------------------------------------------
 // Query rows as the B operand
 
 // PARTS: bf16 parts of a query value (3 for float32 queries: the exact split
@@ -165,6 +186,16 @@ struct KTile<true, D> {
       for (int s = 0; s < D / 32; ++s) f[u][s] = load_vec<kStream, u32x4>(r + s * 64);
     }
   }
+  // tile `sub` of a stage
+  __device__ __forceinline__ void read(const char* st, int sub, int lane) {
+    const int m = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s)
+        f[u][s] = *reinterpret_cast<const u32x4*>(
+            st + Stage<true, D>::at(sub * 32 + ((m >> 2) << 3) + u * 4 + (m & 3), c + s * 4));
+  }
   template <int PARTS>
   __device__ __forceinline__ void scores(const QFrag<true, D, PARTS>& q, float (&z)[8]) const {
 #pragma unroll
@@ -191,6 +222,12 @@ struct KTile<false, D> {
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) f[s] = load_vec<kStream, f32x4>(r + s * 64);
   }
+  __device__ __forceinline__ void read(const char* st, int sub, int lane) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      f[s] = *reinterpret_cast<const f32x4*>(
+          st + Stage<false, D>::at(sub * 16 + (lane & 15), (lane >> 4) + s * 4));
+  }
   template <int PARTS>
   __device__ __forceinline__ void scores(const QFrag<false, D, PARTS>& q, float (&z)[4]) const {
     // four sums of D/4 products each: shorter chains round less (one chain:
@@ -203,6 +240,46 @@ struct KTile<false, D> {
         a[e] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[s][e], q.f[s][e], a[e], 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] = (a[0][i] + a[1][i]) + (a[2][i] + a[3][i]);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Weights as the B operand of the second product
+
+// PP bf16 parts: 3 (p exact), 2 (p to 16 significant bits) or 1 (rounded to
+// nearest even).
+template <bool BF, int PP>
+struct PFrag;
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+template <int PP>
+struct PFrag<true, PP> {
+  u32x4 b[PP];
+  __device__ __forceinline__ void set(const float (&p)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (PP == 1) {
+        const f32x2 x = {p[2 * k], p[2 * k + 1]};
+        b[0][k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+      } else {
+        uint32_t x[3], y[3];
+        split3(p[2 * k], x);
+        split3(p[2 * k + 1], y);
+#pragma unroll
+        for (int s = 0; s < PP; ++s) b[s][k] = pack_hi(x[s], y[s]);
+      }
+    }
+  }
+};
+
+template <int PP>
+struct PFrag<false, PP> {
+  float b[4];
+  __device__ __forceinline__ void set(const float (&p)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = p[i];
   }
 };
 
@@ -228,6 +305,17 @@ struct VTile<true, D> {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = load_vec<kStream, vec>(r + j * (D * 2));
   }
+  __device__ __forceinline__ void read(const char* st, int sub, int lane) {
+    const int m = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = sub * 32 + c * 8 + j;
+      if constexpr (D == 128)
+        f[j] = *reinterpret_cast<const vec*>(st + Stage<true, D>::at(r, m));
+      else
+        f[j] = *reinterpret_cast<const vec*>(st + Stage<true, D>::at(r, m >> 1) + (m & 1) * 8);
+    }
+  }
   __device__ __forceinline__ void clear(int j) { f[j] = vec(0); }
   // An infinity or NaN among the values held?
   __device__ __forceinline__ bool any_nonfinite() const {
@@ -239,44 +327,18 @@ struct VTile<true, D> {
         bad |= (f[j][e] & 0x7f800000u) == 0x7f800000u || (f[j][e] & 0x7f80u) == 0x7f80u;
     return bad;
   }
-  // acc += V^T P^T with P in PP bf16 parts: 3 (p exact), 2 (p to 16
-  // significant bits) or 1 (rounded to nearest even)
-  // kMine: only lanes with `mine` take the sums
-  template <int PP, bool kMine = false>
-  __device__ __forceinline__ void pv(const float (&p)[8], f32x4 (&acc)[kAcc],
-                                     bool mine = true) const {
-    u32x4 b[PP];
-    if constexpr (PP == 1) {
+  // acc[n] += V^T P^T, instruction n
+  template <int PP>
+  __device__ __forceinline__ f32x4 mul(int n, const PFrag<true, PP>& p, f32x4 o) const {
+    u32x4 a;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        b[0][k] = bf16_round(p[2 * k]) | (bf16_round(p[2 * k + 1]) << 16);
-    } else {
+    for (int k = 0; k < 4; ++k)
+      a[k] = (n & 1) ? pack_hi(f[2 * k][n / 2], f[2 * k + 1][n / 2])
+                     : pack_lo(f[2 * k][n / 2], f[2 * k + 1][n / 2]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t x[3], y[3];
-        split3(p[2 * k], x);
-        split3(p[2 * k + 1], y);
-#pragma unroll
-        for (int s = 0; s < PP; ++s) b[s][k] = pack_hi(x[s], y[s]);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < kAcc; ++n) {
-      u32x4 a;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        a[k] = (n & 1) ? pack_hi(f[2 * k][n / 2], f[2 * k + 1][n / 2])
-                       : pack_lo(f[2 * k][n / 2], f[2 * k + 1][n / 2]);
-      f32x4 o = kMine ? f32x4{0, 0, 0, 0} : acc[n];
-#pragma unroll
-      for (int s = PP - 1; s >= 0; --s)
-        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(a), as_bf(b[s]), o, 0, 0, 0);
-      if constexpr (kMine) {
-        if (mine) acc[n] += o;
-      } else {
-        acc[n] = o;
-      }
-    }
+    for (int s = PP - 1; s >= 0; --s)
+      o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(a), as_bf(p.b[s]), o, 0, 0, 0);
+    return o;
   }
   // coordinate of acc[n][i]
   __device__ __forceinline__ static int coord(int c, int n, int i) {
@@ -298,6 +360,15 @@ struct VTile<false, D> {
       for (int h = 0; h < D / 64; ++h)
         f[j][h] = load_vec<kStream, f32x4>(r + j * (D * 4) + h * 256);
   }
+  __device__ __forceinline__ void read(const char* st, int sub, int lane) {
+    const int m = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        f[j][h] = *reinterpret_cast<const f32x4*>(
+            st + Stage<false, D>::at(sub * 16 + c * 4 + j, m + h * 16));
+  }
   __device__ __forceinline__ void clear(int j) {
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) f[j][h] = f32x4{0, 0, 0, 0};
@@ -313,21 +384,12 @@ struct VTile<false, D> {
           bad |= (__float_as_uint(f[j][h][e]) & 0x7f800000u) == 0x7f800000u;
     return bad;
   }
-  template <int PP, bool kMine = false>
-  __device__ __forceinline__ void pv(const float (&p)[4], f32x4 (&acc)[kAcc],
-                                     bool mine = true) const {
+  template <int PP>
+  __device__ __forceinline__ f32x4 mul(int n, const PFrag<false, PP>& p, f32x4 o) const {
 #pragma unroll
-    for (int n = 0; n < kAcc; ++n) {
-      f32x4 o = kMine ? f32x4{0, 0, 0, 0} : acc[n];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o = __builtin_amdgcn_mfma_f32_16x16x4f32(f[j][n >> 2][n & 3], p[j], o, 0, 0, 0);
-      if constexpr (kMine) {
-        if (mine) acc[n] += o;
-      } else {
-        acc[n] = o;
-      }
-    }
+    for (int j = 0; j < 4; ++j)
+      o = __builtin_amdgcn_mfma_f32_16x16x4f32(f[j][n >> 2][n & 3], p.b[j], o, 0, 0, 0);
+    return o;
   }
   __device__ __forceinline__ static int coord(int c, int n, int i) {
     return (n >> 2) * 64 + (c * 4 + i) * 4 + (n & 3);

@@ -10,7 +10,9 @@ output by at most 2 (ez + 2^-22) max_t |v_td - out_d| (numerator and
 denominator), plus the rounding of the running sums: at most 16 per tile or
 part of a row's tokens, each 2^-24 of max |v|. The log of the sum is off by
 ez + 2^-22 plus the roundings of the sum and of the result. A bf16 output adds
-half a step, 2^-8 of its value, and its weights are used to 16 bits: 2^-16.
+half a step, 2^-8 of its value. With bf16 queries the weights are used to 16
+bits (2^-16 of max |v|), in the many-rows form (33 rows of a KV head) to 8,
+each off by at most 2^-8 of itself: 2^-8 of the weighted mean of |v|.
 """
 import math
 
@@ -76,7 +78,7 @@ class Cache:
         return self.k.double().numpy(), self.v.double().numpy()
 
 
-def check(c, q, out, lse, ref, ref_lse):
+def check(c, q, out, lse, ref, ref_lse, mean_abs=0.0):
     k, v = c.np64()
     D = c.D
     # sum_d |q_d k_d| row by row would be exact; the largest |q| bounds it
@@ -89,7 +91,7 @@ def check(c, q, out, lse, ref, ref_lse):
     tiles = sum(-(-L // 16) for L in c.lens) + 64
     tol = 2 * (ez + 2.0**-22)[..., None] * (vmax + np.abs(ref)) + 16 * tiles * 2.0**-24 * vmax
     if q.dtype == torch.bfloat16:
-        tol = tol + 2.0**-8 * np.abs(ref) + 2.0**-16 * vmax
+        tol = tol + 2.0**-8 * np.abs(ref) + 2.0**-16 * vmax + 2.0**-8 * mean_abs
     o = out.double().cpu().numpy()
     assert np.isfinite(o).all()
     err = np.abs(o - ref)
@@ -100,6 +102,16 @@ def check(c, q, out, lse, ref, ref_lse):
     le = np.abs(np.where(none, 0, ll) - np.where(none, 0, ref_lse))
     lt = ez + 2.0**-22 + 2.0**-23 * np.where(none, 0, np.abs(ref_lse)) + 16 * tiles * 2.0**-24
     assert (le <= lt).all(), float((le / lt).max())
+
+
+def reference(c, q, lens, window, sinks, rows):
+    """out, lse and, where the many-rows form rounds weights, the weighted mean of |v|."""
+    k, v = c.np64()
+    qn = q.double().numpy()
+    out, lse = S.window_decode(qn, k, v, c.table, lens, window, sinks)
+    rounded = q.dtype == torch.bfloat16 and rows >= 33
+    return out, lse, (S.window_decode(qn, k, np.abs(v), c.table, lens, window, sinks)[0]
+                      if rounded else 0.0)
 
 
 def run_window(c, q, window, sinks, **kw):
@@ -126,6 +138,10 @@ def run_window(c, q, window, sinks, **kw):
     ("bf16", "f32", 128, 16, 1, 1, 40, 30, 2),
     ("bf16", "bf16", 128, 16, 2, 4, 37, 2**31 - 1, 2**31 - 1),
     ("f32", "f32", 128, 64, 1, 1, 33, 20, 5),
+    ("bf16", "bf16", 64, 64, 1, 8, 50, 77, 33),
+    ("bf16", "f32", 64, 32, 2, 2, 70, 2**31 - 1, 0),
+    ("f32", "f32", 64, 16, 1, 8, 9, 100, 17),
+    ("bf16", "bf16", 128, 32, 1, 1, 140, 64, 1),
 ])
 def test_window(kv, qt, D, ps, Hkv, G, n, window, sinks):
     # lengths of 0 and 1, around a page, a tile and several splits
@@ -134,8 +150,7 @@ def test_window(kv, qt, D, ps, Hkv, G, n, window, sinks):
     q = c.query(n, Hkv * G, qt)
     announce(f"window {kv}/{qt} D{D} ps{ps} Hkv{Hkv} G{G} n{n} W{window} S{sinks}")
     out, lse = run_window(c, q, window, sinks)
-    ref = S.window_decode(q.double().numpy(), *c.np64(), c.table, lens, window, sinks)
-    check(c, q, out, lse, *ref)
+    check(c, q, out, lse, *reference(c, q, lens, window, sinks, n * G))
 
 
 @pytest.mark.parametrize("kv,qt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
@@ -171,7 +186,8 @@ def test_hidden_rows_have_no_effect():
                                                window, sinks))
 
 
-@pytest.mark.parametrize("kv,qt,G", [("bf16", "bf16", 4), ("bf16", "f32", 1), ("f32", "f32", 2)])
+@pytest.mark.parametrize("kv,qt,G", [("bf16", "bf16", 4), ("bf16", "f32", 1), ("f32", "f32", 2),
+                                     ("bf16", "bf16", 1), ("bf16", "f32", 8)])
 def test_infinite_value_reaches_only_the_rows_that_see_it(kv, qt, G):
     """The newest of 24 tokens and the oldest in the first one's window hold
     values that are not finite: the rows between see neither."""
@@ -191,7 +207,9 @@ def test_infinite_value_reaches_only_the_rows_that_see_it(kv, qt, G):
     assert np.isfinite(o[~bad]).all()
     o[bad] = 0
     ref = np.where(bad, 0, ref)
-    check(c, q, torch.from_numpy(o), lse, ref, ref_lse)
+    mean_abs = S.window_decode(q.double().numpy(), c.np64()[0], np.abs(c.np64()[1]), c.table,
+                               (L,), window, 0)[0] if n * G >= 33 else 0.0
+    check(c, q, torch.from_numpy(o), lse, ref, ref_lse, np.where(bad, 0, mean_abs))
 
 
 def test_pages_that_are_not_there():
@@ -274,7 +292,7 @@ def test_prefix(kv, qt, D, ps, Hkv, G, B, pages):
     q = c.query(1, Hkv * G, qt)
     announce(f"prefix {kv}/{qt} D{D} ps{ps} Hkv{Hkv} G{G} B{B} pages{pages}")
     out, lse = run_prefix(c, q, pages)
-    check(c, q, out, lse, *S.window_decode(q.double().numpy(), *c.np64(), c.table, lens, 1 << 30, 0))
+    check(c, q, out, lse, *reference(c, q, lens, 1 << 30, 0, B * G))
 
 
 def test_prefix_is_the_whole_table():
@@ -287,24 +305,26 @@ def test_prefix_is_the_whole_table():
                                            1 << 30, 0))
 
 
+@pytest.mark.parametrize("times", [1, 4])
 @pytest.mark.parametrize("kv,qt", [("bf16", "bf16"), ("f32", "f32")])
-def test_prefix_values_hidden_from_short_sequences(kv, qt):
+def test_prefix_values_hidden_from_short_sequences(kv, qt, times):
     """A prefix value that is not finite, behind the end of some sequences of
     the batch: only the others' outputs hold it."""
     P = 6 * 16
-    lens = [P + 3, 50, P, 0, 60, 61]
+    lens = [P + 3, 50, P, 0, 60, 61] * times
     c = Cache(13, lens, 1, 64, 16, kv, prefix_pages=6)
     c.v[c.table[0, 60 // 16], 0, 60 % 16, 7] = math.inf
     q = c.query(1, 2, qt)
     announce(f"prefix infinite value {kv}")
     out, lse = run_prefix(c, q, 6)
-    ref, ref_lse = S.window_decode(q.double().numpy(), *c.np64(), c.table, lens, 1 << 30, 0)
+    ref, ref_lse, mean_abs = reference(c, q, lens, 1 << 30, 0, 2 * len(lens))
     o = out.double().cpu().numpy()
     sees = np.array(lens) > 60
     assert not np.isfinite(o[sees][..., 7]).any()
     o[sees, ..., 7] = 0
     ref[sees, ..., 7] = 0
-    check(c, q, torch.from_numpy(o), lse, ref, ref_lse)
+    mean_abs = np.nan_to_num(mean_abs, posinf=0.0)
+    check(c, q, torch.from_numpy(o), lse, ref, ref_lse, mean_abs)
 
 
 def test_prefix_equals_window_over_the_same_pages():
