@@ -423,6 +423,7 @@ int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int3
  *   keep         1 .. 2^25; sinks, recent >= 0 with sinks + recent <= keep (else
  *                ENTMAXKV_ERR_INVALID)
  *   weights      float32 [batch, num_kv_heads, max_pages_per_seq * page_size]
+ *                (16-byte aligned)
  *   new_table    int32 [batch, max_pages_per_seq], the block table afterwards:
  *                its first ceil(n / page_size) columns name the pages written,
  *                which no sequence may read in this call (a page that is read

@@ -762,7 +762,8 @@ int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
   if (!k_pool || !v_pool || !block_table || !seq_lens || !weights || !new_table || !kept ||
       !new_lens)
     return ENTMAXKV_ERR_INVALID;
-  if (!aligned(k_pool, 16) || !aligned(v_pool, 16)) return ENTMAXKV_ERR_INVALID;
+  if (!aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(weights, 16))
+    return ENTMAXKV_ERR_INVALID;
   // the copies run in any order
   if (new_weights == weights || new_lens == seq_lens || new_table == block_table)
     return ENTMAXKV_ERR_INVALID;

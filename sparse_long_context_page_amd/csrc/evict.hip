@@ -12,10 +12,13 @@ namespace ekv {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Weights. One pass over K: a wave takes tiles of one (sequence, KV head);
-// scores as in the softmax decode (row = head = lane % 16), then the sum over
-// rows by a butterfly across the 16 lanes that leaves each lane complete sums
-// of its own tokens. Bound by reading K.
+// Weights. One pass over K: scores as in the softmax decode (row = head =
+// lane % 16), then the sum over rows by a butterfly across the 16 lanes that
+// leaves each lane complete sums of its own tokens. Bound by reading K, which
+// each wave streams through LDS of its own, one tile ahead. The tiles of all
+// sequences, end to end, are shared out evenly over the workgroups of a KV
+// head, whatever the lengths (an equal number of workgroups a sequence: 89
+// against 7x us on lengths of 22K to 32K). No sum crosses a workgroup.
 
 struct WeightArgs {
   const void* q;
@@ -25,8 +28,8 @@ struct WeightArgs {
   const float* tau;
   const float* w_in;  // nullable
   float* w_out;
-  int H, Hkv, G, ps, max_pages, num_phys;
-  int window, sinks, splits;
+  int batch, H, Hkv, G, ps, max_pages, num_phys;
+  int window, sinks, wgs;  // workgroups a KV head
   float decay, am1, m;
 };
 
@@ -45,23 +48,20 @@ __device__ __forceinline__ float weight_of(float z, float tau, float am1, float 
   return x == 0.0f ? 0.0f : exp2f(m * log2f(x));
 }
 
+constexpr int kWeightWaves = 4;
+
+// Tiles [v0, v1) of sequence b.
 template <bool BF, int D, int PARTS, int POW>
-__global__ __launch_bounds__(256) void weights_kernel(WeightArgs a) {
+__device__ __forceinline__ void weights_of(const WeightArgs& a, int b, int g, int L, int v0,
+                                           int v1, const WaveTile<BF, D>& tile,
+                                           char (&buf)[2][WaveTile<BF, D>::kBytes], int wave,
+                                           int lane) {
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
-  constexpr int NW = 256 / kWave;
+  constexpr int NW = kWeightWaves;
   constexpr int QB = PARTS == 1 ? 2 : 4;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane >> 4, rl = lane & 15;
-  const int split = blockIdx.x % a.splits;
-  const int x = blockIdx.x / a.splits;
-  const int g = x % a.Hkv, b = x / a.Hkv;
-  const int L = clamp_len(a.seq_lens[b], a.max_pages * a.ps);
   const int vis_lo = max(L - a.window, 0);
-  const int tiles = (L + TT - 1) / TT;
-  const int per = (tiles + a.splits - 1) / a.splits;
-  const int v0 = min(split * per, tiles), v1 = min(v0 + per, tiles);
   const int npages = (L + a.ps - 1) / a.ps;
   const int32_t* table = a.block_table + (size_t)b * a.max_pages;
   KvView kv;
@@ -93,15 +93,29 @@ __global__ __launch_bounds__(256) void weights_kernel(WeightArgs a) {
     auto pages = [&](int j) {
       return TilePages{__builtin_amdgcn_readlane(pg0, j), __builtin_amdgcn_readlane(pg1, j)};
     };
-    KTile<BF, D> kt;
+    // the sum that this lane adds to, in tile j (0: none of its own)
+    auto old_sum = [&](int j) {
+      const int t = (base + j * NW) * TT + tile_token<BF>(c, own);
+      return a.w_in && Sum::owner(rl) && t < L ? a.w_in[wrow + t] : 0.0f;
+    };
     TilePages pc = pages(0);
-    kt.template load<true>(kv, pc, base * TT, lane);
+    float old = old_sum(0);
+    tile.load(kv, pc, base * TT, buf[0]);
     for (int j = 0; j < nt; ++j) {
       const int t0 = (base + j * NW) * TT;
+      const TilePages pn = pages(min(j + 1, nt - 1));
+      float next = 0.0f;
+      if (j + 1 < nt) {
+        next = old_sum(j + 1);
+        tile.load(kv, pn, (base + (j + 1) * NW) * TT, buf[(j + 1) & 1]);
+        wait_vmcnt<WaveTile<BF, D>::kLoads>();  // tile j has landed: the next one's are newer
+      } else {
+        wait_vmcnt<0>();
+      }
+      KTile<BF, D> kt;
+      kt.read(buf[j & 1], 0, lane);
       float z[NZ];
       kt.template scores<PARTS>(q, z);
-      const TilePages pn = pages(min(j + 1, nt - 1));
-      if (j + 1 < nt) kt.template load<true>(kv, pn, (base + (j + 1) * NW) * TT, lane);
       const bool page_ok = (!BF || c < 2 ? pc.p0 : pc.p1) >= 0;
 #pragma unroll
       for (int i = 0; i < NZ; ++i) {
@@ -111,33 +125,265 @@ __global__ __launch_bounds__(256) void weights_kernel(WeightArgs a) {
       }
       Sum::reduce(z, rl);
       const int t = t0 + tile_token<BF>(c, own);
-      if (Sum::owner(rl) && t < L)
-        a.w_out[wrow + t] = (a.w_in ? a.decay * a.w_in[wrow + t] : 0.0f) + z[0];
+      if (Sum::owner(rl) && t < L) a.w_out[wrow + t] = (a.w_in ? a.decay * old : 0.0f) + z[0];
       pc = pn;
+      old = next;
     }
+  }
+}
+
+template <bool BF, int D, int PARTS, int POW>
+__global__ __launch_bounds__(kWeightWaves* kWave) void weights_kernel(WeightArgs a) {
+  constexpr int TT = kTile<BF>;
+  __shared__ __align__(16) char buf[kWeightWaves][2][WaveTile<BF, D>::kBytes];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  // KV heads first: what runs together reads neighbouring parts of a page
+  const int g = blockIdx.x % a.Hkv, wg = blockIdx.x / a.Hkv;
+  const int max_tokens = a.max_pages * a.ps;
+  WaveTile<BF, D> tile;
+  tile.init(lane);
+  // every wave goes through the lengths, 64 sequences at a time: first for
+  // the sum of all tiles, then for this workgroup's share [lo, hi) of them
+  const auto tiles_of = [&](int b, int* L) {
+    *L = b < a.batch ? clamp_len(a.seq_lens[b], max_tokens) : 0;
+    return (*L + TT - 1) / TT;
+  };
+  long long total = 0;
+  int L = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += kWave) total += wave_sum(tiles_of(b0 + lane, &L));
+  const long long lo = total * wg / a.wgs, hi = total * (wg + 1) / a.wgs;
+  long long at = 0;
+  for (int b0 = 0; b0 < a.batch && at < hi; b0 += kWave) {
+    const int n = tiles_of(b0 + lane, &L);
+    const int incl = wave_incl_scan(n, lane);
+    const long long first = at + incl - n;
+    uint64_t mine = __ballot(n > 0 && first < hi && first + n > lo);
+    while (mine) {
+      const int s = __builtin_ctzll(mine);
+      mine &= mine - 1;
+      const long long f = at + lane_value(incl - n, s);
+      const int ns = lane_value(n, s);
+      weights_of<BF, D, PARTS, POW>(a, b0 + s, g, lane_value(L, s), (int)max(lo - f, 0ll),
+                                    (int)min(hi - f, (long long)ns), tile, buf[wave], wave, lane);
+    }
+    at += lane_value(incl, kWave - 1);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Selection: one workgroup per (sequence, KV head). A radix select over the
-// order-preserving image of the weights, 8 bits a pass from the top, finds
-// the smallest kept weight; each wave owns a contiguous stretch of tokens and
-// the kept ones are written in order behind those of the waves before it.
+// order-preserving image of the weights finds the smallest kept one: digits of
+// kDigit bits from the highest bit in which the keys differ (so that the first
+// histogram is spread and its LDS atomics seldom meet), until the boundary
+// digit is taken whole. Wave v holds the v-th stretch of the row, four
+// neighbouring tokens a lane and step, in registers where it has at most
+// kRegSteps steps (32768 tokens a row), else it reads it again for each pass;
+// the kept tokens are written in order behind those of the waves before.
 
 constexpr int kEvThreads = 1024;
 constexpr int kEvWaves = kEvThreads / kWave;
+constexpr int kDigit = 11;
+constexpr int kBins = 1 << kDigit;
+constexpr int kRegSteps = 8;   // steps of 4 * kWave tokens that a wave keeps in registers
+constexpr int kStep = 4 * kWave;
 
 __device__ __forceinline__ uint32_t weight_order(float w) {
   return w != w ? 0xffffffffu : float_order(w + 0.0f);  // a NaN counts as the largest
 }
 
+// Bins lie with a gap after every 32: a lane sums kPerLane neighbours, on
+// other banks than the next lane's.
+constexpr int kPerLane = kBins / kWave;
+__host__ __device__ constexpr int bin_at(int b) { return b + b / kPerLane; }
+
+struct EvictLds {
+  int hist[bin_at(kBins)];
+  uint32_t range[kEvWaves][2];
+  int wcnt[kEvWaves][2];
+  int bc[3];
+};
+
+// kRegs: the row fits the registers.
+template <bool kRegs>
+__device__ __forceinline__ void select_tokens(const float* __restrict__ w, int lo, int hi, int k,
+                                              int pos, int32_t* __restrict__ out, EvictLds& sh) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  // stretches of whole steps, from the step that holds token lo
+  const int first = lo & ~3;
+  const int per = ((hi - first + kEvWaves * kStep - 1) / (kEvWaves * kStep)) * kStep;
+  const int w0 = min(first + wave * per, hi), w1 = min(w0 + per, hi);
+  const int steps = (w1 - w0 + kStep - 1) / kStep;
+  // order keys of the lane's four tokens of step i; 0 (below every key) for
+  // tokens that do not compete
+  const auto load = [&](int i) -> uint4 {
+    const int t = w0 + i * kStep + lane * 4;
+    if (t >= w1) return make_uint4(0, 0, 0, 0);
+    const float4 f = *reinterpret_cast<const float4*>(w + t);
+    return make_uint4(t >= lo ? weight_order(f.x) : 0u,
+                      t + 1 >= lo && t + 1 < w1 ? weight_order(f.y) : 0u,
+                      t + 2 >= lo && t + 2 < w1 ? weight_order(f.z) : 0u,
+                      t + 3 >= lo && t + 3 < w1 ? weight_order(f.w) : 0u);
+  };
+  uint4 reg[kRegs ? kRegSteps : 1];
+  if constexpr (kRegs) {
+#pragma unroll
+    for (int i = 0; i < kRegSteps; ++i) reg[i] = load(i);
+  }
+  const auto each = [&](auto f) {
+    if constexpr (kRegs) {
+#pragma unroll
+      for (int i = 0; i < kRegSteps; ++i) {
+        f(reg[i].x);
+        f(reg[i].y);
+        f(reg[i].z);
+        f(reg[i].w);
+      }
+    } else {
+      constexpr int U = 4;  // loads in flight
+      for (int i = 0; i < steps; i += U) {
+        uint4 o[U];
+#pragma unroll
+        for (int e = 0; e < U; ++e) o[e] = load(i + e);
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          f(o[e].x);
+          f(o[e].y);
+          f(o[e].z);
+          f(o[e].w);
+        }
+      }
+    }
+  };
+
+  // the range of the keys
+  uint32_t mn = 0xffffffffu, mx = 0;
+  each([&](uint32_t o) {
+    mn = min(mn, o - 1u);  // 0 wraps to the largest
+    mx = max(mx, o);
+  });
+  mn = wave_min(mn);
+  mx = wave_max(mx);
+  if (lane == 0) {
+    sh.range[wave][0] = mn;
+    sh.range[wave][1] = mx;
+  }
+  for (int i = tid; i < bin_at(kBins); i += kEvThreads) sh.hist[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kEvWaves; ++v) {
+    mn = min(mn, sh.range[v][0]);
+    mx = max(mx, sh.range[v][1]);
+  }
+  ++mn;  // (there is a key: the row is longer than what is kept)
+  // the boundary: keys above `prefix` (under the mask) and k equal ones stay
+  uint32_t prefix = mx, pmask = 0xffffffffu;
+  if (mn != mx) {
+    int hb = 31 - __clz(mn ^ mx);
+    pmask = ~((2u << hb) - 1u);
+    prefix = mx & pmask;
+    while (true) {
+      const int sh0 = hb >= kDigit - 1 ? hb - (kDigit - 1) : 0;
+      const uint32_t dmask = (2u << (hb - sh0)) - 1u;
+      each([&](uint32_t o) {
+        if (o != 0u && (o & pmask) == prefix) atomicAdd(&sh.hist[bin_at((o >> sh0) & dmask)], 1);
+      });
+      __syncthreads();
+      if (wave == 0) {
+        // the lane whose kPerLane bins, counted from the top, hold the
+        // k-th key, then the bin among them
+        int s = 0;
+#pragma unroll 8
+        for (int i = 0; i < kPerLane; ++i) s += sh.hist[bin_at(kBins - 1 - (lane * kPerLane + i))];
+        const int below = wave_incl_scan(s, lane);
+        const uint64_t hit = __ballot(below - s < k && k <= below);
+        const int src = __builtin_ctzll(hit);
+        const int base = lane_value(below - s, src);
+        const int bin = kBins - 1 - (src * kPerLane + lane);
+        const int cnt = lane < kPerLane ? sh.hist[bin_at(bin)] : 0;
+        const int upto = base + wave_incl_scan(cnt, lane);
+        if (upto - cnt < k && k <= upto) {
+          sh.bc[0] = bin;
+          sh.bc[1] = upto - cnt;
+          sh.bc[2] = cnt;
+        }
+      }
+      __syncthreads();
+      prefix |= (uint32_t)sh.bc[0] << sh0;
+      pmask |= dmask << sh0;
+      k -= sh.bc[1];
+      if (sh.bc[2] == k || sh0 == 0) break;
+      hb = sh0 - 1;
+      for (int i = tid; i < bin_at(kBins); i += kEvThreads) sh.hist[i] = 0;
+      __syncthreads();
+    }
+  }
+
+  // where each wave's kept tokens go
+  int gt = 0, eq = 0;
+  each([&](uint32_t o) {
+    const uint32_t x = o & pmask;
+    gt += x > prefix;
+    eq += o != 0u && x == prefix;
+  });
+  gt = wave_sum(gt);
+  eq = wave_sum(eq);
+  if (lane == 0) {
+    sh.wcnt[wave][0] = gt;
+    sh.wcnt[wave][1] = eq;
+  }
+  __syncthreads();
+  int eqs = 0;
+  for (int v = 0; v < wave; ++v) {
+    pos += sh.wcnt[v][0];
+    eqs += sh.wcnt[v][1];
+  }
+  pos += min(eqs, k);
+  const auto emit = [&](int i, const uint4& o) {
+    const int t = w0 + i * kStep + lane * 4;
+    const uint32_t k4[4] = {o.x, o.y, o.z, o.w};
+    int e = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) e += k4[r] != 0u && (k4[r] & pmask) == prefix;
+    const int eincl = wave_incl_scan(e, lane);
+    int rank = eqs + eincl - e;  // equal keys before this lane's
+    bool take[4];
+    int n = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t x = k4[r] & pmask;
+      const bool is = k4[r] != 0u && x == prefix;
+      take[r] = x > prefix || (is && rank < k);
+      rank += is;
+      n += take[r];
+    }
+    const int nincl = wave_incl_scan(n, lane);
+    int at = pos + nincl - n;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (take[r]) out[at++] = t + r;
+    pos += lane_value(nincl, kWave - 1);
+    eqs += lane_value(eincl, kWave - 1);
+  };
+  if constexpr (kRegs) {
+#pragma unroll
+    for (int i = 0; i < kRegSteps; ++i)
+      if (i < steps) emit(i, reg[i]);
+  } else {
+    uint4 o = load(0);
+    for (int i = 0; i < steps; ++i) {
+      const uint4 nx = load(i + 1);
+      emit(i, o);
+      o = nx;
+    }
+  }
+}
+
 __global__ __launch_bounds__(kEvThreads) void evict_select_kernel(
     const int32_t* __restrict__ lens, const float* __restrict__ weights, int Hkv, int max_tokens,
     int keep, int sinks, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ new_lens) {
-  __shared__ int hist[256];
-  __shared__ int wcnt[kEvWaves][2];
-  __shared__ int bc[2];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  __shared__ EvictLds sh;
+  const int tid = threadIdx.x;
   const int row = blockIdx.x, b = row / Hkv;
   const int L = clamp_len(lens[b], max_tokens);
   const int n = min(L, keep);
@@ -149,78 +395,15 @@ __global__ __launch_bounds__(kEvThreads) void evict_select_kernel(
     return;
   }
   // tokens [sinks, hi) compete for keep - sinks - recent places
-  const int hi = L - recent;
-  const float* w = weights + (size_t)row * max_tokens;
-  uint32_t prefix = 0, pmask = 0;
-  int k = keep - sinks - recent;  // places left among keys equal to the prefix
-  for (int lo = 24; k > 0; lo -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int t = sinks + tid; t < hi; t += kEvThreads) {
-      const uint32_t o = weight_order(w[t]);
-      if ((o & pmask) == prefix) atomicAdd(&hist[(o >> lo) & 255], 1);
-    }
-    __syncthreads();
-    if (wave == 0) {
-      int c4[4], s = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s += c4[i] = hist[4 * lane + i];
-      const int incl = wave_incl_scan(s, lane);
-      int above = lane_value(incl, kWave - 1) - incl;
-      if (above < k && k <= above + s) {
-#pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          if (above < k && k <= above + c4[i]) {
-            bc[0] = 4 * lane + i;
-            bc[1] = above;
-          }
-          above += c4[i];
-        }
-      }
-    }
-    __syncthreads();
-    prefix |= (uint32_t)bc[0] << lo;
-    pmask |= 255u << lo;
-    k -= bc[1];
-    if (lo == 0) break;
-  }
-  // Kept: keys above the prefix, and the first k equal to it. (No places: the
-  // mask is empty, every key equals the prefix, and k = 0 of them are kept.)
-  const int per = ((hi - sinks + kEvWaves - 1) / kEvWaves + kWave - 1) & ~(kWave - 1);
-  const int w0 = min(sinks + wave * per, hi), w1 = min(w0 + per, hi);
-  int gt = 0, eq = 0;
-  for (int t = w0 + lane; t < w1; t += kWave) {
-    const uint32_t o = weight_order(w[t]) & pmask;
-    gt += o > prefix;
-    eq += o == prefix;
-  }
-  gt = wave_sum(gt);
-  eq = wave_sum(eq);
-  if (lane == 0) {
-    wcnt[wave][0] = gt;
-    wcnt[wave][1] = eq;
-  }
-  __syncthreads();
-  int pos = sinks, eqs = 0;
-  for (int v = 0; v < wave; ++v) {
-    pos += wcnt[v][0];
-    eqs += wcnt[v][1];
-  }
-  pos += min(eqs, k);
-  for (int base = w0; base < w1; base += kWave) {
-    const int t = base + lane;
-    const uint32_t o = t < w1 ? weight_order(w[t]) & pmask : 0u;
-    const bool is_eq = t < w1 && o == prefix;
-    const uint64_t em = __ballot(is_eq);
-    const int rank = eqs + __popcll(em & lanemask_below(lane));
-    const bool take = t < w1 && (o > prefix || (is_eq && rank < k));
-    const uint64_t tm = __ballot(take);
-    if (take) out[pos + __popcll(tm & lanemask_below(lane))] = t;
-    pos += __popcll(tm);
-    eqs += __popcll(em);
-  }
+  const int hi = L - recent, places = keep - sinks - recent;
   for (int i = tid; i < sinks; i += kEvThreads) out[i] = i;
   for (int i = tid; i < recent; i += kEvThreads) out[keep - recent + i] = hi + i;
+  if (places == 0) return;
+  const float* w = weights + (size_t)row * max_tokens;
+  if (hi - (sinks & ~3) <= kEvWaves * kRegSteps * kStep)
+    select_tokens<true>(w, sinks, hi, places, sinks, out, sh);
+  else
+    select_tokens<false>(w, sinks, hi, places, sinks, out, sh);
 }
 
 // ---------------------------------------------------------------------------
@@ -320,13 +503,16 @@ hipError_t launch_weights(const LaunchShape& s, const void* q, bool q_bf16, cons
   else
     for (int m = 1; m <= 4; ++m)
       if (1.0 / am1 - m < 1e-6 && m - 1.0 / am1 < 1e-6) pow = m;
-  const long long units = (long long)s.batch * s.num_kv_heads;
-  const long long tiles = ((long long)s.max_pages * s.page_size + (s.bf16 ? 31 : 15)) / (s.bf16 ? 32 : 16);
-  long long splits = (8 * kNumCUs + units - 1) / units;
-  if (splits > (tiles + 3) / 4) splits = (tiles + 3) / 4;
-  if (splits < 1) splits = 1;
-  a.splits = (int)splits;
-  const int items = (int)(units * splits);
+  // as many workgroups as the CUs hold at once (their LDS: two at 128 dims),
+  // each wave with a tile at least
+  const int row = s.head_dim * (s.bf16 ? 2 : 4), tt = s.bf16 ? kTile<true> : kTile<false>;
+  const long long lds = (long long)kWeightWaves * 2 * tt * row;
+  const long long most = ((long long)s.max_pages * s.page_size + tt - 1) / tt * s.batch;
+  long long wgs = ((long long)(kLdsPerCU / lds) * kNumCUs + s.num_kv_heads - 1) / s.num_kv_heads;
+  if (wgs > (most + kWeightWaves - 1) / kWeightWaves) wgs = (most + kWeightWaves - 1) / kWeightWaves;
+  a.batch = s.batch;
+  a.wgs = (int)wgs;
+  const int items = (int)(wgs * s.num_kv_heads);
   if (!s.bf16) return s.head_dim == 64 ? launch_w<false, 64, 3>(a, pow, items, st)
                                        : launch_w<false, 128, 3>(a, pow, items, st);
   if (q_bf16) return s.head_dim == 64 ? launch_w<true, 64, 1>(a, pow, items, st)

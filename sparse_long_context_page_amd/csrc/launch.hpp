@@ -283,7 +283,6 @@ hipError_t launch_tau_pv_f32(const LaunchShape& s, const SplitPlan& p, const voi
 // or one block of the many-rows form); a block's tokens are split over
 // `splits` workgroups (`pre_splits` over the prefix), whose parts are joined
 // by a second kernel when there is more than one per row.
-constexpr int kAttWgsPerCU = 2;     // workgroups a CU holds at the kernel's register use
 constexpr int kAttMaxSplits = 256;  // parts of a row block
 constexpr int kAttManyRows = 33;    // rows of a KV head from which the many-rows form runs
 struct AttendPlan {

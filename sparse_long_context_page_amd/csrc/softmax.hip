@@ -30,8 +30,6 @@ namespace ekv {
 namespace {
 
 constexpr float kSlack = 6.0f;
-constexpr int kAttWaves = 4;
-constexpr int kAttThreads = kAttWaves * kWave;
 
 struct AttendArgs {
   const void* q;
@@ -44,7 +42,7 @@ struct AttendArgs {
   float* lse;     // nullable
   float* part_o;  // [rows, slots, D]
   float* part_ml; // [rows, slots, 2]
-  int batch, H, Hkv, G, n, ps, max_pages, num_phys;
+  int batch, H, Hkv, g_bits, n, ps_bits, max_pages, num_phys;  // 2^g_bits heads a KV head
   int window, sinks;
   int prefix;                                  // tokens of the shared prefix (0: none)
   int pre_block, pre_splits, pre_items;        // rows per block and splits of the prefix part
@@ -73,7 +71,7 @@ __device__ __forceinline__ Block block_of(const AttendArgs& a, int item) {
     w.b = 0;
     w.split = x % a.pre_splits;
     w.r0 = x / a.pre_splits * a.pre_block;
-    w.nrows = min(a.pre_block, a.batch * a.G - w.r0);
+    w.nrows = min(a.pre_block, (a.batch << a.g_bits) - w.r0);
     w.splits = a.pre_splits;
     w.slot = w.split;
   } else {
@@ -81,7 +79,7 @@ __device__ __forceinline__ Block block_of(const AttendArgs& a, int item) {
     x /= a.splits;
     w.r0 = x % a.row_blocks * a.row_block;
     w.b = x / a.row_blocks;
-    w.nrows = min(a.row_block, a.n * a.G - w.r0);
+    w.nrows = min(a.row_block, (a.n << a.g_bits) - w.r0);
     w.splits = a.splits;
     w.slot = a.pre_items ? a.pre_splits + w.split : w.split;
   }
@@ -93,13 +91,13 @@ __device__ __forceinline__ Block block_of(const AttendArgs& a, int item) {
 __device__ __forceinline__ void row_of(const AttendArgs& a, const Block& w, int L, int r,
                                        int* row, int* lo, int* hi) {
   if (w.pre) {
-    const int b = r / a.G;
-    *row = b * a.H + w.g * a.G + (r - b * a.G);
+    const int b = r >> a.g_bits;
+    *row = b * a.H + (w.g << a.g_bits) + (r - (b << a.g_bits));
     *lo = 0;
-    *hi = min(clamp_len(a.seq_lens[b], a.max_pages * a.ps), a.prefix);
+    *hi = min(clamp_len(a.seq_lens[b], a.max_pages << a.ps_bits), a.prefix);
   } else {
-    const int i = r / a.G;
-    *row = (w.b * a.n + i) * a.H + w.g * a.G + (r - i * a.G);
+    const int i = r >> a.g_bits;
+    *row = (w.b * a.n + i) * a.H + (w.g << a.g_bits) + (r - (i << a.g_bits));
     const int pos = L - a.n + i;
     *hi = max(pos + 1, 0);
     *lo = max(max(pos - a.window + 1, a.prefix), 0);
@@ -112,7 +110,7 @@ struct Span {
   int lo, hi, flo, fhi;
 };
 __device__ __forceinline__ Span span_of(const AttendArgs& a, int L, int r0, int nrows) {
-  const int p0 = L - a.n + r0 / a.G, p1 = L - a.n + (r0 + nrows - 1) / a.G;
+  const int p0 = L - a.n + (r0 >> a.g_bits), p1 = L - a.n + ((r0 + nrows - 1) >> a.g_bits);
   Span s;
   s.lo = max(max(p0 - a.window + 1, a.prefix), 0);
   s.hi = max(p1 + 1, 0);
@@ -139,11 +137,11 @@ template <bool BF, int D>
 __device__ __forceinline__ Views views_of(const AttendArgs& a, const Block& w) {
   constexpr int kElem = BF ? 2 : 4;
   Views x;
-  const size_t head_off = (size_t)w.g * a.ps * D * kElem;
+  const size_t head_off = (size_t)((w.g << a.ps_bits) * D) * kElem;
   x.k.base = static_cast<const char*>(a.k_pool) + head_off;
   x.v.base = static_cast<const char*>(a.v_pool) + head_off;
-  x.k.page_bytes = x.v.page_bytes = (size_t)a.Hkv * a.ps * D * kElem;
-  x.k.page_size = x.v.page_size = a.ps;
+  x.k.page_bytes = x.v.page_bytes = (size_t)((a.Hkv << a.ps_bits) * D) * kElem;
+  x.k.page_size = x.v.page_size = 1 << a.ps_bits;
   x.table = w.pre ? a.prefix_table : a.block_table + (size_t)w.b * a.max_pages;
   return x;
 }
@@ -240,13 +238,13 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 // ---------------------------------------------------------------------------
 // Few rows
 
-template <bool BF, int D>
+template <int D, int NW>
 struct TokensLds {
-  float o[kAttWaves][16][D + 4];
-  float ml[kAttWaves][16][2];
+  float o[NW][16][D + 4];
+  float ml[NW][16][2];
 };
 
-template <bool BF, int D, int PARTS>
+template <bool BF, int D, int PARTS, int NW>
 __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& w, char* smem) {
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
@@ -254,13 +252,13 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
   constexpr int PP = PARTS == 3 ? 3 : 2;
   constexpr int QB = PARTS == 1 ? 2 : 4;
   constexpr int kAcc = VTile<BF, D>::kAcc;
-  TokensLds<BF, D>& sh = *reinterpret_cast<TokensLds<BF, D>*>(smem);
+  TokensLds<D, NW>& sh = *reinterpret_cast<TokensLds<D, NW>*>(smem);
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane >> 4, rl = lane & 15;
 
-  const int L = w.pre ? a.prefix : clamp_len(a.seq_lens[w.b], a.max_pages * a.ps);
+  const int L = w.pre ? a.prefix : clamp_len(a.seq_lens[w.b], a.max_pages << a.ps_bits);
   int lo = 0, hi = 0, row = 0;
   if (rl < w.nrows) row_of(a, w, L, w.r0 + rl, &row, &lo, &hi);
   const int sinks = a.sinks;
@@ -268,7 +266,7 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
   const TileSpan span = tile_span<TT>(u.lo, u.hi, sinks);
   const int per = (span.n + w.splits - 1) / w.splits;
   const int v0 = min(w.split * per, span.n), v1 = min(v0 + per, span.n);
-  const int npages = (u.hi + a.ps - 1) / a.ps;
+  const int npages = (u.hi + (1 << a.ps_bits) - 1) >> a.ps_bits;
   const Views x = views_of<BF, D>(a, w);
 
   QFrag<BF, D, PARTS> q;
@@ -279,21 +277,21 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
   for (int n = 0; n < kAcc; ++n) acc[n] = f32x4{0, 0, 0, 0};
   float m = kLowest<PARTS>, l = 0.0f;
 
-  for (int base = v0 + wave; base < v1; base += kAttWaves * kWave) {
+  for (int base = v0 + wave; base < v1; base += NW * kWave) {
     // pages of this wave's next 64 tiles, one tile per lane
-    const int nt = min(kWave, (v1 - base + kAttWaves - 1) / kAttWaves);
+    const int nt = min(kWave, (v1 - base + NW - 1) / NW);
     int pg0 = -1, pg1 = -1;
     if (lane < nt) {
-      const int j = span.tile(base + lane * kAttWaves) * TT / a.ps;
+      const int j = (span.tile(base + lane * NW) * TT) >> a.ps_bits;
       pg0 = pg1 = page_at(a, x.table, npages, j);
-      if (BF && a.ps == 16) pg1 = page_at(a, x.table, npages, j + 1);
+      if (BF && a.ps_bits == 4) pg1 = page_at(a, x.table, npages, j + 1);
     }
     KTile<BF, D> kt;
     VTile<BF, D> vt;
     auto pages = [&](int j) {
       return TilePages{__builtin_amdgcn_readlane(pg0, j), __builtin_amdgcn_readlane(pg1, j)};
     };
-    auto start = [&](int j) { return span.tile(base + j * kAttWaves) * TT; };
+    auto start = [&](int j) { return span.tile(base + j * NW) * TT; };
     TilePages pc = pages(0);
     int t0 = start(0);
     kt.template load<true>(x.k, pc, t0, lane);
@@ -372,16 +370,16 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
   }
   __syncthreads();
   constexpr int TPR = D / 4;  // threads per row, 4 coordinates each
-  for (int r = tid / TPR; r < w.nrows; r += kAttThreads / TPR) {
+  for (int r = tid / TPR; r < w.nrows; r += NW * kWave / TPR) {
     const int d = (tid % TPR) * 4;
     float M = -FLT_MAX;
 #pragma unroll
-    for (int v = 0; v < kAttWaves; ++v)
+    for (int v = 0; v < NW; ++v)
       if (!(sh.ml[v][r][1] == 0.0f)) M = fmaxf(M, sh.ml[v][r][0]);
     float ls = 0.0f;
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
-    for (int v = 0; v < kAttWaves; ++v) {
+    for (int v = 0; v < NW; ++v) {
       const float lv = sh.ml[v][r][1];
       if (lv == 0.0f) continue;
       const float f = exp2f((sh.ml[v][r][0] - M) * kLog2e);
@@ -412,10 +410,20 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
 template <bool BF, int PARTS>
 constexpr int kRowTiles = BF && PARTS == 1 ? 2 : 1;
 
-template <bool BF, int D>
+// Two groups of four waves: each group takes half of the workgroup's stages
+// for all of its rows, so a CU's eight waves finish a row block with one part
+// (four waves and twice the splits: 14 us more in the join of 32768 rows).
+constexpr int kRowWaves = 4;
+constexpr int kRowGroups = 2;
+
+template <bool BF, int D, int PARTS>
 struct RowsLds {
-  char st[2][2][Stage<BF, D>::kBytes];  // [buffer][K, V]
-  int ok[2][kAttWaves];                 // is that quarter of the stage in a physical page?
+  union {
+    char st[kRowGroups][2][2][Stage<BF, D>::kBytes];  // [group][buffer][K, V]
+    f32x4 o[kRowGroups - 1][kRowWaves][kRowTiles<BF, PARTS>][VTile<BF, D>::kAcc][kWave];
+  };
+  float ml[kRowGroups - 1][kRowWaves][kRowTiles<BF, PARTS>][16][2];
+  int ok[kRowGroups][2][kRowWaves];  // is that quarter of the stage in a physical page?
 };
 
 template <bool BF, int D, int PARTS>
@@ -431,14 +439,15 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   typedef Stage<BF, D> St;
   constexpr int ST = St::kTokens;
   constexpr int kChunk = 32;                          // stages between two looks at the table
-  constexpr int kLoads = St::kBytes / kAttWaves / 1024;  // of K a wave and stage, and of V
-  RowsLds<BF, D>& sh = *reinterpret_cast<RowsLds<BF, D>*>(smem);
+  constexpr int kLoads = St::kBytes / kRowWaves / 1024;  // of K a wave and stage, and of V
+  RowsLds<BF, D, PARTS>& sh = *reinterpret_cast<RowsLds<BF, D, PARTS>*>(smem);
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wave = wid % kRowWaves, grp = wid / kRowWaves;
   const int c = lane >> 4, rl = lane & 15;
 
-  const int L = w.pre ? a.prefix : clamp_len(a.seq_lens[w.b], a.max_pages * a.ps);
+  const int L = w.pre ? a.prefix : clamp_len(a.seq_lens[w.b], a.max_pages << a.ps_bits);
   const int sinks = a.sinks;
   const int wr = wave * (16 * RT);                      // first row of this wave in the block
   const int wrows = max(min(16 * RT, w.nrows - wr), 0);  // its rows
@@ -462,8 +471,11 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   if (!w.pre) all = span_of(a, L, w.r0, w.nrows);
   const TileSpan span = tile_span<ST>(all.lo, all.hi, sinks);
   const int per = (span.n + w.splits - 1) / w.splits;
-  const int v0 = min(w.split * per, span.n), v1 = min(v0 + per, span.n);
-  const int npages = (all.hi + a.ps - 1) / a.ps;
+  const int b0 = min(w.split * per, span.n), b1 = min(b0 + per, span.n);
+  // stages of this group, and steps that every group makes
+  const int steps = (b1 - b0 + kRowGroups - 1) / kRowGroups;
+  const int v0 = min(b0 + grp * steps, b1), mine = min(steps, b1 - v0);
+  const int npages = (all.hi + (1 << a.ps_bits) - 1) >> a.ps_bits;
   const Views x = views_of<BF, D>(a, w);
 
   // where this lane's 16 bytes of each direct load come from, past the row
@@ -473,7 +485,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   for (int i = 0; i < kLoads; ++i) {
     const int at = i * 1024 + lane * 16;
     const int r = at / St::kRow, slot = at % St::kRow / 16;
-    from[i] = r * St::kRow + ((slot ^ St::swizzle(wave * (ST / kAttWaves) + r)) << 4);
+    from[i] = r * St::kRow + ((slot ^ St::swizzle(wave * (ST / kRowWaves) + r)) << 4);
   }
 
   f32x4 acc[RT][kAcc];
@@ -486,19 +498,20 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
     l[t] = 0.0f;
   }
 
-  for (int base = v0; base < v1; base += kChunk) {
-    const int ns = min(kChunk, v1 - base);
+  for (int done = 0; done < steps; done += kChunk) {
+    const int base = v0 + done;
+    const int ns = min(kChunk, max(mine - done, 0)), nb = min(kChunk, steps - done);
     // page of this wave's quarter of each stage, one stage per lane
     int pg = -1;
     if (lane < ns)
       pg = page_at(a, x.table, npages,
-                   (span.tile(base + lane) * ST + wave * (ST / kAttWaves)) / a.ps);
+                   (span.tile(base + lane) * ST + wave * (ST / kRowWaves)) >> a.ps_bits);
     auto stage = [&](int j) {
       const int p = __builtin_amdgcn_readlane(pg, j);
-      const int t = span.tile(base + j) * ST + wave * (ST / kAttWaves);
+      const int t = span.tile(base + j) * ST + wave * (ST / kRowWaves);
       const size_t off =
-          (size_t)max(p, 0) * x.k.page_bytes + (size_t)(t & (a.ps - 1)) * St::kRow;
-      char* dst = sh.st[j & 1][0] + wave * (St::kBytes / kAttWaves);
+          (size_t)max(p, 0) * x.k.page_bytes + (size_t)(t & ((1 << a.ps_bits) - 1)) * St::kRow;
+      char* dst = sh.st[grp][j & 1][0] + wave * (St::kBytes / kRowWaves);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
         __builtin_amdgcn_global_load_lds(x.k.base + off + from[i], dst + i * 1024, 16, 0, 0);
@@ -506,23 +519,23 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
       for (int i = 0; i < kLoads; ++i)
         __builtin_amdgcn_global_load_lds(x.v.base + off + from[i], dst + St::kBytes + i * 1024, 16,
                                          0, 0);
-      if (lane == 0) sh.ok[j & 1][wave] = p >= 0;
+      if (lane == 0) sh.ok[grp][j & 1][wave] = p >= 0;
     };
-    stage(0);
+    if (ns > 0) stage(0);
     wait_vmcnt<0>();
     __syncthreads();
     uint64_t put_off = 0;  // two tiles a stage
-    for (int j = 0; j < ns; ++j) {
+    for (int j = 0; j < nb; ++j) {
       if (j + 1 < ns) stage(j + 1);
-      const int ts = span.tile(base + j) * ST;
-      const char* kst = sh.st[j & 1][0];
-      const char* vst = sh.st[j & 1][1];
+      const int ts = j < ns ? span.tile(base + j) * ST : INT32_MAX - ST;  // past every row
+      const char* kst = sh.st[grp][j & 1][0];
+      const char* vst = sh.st[grp][j & 1][1];
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
         const int t0 = ts + sub * TT;
         // a tile none of this wave's rows sees
         if (t0 >= u.hi || (t0 + TT <= u.lo && t0 >= sinks)) continue;
-        const bool ok0 = sh.ok[j & 1][2 * sub] != 0, ok1 = sh.ok[j & 1][2 * sub + 1] != 0;
+        const bool ok0 = sh.ok[grp][j & 1][2 * sub] != 0, ok1 = sh.ok[grp][j & 1][2 * sub + 1] != 0;
         const bool full = __builtin_amdgcn_readfirstlane(ok0 && ok1) &&
                           t0 + TT <= u.fhi && (t0 >= u.flo || t0 + TT <= sinks);
         const bool page_ok = c < 2 ? ok0 : ok1;
@@ -588,17 +601,48 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
       put_off &= put_off - 1;
       const int t0 = span.tile(base + j / 2) * ST + (j & 1) * TT;
       TilePages pp;
-      pp.p0 = pp.p1 = page_at(a, x.table, npages, t0 / a.ps);
-      if (BF && a.ps == 16) pp.p1 = page_at(a, x.table, npages, t0 / a.ps + 1);
+      pp.p0 = pp.p1 = page_at(a, x.table, npages, t0 >> a.ps_bits);
+      if (BF && a.ps_bits == 4) pp.p1 = page_at(a, x.table, npages, (t0 >> a.ps_bits) + 1);
 #pragma unroll
       for (int t = 0; t < RT; ++t)
         late_tile<BF, D, PARTS, PP>(x, pp, t0, lane, q[t], lo[t], hi[t], sinks, m[t], acc[t]);
     }
   }
 
+  // join the groups: the others leave their parts in LDS, lane by lane (every
+  // stage has been read: the loop ends with a barrier)
+#pragma unroll
+  for (int t = 0; t < RT; ++t) l[t] = group_sum(l[t]);
+  if (grp > 0) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+#pragma unroll
+      for (int n = 0; n < kAcc; ++n) sh.o[grp - 1][wave][t][n][lane] = acc[t][n];
+      if (c == 0) {
+        sh.ml[grp - 1][wave][t][rl][0] = m[t];
+        sh.ml[grp - 1][wave][t][rl][1] = l[t];
+      }
+    }
+  }
+  __syncthreads();
+  if (grp > 0) return;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const float ls = group_sum(l[t]);
+#pragma unroll
+    for (int e = 0; e < kRowGroups - 1; ++e) {
+      const float me = sh.ml[e][wave][t][rl][0], le = sh.ml[e][wave][t][rl][1];
+      const float mn = le == 0.0f ? m[t] : l[t] == 0.0f ? me : fmaxf(m[t], me);
+      const float f = l[t] == 0.0f ? 0.0f : exp2f((m[t] - mn) * kLog2e);
+      const float fe = le == 0.0f ? 0.0f : exp2f((me - mn) * kLog2e);
+      l[t] = f * l[t] + fe * le;
+#pragma unroll
+      for (int n = 0; n < kAcc; ++n) acc[t][n] = f * acc[t][n] + fe * sh.o[e][wave][t][n][lane];
+      m[t] = mn;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const float ls = l[t];
     if (t * 16 + rl >= wrows) continue;
     if (a.slots > 1) {
       const size_t part = (size_t)row[t] * a.slots + w.slot;
@@ -626,8 +670,12 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   }
 }
 
+// Waves of a workgroup: eight where the many-rows form is among the parts,
+// else four.
+constexpr int att_waves(bool rows) { return rows ? kRowWaves * kRowGroups : 4; }
+
 template <bool BF, int D, int PARTS, bool ROWS>
-__global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(att_waves(ROWS) * kWave, 2) void attend_kernel(AttendArgs a) {
   extern __shared__ __align__(16) char smem[];
   const Block w = block_of(a, blockIdx.x);
   if constexpr (ROWS) {
@@ -636,7 +684,7 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(AttendArgs a) {
       return;
     }
   }
-  attend_tokens<BF, D, PARTS>(a, w, smem);
+  attend_tokens<BF, D, PARTS, att_waves(ROWS)>(a, w, smem);
 }
 
 // Joins the parts of each row. D/4 threads hold 4 coordinates each of a row's
@@ -734,16 +782,18 @@ hipError_t raise_lds(const void* kernel, size_t bytes, std::atomic<uint64_t>& do
 
 template <bool BF, int D, int PARTS>
 hipError_t launch(const AttendArgs& a, long long items, hipStream_t st) {
-  constexpr size_t few = sizeof(TokensLds<BF, D>), many = sizeof(RowsLds<BF, D>);
   if (a.pre_rows || a.own_rows) {
     auto* f = attend_kernel<BF, D, PARTS, true>;
+    constexpr size_t few = sizeof(TokensLds<D, att_waves(true)>);
+    constexpr size_t many = sizeof(RowsLds<BF, D, PARTS>);
     constexpr size_t lds = few > many ? few : many;
     static std::atomic<uint64_t> raised{0};  // devices whose kernel has the limit
     if (hipError_t e = raise_lds(reinterpret_cast<const void*>(f), lds, raised)) return e;
-    hipLaunchKernelGGL(f, dim3((unsigned)items), dim3(kAttThreads), lds, st, a);
+    hipLaunchKernelGGL(f, dim3((unsigned)items), dim3(att_waves(true) * kWave), lds, st, a);
   } else {
     hipLaunchKernelGGL((attend_kernel<BF, D, PARTS, false>), dim3((unsigned)items),
-                       dim3(kAttThreads), few, st, a);
+                       dim3(att_waves(false) * kWave), sizeof(TokensLds<D, att_waves(false)>), st,
+                       a);
   }
   return hipGetLastError();
 }
@@ -782,11 +832,14 @@ AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int
   const int TT = s.bf16 ? kTile<true> : kTile<false>;
   const long long total = (long long)s.max_pages * s.page_size;
   const long long prefix = (long long)prefix_pages * s.page_size;
-  const int many = kAttWaves * 16 * (s.bf16 && q_bf16 ? kRowTiles<true, 1> : kRowTiles<true, 3>);
-  const long long want = (long long)kAttWgsPerCU * kNumCUs;
+  const int many = kRowWaves * 16 * (s.bf16 && q_bf16 ? kRowTiles<true, 1> : kRowTiles<true, 3>);
   p.rows = (long long)s.batch * n * s.num_q_heads;
   const int own = n * s.group, pre = s.batch * s.group;
   p.own_rows = own >= kAttManyRows;
+  p.pre_rows = prefix_pages > 0 && pre >= kAttManyRows;
+  // eight waves a CU, four or eight a workgroup
+  const int waves = att_waves(p.own_rows || p.pre_rows);
+  const long long want = (long long)8 / waves * kNumCUs;
   p.row_block = p.own_rows ? many : 16;
   p.row_blocks = (own + p.row_block - 1) / p.row_block;
   // tokens a row block of the sequences' own part can see
@@ -794,18 +847,17 @@ AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int
   const long long seen = total - prefix < span ? total - prefix : span;
   const long long tiles = (seen + TT - 1) / TT + 1 + (sinks + TT - 1) / TT;
   const long long blocks = (long long)s.batch * s.num_kv_heads * p.row_blocks;
-  // a workgroup's tokens: at least one tile a wave, or four stages
-  const int least = p.own_rows ? 8 : kAttWaves;
+  // a workgroup's tokens: at least one tile a wave, or two stages a group
+  const int few = waves, many_tiles = 4 * kRowGroups;
   if (prefix_pages > 0) {
-    p.pre_rows = pre >= kAttManyRows;
     p.pre_block = p.pre_rows ? many : 16;
     const long long pre_blocks =
         (long long)s.num_kv_heads * ((pre + p.pre_block - 1) / p.pre_block);
     p.pre_splits = splits_for(pre_blocks, (prefix + TT - 1) / TT, want,
-                              p.pre_rows ? 8 : kAttWaves);
+                              p.pre_rows ? many_tiles : few);
     p.pre_items = pre_blocks * p.pre_splits;
   }
-  p.splits = total > prefix ? splits_for(blocks, tiles, want, least) : 0;
+  p.splits = total > prefix ? splits_for(blocks, tiles, want, p.own_rows ? many_tiles : few) : 0;
   p.items = p.pre_items + blocks * p.splits;
   p.slots = p.pre_splits + p.splits;
   if (p.slots > 1) {
@@ -835,9 +887,9 @@ hipError_t launch_attend(const LaunchShape& s, const AttendPlan& p, const void* 
   a.batch = s.batch;
   a.H = s.num_q_heads;
   a.Hkv = s.num_kv_heads;
-  a.G = s.group;
+  a.g_bits = __builtin_ctz(s.group);
   a.n = n;
-  a.ps = s.page_size;
+  a.ps_bits = __builtin_ctz(s.page_size);
   a.max_pages = s.max_pages;
   a.num_phys = s.num_phys;
   a.window = window;

@@ -112,6 +112,32 @@ struct Stage {
   }
 };
 
+// One K tile streamed into LDS by one wave for itself, whole rows at a time
+// (a score operand loaded straight from memory touches 64 bytes of 16 rows at
+// once: 5.0 TB/s against 6.x for whole rows). Same layout as a stage.
+template <bool BF, int D>
+struct WaveTile {
+  static constexpr int kBytes = Stage<BF, D>::kBytes / 2;
+  static constexpr int kLoads = kBytes / 1024;
+  static constexpr int kRow = Stage<BF, D>::kRow;
+  int from[kLoads];  // this lane's source past the tile's first row, per load
+  int row[kLoads];   // and its row (uniform over kRow / 16 lanes)
+  __device__ __forceinline__ void init(int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = i * 1024 + lane * 16;
+      row[i] = at / kRow;
+      from[i] = ((at % kRow / 16) ^ Stage<BF, D>::swizzle(row[i])) << 4;
+    }
+  }
+  __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0,
+                                       char* dst) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      lds_load16(row_ptr<BF, D>(v, p, t0, row[i]) + from[i], dst + i * 1024);
+  }
+};
+
 // ---------------------------------------------------------------------------
 // Query rows as the B operand
 

@@ -73,6 +73,7 @@ def test_weights_refusals(ek, kw, code):
     (dict(sinks=2**31 - 1, recent=2**31 - 1), INVALID), (dict(w=None), INVALID),
     (dict(new_table=None), INVALID), (dict(new_table=D), INVALID), (dict(kept=None), INVALID),
     (dict(new_lens=None), INVALID), (dict(new_lens=D), INVALID), (dict(new_w=D), INVALID),
+    (dict(w=ctypes.c_void_p(260)), INVALID),
     (dict(k=ctypes.c_void_p(264)), INVALID),
 ])
 def test_evict_refusals(ek, kw, code):
