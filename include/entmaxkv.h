@@ -438,7 +438,7 @@ int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int3
  * may not overlap the inputs they replace (the same pointer is
  * ENTMAXKV_ERR_INVALID). Page boxes and moments of the new pages are built by
  * entmaxkv_build_page_meta / _moments with new_table and new_lens. Kernels
- * launched: 2 (selection, copy).
+ * launched: 1.
  */
 int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
                    const int32_t* block_table, const int32_t* seq_lens, const float* weights,

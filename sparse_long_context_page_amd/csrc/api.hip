@@ -754,11 +754,7 @@ int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
   if (rc) return rc;
   if (keep <= 0 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
     return ENTMAXKV_ERR_INVALID;
-  const long long max_tokens = (long long)s.max_pages * s.page_size;
   if (keep > kMaxWindow) return ENTMAXKV_ERR_UNSUPPORTED;
-  // at most one workgroup per 64 tokens of a (sequence, KV head)
-  if ((long long)s.batch * s.num_kv_heads * (max_tokens / 64 + 2) > 0x7fffffffLL)
-    return ENTMAXKV_ERR_UNSUPPORTED;
   if (!k_pool || !v_pool || !block_table || !seq_lens || !weights || !new_table || !kept ||
       !new_lens)
     return ENTMAXKV_ERR_INVALID;
@@ -769,14 +765,10 @@ int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
     return ENTMAXKV_ERR_INVALID;
   const Events ev{events, stream};
   if (!ev.before(0)) return ENTMAXKV_ERR_HIP;
-  if (launch_evict_select(s, seq_lens, weights, keep, sinks, recent, kept, new_lens, stream) !=
-      hipSuccess)
+  if (launch_evict(s, k_pool, v_pool, block_table, seq_lens, weights, keep, sinks, recent,
+                   new_table, kept, new_lens, new_weights, stream) != hipSuccess)
     return ENTMAXKV_ERR_HIP;
-  if (!ev.after(0) || !ev.before(1)) return ENTMAXKV_ERR_HIP;
-  if (launch_evict_copy(s, k_pool, v_pool, block_table, seq_lens, weights, keep, new_table, kept,
-                        new_weights, stream) != hipSuccess)
-    return ENTMAXKV_ERR_HIP;
-  if (!ev.after(1)) return ENTMAXKV_ERR_HIP;
+  if (!ev.after(0)) return ENTMAXKV_ERR_HIP;
   return ENTMAXKV_OK;
 }
 

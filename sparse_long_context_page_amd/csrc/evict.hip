@@ -172,14 +172,21 @@ __global__ __launch_bounds__(kWeightWaves* kWave) void weights_kernel(WeightArgs
 }
 
 // ---------------------------------------------------------------------------
-// Selection: one workgroup per (sequence, KV head). A radix select over the
-// order-preserving image of the weights finds the smallest kept one: digits of
-// kDigit bits from the highest bit in which the keys differ (so that the first
-// histogram is spread and its LDS atomics seldom meet), until the boundary
-// digit is taken whole. Wave v holds the v-th stretch of the row, four
-// neighbouring tokens a lane and step, in registers where it has at most
-// kRegSteps steps (32768 tokens a row), else it reads it again for each pass;
-// the kept tokens are written in order behind those of the waves before.
+// Eviction, one kernel: `splits` workgroups per (sequence, KV head) each find
+// the row's kept tokens, list those of their own share of the slots and copy
+// these. (Finding them again costs reads that the L2 serves; handing a list
+// from one kernel to the next cost a launch and left most CUs idle meanwhile:
+// 15.7 -> xx us for 1001 of 4001 tokens, 134 -> xx us for 8 sequences.)
+//
+// The smallest kept weight comes from a radix select over the
+// order-preserving image of the weights, less its least value: digits of
+// kDigit bits from the range's highest bit (so that the first histogram is
+// spread and its LDS atomics seldom meet), until the boundary digit is taken whole or
+// holds so few keys that each can be ranked among them. Wave v holds the v-th
+// stretch of the row, four neighbouring tokens a lane and step, in registers
+// where it has at most kRegSteps steps (32768 tokens a row), else it reads it
+// again for each pass. The copy is bound by memory: kept rows of K and V read
+// and written once.
 
 constexpr int kEvThreads = 1024;
 constexpr int kEvWaves = kEvThreads / kWave;
@@ -187,9 +194,15 @@ constexpr int kDigit = 11;
 constexpr int kBins = 1 << kDigit;
 constexpr int kRegSteps = 8;   // steps of 4 * kWave tokens that a wave keeps in registers
 constexpr int kStep = 4 * kWave;
+constexpr int kFew = 256;      // boundary keys ranked one against the other
 
 __device__ __forceinline__ uint32_t weight_order(float w) {
   return w != w ? 0xffffffffu : float_order(w + 0.0f);  // a NaN counts as the largest
+}
+
+// Set bits of m below this lane's.
+__device__ __forceinline__ int lanes_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
 }
 
 // Bins lie with a gap after every 32: a lane sums kPerLane neighbours, on
@@ -199,31 +212,36 @@ __host__ __device__ constexpr int bin_at(int b) { return b + b / kPerLane; }
 
 struct EvictLds {
   int hist[bin_at(kBins)];
+  __align__(16) uint32_t few[kFew];
+  int nfew;
   uint32_t range[kEvWaves][2];
   int wcnt[kEvWaves][2];
-  int bc[3];
+  uint32_t bc[3];
 };
 
-// kRegs: the row fits the registers.
-template <bool kRegs>
+// Calls keep_at(position among the kept, token) for the k heaviest of the
+// tokens [lo, hi) (at least k + 1 of them), in token order per wave; positions
+// count from pos. kRegs: the row fits the registers.
+template <bool kRegs, typename Emit>
 __device__ __forceinline__ void select_tokens(const float* __restrict__ w, int lo, int hi, int k,
-                                              int pos, int32_t* __restrict__ out, EvictLds& sh) {
+                                              int pos, EvictLds& sh, Emit keep_at) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   // stretches of whole steps, from the step that holds token lo
   const int first = lo & ~3;
   const int per = ((hi - first + kEvWaves * kStep - 1) / (kEvWaves * kStep)) * kStep;
   const int w0 = min(first + wave * per, hi), w1 = min(w0 + per, hi);
   const int steps = (w1 - w0 + kStep - 1) / kStep;
-  // order keys of the lane's four tokens of step i; 0 (below every key) for
-  // tokens that do not compete
+  // keys of the lane's four tokens of step i: order keys less `low` (from 1
+  // up), 0 for tokens that do not compete
+  uint32_t low = 0;
   const auto load = [&](int i) -> uint4 {
     const int t = w0 + i * kStep + lane * 4;
     if (t >= w1) return make_uint4(0, 0, 0, 0);
     const float4 f = *reinterpret_cast<const float4*>(w + t);
-    return make_uint4(t >= lo ? weight_order(f.x) : 0u,
-                      t + 1 >= lo && t + 1 < w1 ? weight_order(f.y) : 0u,
-                      t + 2 >= lo && t + 2 < w1 ? weight_order(f.z) : 0u,
-                      t + 3 >= lo && t + 3 < w1 ? weight_order(f.w) : 0u);
+    return make_uint4(t >= lo ? weight_order(f.x) - low : 0u,
+                      t + 1 >= lo && t + 1 < w1 ? weight_order(f.y) - low : 0u,
+                      t + 2 >= lo && t + 2 < w1 ? weight_order(f.z) - low : 0u,
+                      t + 3 >= lo && t + 3 < w1 ? weight_order(f.w) - low : 0u);
   };
   uint4 reg[kRegs ? kRegSteps : 1];
   if constexpr (kRegs) {
@@ -234,6 +252,7 @@ __device__ __forceinline__ void select_tokens(const float* __restrict__ w, int l
     if constexpr (kRegs) {
 #pragma unroll
       for (int i = 0; i < kRegSteps; ++i) {
+        if (i * kStep >= per) break;  // the same in every wave
         f(reg[i].x);
         f(reg[i].y);
         f(reg[i].z);
@@ -269,15 +288,31 @@ __device__ __forceinline__ void select_tokens(const float* __restrict__ w, int l
     sh.range[wave][1] = mx;
   }
   for (int i = tid; i < bin_at(kBins); i += kEvThreads) sh.hist[i] = 0;
+  if (tid == 0) sh.nfew = 0;
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < kEvWaves; ++v) {
     mn = min(mn, sh.range[v][0]);
     mx = max(mx, sh.range[v][1]);
   }
-  ++mn;  // (there is a key: the row is longer than what is kept)
+  // keys from 1 up: the digits then start at the range's own highest bit, not
+  // at one that an exponent crosses (weights between 1e-3 and 10: 128 bins a
+  // binade, not 8; 8.7 -> 3 us of LDS atomics for 32768 keys)
+  low = mn;  // (one less than the least key: the row is longer than what is kept)
+  mx -= low;
+  mn = 1;
+  if constexpr (kRegs) {
+#pragma unroll
+    for (int i = 0; i < kRegSteps; ++i) {
+      reg[i].x -= reg[i].x ? low : 0u;
+      reg[i].y -= reg[i].y ? low : 0u;
+      reg[i].z -= reg[i].z ? low : 0u;
+      reg[i].w -= reg[i].w ? low : 0u;
+    }
+  }
   // the boundary: keys above `prefix` (under the mask) and k equal ones stay
   uint32_t prefix = mx, pmask = 0xffffffffu;
+  bool whole = false;  // every equal key stays
   if (mn != mx) {
     int hb = 31 - __clz(mn ^ mx);
     pmask = ~((2u << hb) - 1u);
@@ -286,7 +321,8 @@ __device__ __forceinline__ void select_tokens(const float* __restrict__ w, int l
       const int sh0 = hb >= kDigit - 1 ? hb - (kDigit - 1) : 0;
       const uint32_t dmask = (2u << (hb - sh0)) - 1u;
       each([&](uint32_t o) {
-        if (o != 0u && (o & pmask) == prefix) atomicAdd(&sh.hist[bin_at((o >> sh0) & dmask)], 1);
+        if (o != 0u && (o & pmask) == prefix)
+          atomicAdd(&sh.hist[bin_at((o >> sh0) & dmask)], 1);
       });
       __syncthreads();
       if (wave == 0) {
@@ -309,10 +345,39 @@ __device__ __forceinline__ void select_tokens(const float* __restrict__ w, int l
         }
       }
       __syncthreads();
-      prefix |= (uint32_t)sh.bc[0] << sh0;
+      const int cnt = sh.bc[2];
+      prefix |= sh.bc[0] << sh0;
       pmask |= dmask << sh0;
-      k -= sh.bc[1];
-      if (sh.bc[2] == k || sh0 == 0) break;
+      k -= (int)sh.bc[1];
+      whole = cnt == k;
+      if (whole || sh0 == 0) break;
+      if (cnt <= kFew) {
+        // the boundary digit's keys, ranked by counting
+        each([&](uint32_t o) {
+          if (o != 0u && (o & pmask) == prefix) sh.few[atomicAdd(&sh.nfew, 1)] = o;
+        });
+        __syncthreads();
+        if (tid < cnt) {
+          const uint32_t o = sh.few[tid];
+          int more = 0, same = 0;
+#pragma unroll 4
+          for (int i = 0; i < cnt; ++i) {
+            more += sh.few[i] > o;
+            same += sh.few[i] == o;
+          }
+          if (more < k && k <= more + same) {  // one value, maybe of several threads
+            sh.bc[0] = o;
+            sh.bc[1] = more;
+            sh.bc[2] = same;
+          }
+        }
+        __syncthreads();
+        prefix = sh.bc[0];
+        pmask = 0xffffffffu;
+        k -= (int)sh.bc[1];
+        whole = (int)sh.bc[2] == k;
+        break;
+      }
       hb = sh0 - 1;
       for (int i = tid; i < bin_at(kBins); i += kEvThreads) sh.hist[i] = 0;
       __syncthreads();
@@ -342,28 +407,36 @@ __device__ __forceinline__ void select_tokens(const float* __restrict__ w, int l
   const auto emit = [&](int i, const uint4& o) {
     const int t = w0 + i * kStep + lane * 4;
     const uint32_t k4[4] = {o.x, o.y, o.z, o.w};
-    int e = 0;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) e += k4[r] != 0u && (k4[r] & pmask) == prefix;
-    const int eincl = wave_incl_scan(e, lane);
-    int rank = eqs + eincl - e;  // equal keys before this lane's
     bool take[4];
-    int n = 0;
+    if (whole) {  // no ranks among equals
+#pragma unroll
+      for (int r = 0; r < 4; ++r) take[r] = k4[r] != 0u && (k4[r] & pmask) >= prefix;
+    } else {
+      int e = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) e += k4[r] != 0u && (k4[r] & pmask) == prefix;
+      const int eincl = wave_incl_scan(e, lane);
+      int rank = eqs + eincl - e;  // equal keys before this lane's
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t x = k4[r] & pmask;
+        const bool is = k4[r] != 0u && x == prefix;
+        take[r] = x > prefix || (is && rank < k);
+        rank += is;
+      }
+      eqs += lane_value(eincl, kWave - 1);
+    }
+    int at = pos, n = 0;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint32_t x = k4[r] & pmask;
-      const bool is = k4[r] != 0u && x == prefix;
-      take[r] = x > prefix || (is && rank < k);
-      rank += is;
-      n += take[r];
+      const uint64_t m = __ballot(take[r]);
+      at += lanes_below(m);
+      n += __popcll(m);
     }
-    const int nincl = wave_incl_scan(n, lane);
-    int at = pos + nincl - n;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (take[r]) out[at++] = t + r;
-    pos += lane_value(nincl, kWave - 1);
-    eqs += lane_value(eincl, kWave - 1);
+      if (take[r]) keep_at(at++, t + r);
+    pos += n;
   };
   if constexpr (kRegs) {
 #pragma unroll
@@ -379,79 +452,96 @@ __device__ __forceinline__ void select_tokens(const float* __restrict__ w, int l
   }
 }
 
-__global__ __launch_bounds__(kEvThreads) void evict_select_kernel(
-    const int32_t* __restrict__ lens, const float* __restrict__ weights, int Hkv, int max_tokens,
-    int keep, int sinks, int recent, int32_t* __restrict__ kept, int32_t* __restrict__ new_lens) {
+struct EvictArgs {
+  char* k_pool;
+  char* v_pool;
+  const int32_t* bt;
+  const int32_t* lens;
+  const float* weights;
+  const int32_t* new_table;
+  int32_t* kept;
+  int32_t* new_lens;
+  float* new_weights;  // nullable
+  int Hkv, ps_bits, max_pages, num_phys;
+  int keep, sinks, recent, rows;
+};
+
+template <int ROW>  // bytes of a row
+__global__ __launch_bounds__(kEvThreads) void evict_kernel(EvictArgs a, int splits) {
   __shared__ EvictLds sh;
   const int tid = threadIdx.x;
-  const int row = blockIdx.x, b = row / Hkv;
-  const int L = clamp_len(lens[b], max_tokens);
-  const int n = min(L, keep);
-  int32_t* out = kept + (size_t)row * keep;
-  if (row % Hkv == 0 && tid == 0) new_lens[b] = n;
-  for (int i = n + tid; i < keep; i += kEvThreads) out[i] = -1;
-  if (L <= keep) {
-    for (int i = tid; i < n; i += kEvThreads) out[i] = i;
-    return;
-  }
-  // tokens [sinks, hi) compete for keep - sinks - recent places
-  const int hi = L - recent, places = keep - sinks - recent;
-  for (int i = tid; i < sinks; i += kEvThreads) out[i] = i;
-  for (int i = tid; i < recent; i += kEvThreads) out[keep - recent + i] = hi + i;
-  if (places == 0) return;
-  const float* w = weights + (size_t)row * max_tokens;
-  if (hi - (sinks & ~3) <= kEvWaves * kRegSteps * kStep)
-    select_tokens<true>(w, sinks, hi, places, sinks, out, sh);
-  else
-    select_tokens<false>(w, sinks, hi, places, sinks, out, sh);
-}
-
-// ---------------------------------------------------------------------------
-// Copy: kept rows of K and V to the new pages (row_bytes / 16 lanes a row),
-// and the weights: the kept ones in slot order, 0 behind them. Workgroups
-// below `chunks` of a (sequence, KV head) take kCopyRows slots each, those
-// behind clear kClearTokens weights each.
-
-constexpr int kCopyRows = 64;
-constexpr int kClearTokens = 4096;
-
-__global__ __launch_bounds__(256) void evict_copy_kernel(
-    char* k_pool, char* v_pool, const int32_t* __restrict__ bt,
-    const int32_t* __restrict__ lens, const float* __restrict__ weights,
-    const int32_t* __restrict__ new_table, const int32_t* __restrict__ kept, int Hkv, int ps,
-    int row_bytes, int max_pages, int num_phys, int keep, int chunks, int clears,
-    float* __restrict__ new_weights) {
-  const int row = blockIdx.x / (chunks + clears), chunk = blockIdx.x % (chunks + clears);
-  const int b = row / Hkv, g = row % Hkv;
-  const int max_tokens = max_pages * ps;
+  const int row = blockIdx.x % a.rows, split = blockIdx.x / a.rows;
+  const int b = row / a.Hkv, g = row - b * a.Hkv;
+  const int max_tokens = a.max_pages << a.ps_bits;
+  const int L = clamp_len(a.lens[b], max_tokens);
+  const int n = min(L, a.keep);
+  int32_t* kept = a.kept + (size_t)row * a.keep;
+  if (g == 0 && split == 0 && tid == 0) a.new_lens[b] = n;
+  // this workgroup's share of the slots, of the list behind them and of the
+  // weights that end as 0
+  const int per = (n + splits - 1) / splits;
+  const int s0 = min(split * per, n), s1 = min(s0 + per, n);
+  for (int i = n + split * kEvThreads + tid; i < a.keep; i += splits * kEvThreads) kept[i] = -1;
   const size_t wrow = (size_t)row * max_tokens;
-  if (chunk >= chunks) {
-    const int t0 = keep + (chunk - chunks) * kClearTokens;
-    const int end = min(t0 + kClearTokens, max_tokens);
-    for (int t = t0 + threadIdx.x; t < end; t += 256) new_weights[wrow + t] = 0.0f;
-    return;
+  if (a.new_weights)
+    for (int i = n + split * kEvThreads + tid; i < max_tokens; i += splits * kEvThreads)
+      a.new_weights[wrow + i] = 0.0f;
+  if (s0 == s1) return;
+
+  if (L <= a.keep) {
+    for (int i = s0 + tid; i < s1; i += kEvThreads) kept[i] = i;
+  } else {
+    // tokens [sinks, hi) compete for the places between
+    const int hi = L - a.recent, end = a.keep - a.recent, places = end - a.sinks;
+    for (int i = s0 + tid; i < min(s1, a.sinks); i += kEvThreads) kept[i] = i;
+    for (int i = max(s0, end) + tid; i < s1; i += kEvThreads) kept[i] = hi + (i - end);
+    if (places > 0 && s0 < end && s1 > a.sinks) {
+      const float* w = a.weights + wrow;
+      const auto keep_at = [&](int at, int t) {
+        if (at >= s0 && at < s1) kept[at] = t;
+      };
+      if (hi - (a.sinks & ~3) <= kEvWaves * kRegSteps * kStep)
+        select_tokens<true>(w, a.sinks, hi, places, a.sinks, sh, keep_at);
+      else
+        select_tokens<false>(w, a.sinks, hi, places, a.sinks, sh, keep_at);
+    }
   }
-  const int n = min(clamp_len(lens[b], max_tokens), keep);
-  const int lanes = row_bytes / 16;
-  const int off = (threadIdx.x % lanes) * 16;
-  const size_t head = (size_t)g * ps * row_bytes, page = (size_t)Hkv * ps * row_bytes;
-  const int32_t* list = kept + (size_t)row * keep;
-  const int i0 = chunk * kCopyRows, end = min(n, i0 + kCopyRows);
-  if (new_weights && threadIdx.x < kCopyRows) {
-    const int i = i0 + threadIdx.x;
-    if (i < min(keep, max_tokens)) new_weights[wrow + i] = i < n ? weights[wrow + list[i]] : 0.0f;
-  }
-  for (int i = i0 + threadIdx.x / lanes; i < end; i += 256 / lanes) {
-    const int t = list[i];
-    const int po = bt[(size_t)b * max_pages + t / ps];
-    const int pn = new_table[(size_t)b * max_pages + i / ps];
-    if (po < 0 || po >= num_phys || pn < 0 || pn >= num_phys) continue;
-    const size_t src = po * page + head + (size_t)(t % ps) * row_bytes + off;
-    const size_t dst = pn * page + head + (size_t)(i % ps) * row_bytes + off;
-    const uint4 kx = *reinterpret_cast<const uint4*>(k_pool + src);
-    const uint4 vx = *reinterpret_cast<const uint4*>(v_pool + src);
-    *reinterpret_cast<uint4*>(k_pool + dst) = kx;
-    *reinterpret_cast<uint4*>(v_pool + dst) = vx;
+  __syncthreads();  // the share's list is written
+
+  if (a.new_weights)
+    for (int i = s0 + tid; i < s1; i += kEvThreads)
+      a.new_weights[wrow + i] = a.weights[wrow + kept[i]];
+  constexpr int kLanes = ROW / 16;            // a row's lanes, 16 bytes each
+  constexpr int kRows = kEvThreads / kLanes;  // rows at a time
+  constexpr int U = 4;                        // of them a thread holds
+  const int off = tid % kLanes * 16;
+  const size_t page = ((size_t)a.Hkv << a.ps_bits) * ROW, head = ((size_t)g << a.ps_bits) * ROW;
+  const int32_t* bt = a.bt + (size_t)b * a.max_pages;
+  const int32_t* nt = a.new_table + (size_t)b * a.max_pages;
+  const int rmask = (1 << a.ps_bits) - 1;
+  for (int i0 = s0 + tid / kLanes; i0 < s1; i0 += U * kRows) {
+    u32x4 kx[U], vx[U];
+    int po[U], pn[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const int i = min(i0 + e * kRows, s1 - 1);
+      const int t = kept[i];
+      po[e] = bt[t >> a.ps_bits];
+      pn[e] = i0 + e * kRows < s1 ? nt[i >> a.ps_bits] : -1;
+      // (page 0 is read in the place of one that is not there)
+      const bool there = po[e] >= 0 && po[e] < a.num_phys;
+      const size_t src = (there ? (size_t)po[e] : 0) * page + head + (size_t)(t & rmask) * ROW + off;
+      if (!there || pn[e] >= a.num_phys) pn[e] = -1;
+      kx[e] = load_vec<true, u32x4>(a.k_pool + src);
+      vx[e] = load_vec<true, u32x4>(a.v_pool + src);
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      if (pn[e] < 0) continue;
+      const size_t dst = (size_t)pn[e] * page + head + (size_t)((i0 + e * kRows) & rmask) * ROW + off;
+      __builtin_nontemporal_store(kx[e], reinterpret_cast<u32x4*>(a.k_pool + dst));
+      __builtin_nontemporal_store(vx[e], reinterpret_cast<u32x4*>(a.v_pool + dst));
+    }
   }
 }
 
@@ -521,29 +611,38 @@ hipError_t launch_weights(const LaunchShape& s, const void* q, bool q_bf16, cons
                           : launch_w<true, 128, 3>(a, pow, items, st);
 }
 
-hipError_t launch_evict_select(const LaunchShape& s, const int32_t* lens, const float* weights,
-                               int keep, int sinks, int recent, int32_t* kept,
-                               int32_t* new_lens, hipStream_t st) {
-  hipLaunchKernelGGL(evict_select_kernel, dim3((unsigned)(s.batch * s.num_kv_heads)),
-                     dim3(kEvThreads), 0, st, lens, weights, s.num_kv_heads,
-                     s.max_pages * s.page_size, keep, sinks, recent, kept, new_lens);
-  return hipGetLastError();
-}
-
-hipError_t launch_evict_copy(const LaunchShape& s, void* k_pool, void* v_pool, const int32_t* bt,
-                             const int32_t* lens, const float* weights, int keep,
-                             const int32_t* new_table, const int32_t* kept, float* new_weights,
-                             hipStream_t st) {
-  const int row_bytes = s.head_dim * (s.bf16 ? 2 : 4);
-  const int max_tokens = s.max_pages * s.page_size;
-  const int slots = keep < max_tokens ? keep : max_tokens;
-  const int chunks = (slots + kCopyRows - 1) / kCopyRows;
-  const int clears = new_weights ? (max_tokens - slots + kClearTokens - 1) / kClearTokens : 0;
-  const long long rows = (long long)s.batch * s.num_kv_heads;
-  hipLaunchKernelGGL(evict_copy_kernel, dim3((unsigned)(rows * (chunks + clears))), dim3(256), 0,
-                     st, static_cast<char*>(k_pool), static_cast<char*>(v_pool), bt, lens, weights,
-                     new_table, kept, s.num_kv_heads, s.page_size, row_bytes, s.max_pages,
-                     s.num_phys, keep, chunks, clears, new_weights);
+hipError_t launch_evict(const LaunchShape& s, void* k_pool, void* v_pool, const int32_t* bt,
+                        const int32_t* lens, const float* weights, int keep, int sinks,
+                        int recent, const int32_t* new_table, int32_t* kept, int32_t* new_lens,
+                        float* new_weights, hipStream_t st) {
+  EvictArgs a;
+  a.k_pool = static_cast<char*>(k_pool);
+  a.v_pool = static_cast<char*>(v_pool);
+  a.bt = bt;
+  a.lens = lens;
+  a.weights = weights;
+  a.new_table = new_table;
+  a.kept = kept;
+  a.new_lens = new_lens;
+  a.new_weights = new_weights;
+  a.Hkv = s.num_kv_heads;
+  a.ps_bits = __builtin_ctz(s.page_size);
+  a.max_pages = s.max_pages;
+  a.num_phys = s.num_phys;
+  a.keep = keep;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.rows = s.batch * s.num_kv_heads;
+  // one workgroup a CU, of 64 slots at least
+  const int slots = keep < s.max_pages * s.page_size ? keep : s.max_pages * s.page_size;
+  int splits = (kNumCUs + a.rows - 1) / a.rows;
+  if (splits > (slots + 63) / 64) splits = (slots + 63) / 64;
+  const dim3 grid((unsigned)(a.rows * splits)), block(kEvThreads);
+  switch (s.head_dim * (s.bf16 ? 2 : 4)) {
+    case 128: hipLaunchKernelGGL(evict_kernel<128>, grid, block, 0, st, a, splits); break;
+    case 256: hipLaunchKernelGGL(evict_kernel<256>, grid, block, 0, st, a, splits); break;
+    default: hipLaunchKernelGGL(evict_kernel<512>, grid, block, 0, st, a, splits); break;
+  }
   return hipGetLastError();
 }
 

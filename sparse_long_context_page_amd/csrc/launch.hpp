@@ -306,12 +306,9 @@ hipError_t launch_weights(const LaunchShape& s, const void* q, bool q_bf16, cons
                           const int32_t* bt, const int32_t* lens, float alpha, const float* tau,
                           int window, int sinks, float decay, const float* w_in, float* w_out,
                           hipStream_t st);
-hipError_t launch_evict_select(const LaunchShape& s, const int32_t* lens, const float* weights,
-                               int keep, int sinks, int recent, int32_t* kept,
-                               int32_t* new_lens, hipStream_t st);
-hipError_t launch_evict_copy(const LaunchShape& s, void* k_pool, void* v_pool, const int32_t* bt,
-                             const int32_t* lens, const float* weights, int keep,
-                             const int32_t* new_table, const int32_t* kept, float* new_weights,
-                             hipStream_t st);
+hipError_t launch_evict(const LaunchShape& s, void* k_pool, void* v_pool, const int32_t* bt,
+                        const int32_t* lens, const float* weights, int keep, int sinks,
+                        int recent, const int32_t* new_table, int32_t* kept, int32_t* new_lens,
+                        float* new_weights, hipStream_t st);
 
 }  // namespace ekv
