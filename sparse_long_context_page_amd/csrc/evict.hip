@@ -120,7 +120,7 @@ __device__ __forceinline__ void weights_of(const WeightArgs& a, int b, int g, in
 #pragma unroll
       for (int i = 0; i < NZ; ++i) {
         const int t = t0 + tile_token<BF>(c, i);
-        const bool see = live && page_ok && t < L && (t >= vis_lo || t < a.sinks);
+        const bool see = live & page_ok & sees(t, vis_lo, L, a.sinks);
         z[i] = see ? weight_of<POW>(z[i], tau, a.am1, a.m) : 0.0f;
       }
       Sum::reduce(z, rl);

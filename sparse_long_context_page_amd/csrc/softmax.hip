@@ -170,7 +170,7 @@ __device__ __forceinline__ float weight(float z, float m) {
 template <int N>
 __device__ __forceinline__ void raise(float tmax, float& m, float& l, f32x4 (&acc)[N]) {
   const float mn = fmaxf(m, group_max(tmax));
-  const float f = exp2f((m - mn) * kLog2e);
+  const float f = __builtin_amdgcn_exp2f((m - mn) * kLog2e);
   l *= f;
 #pragma unroll
   for (int n = 0; n < N; ++n) acc[n] *= f;
@@ -194,7 +194,7 @@ __device__ __forceinline__ void late_tile(const Views& x, TilePages pg, int t0, 
 #pragma unroll
   for (int i = 0; i < NZ; ++i) {
     const int t = t0 + tile_token<BF>(c, i);
-    const bool see = page_ok && t < hi && (t >= lo || t < sinks);
+    const bool see = page_ok & sees(t, lo, hi, sinks);
     p[i] = see ? weight<PARTS>(p[i], m) : 0.0f;
   }
   PFrag<BF, PP> pf;
@@ -207,7 +207,7 @@ __device__ __forceinline__ void late_tile(const Views& x, TilePages pg, int t0, 
 #pragma unroll
     for (int i = 0; i < NZ; ++i) {
       const int t = t0 + tile_token<BF>(c, i);
-      if (!(page_ok && t < rhi && (t >= rlo || t < sinks))) vt.clear(i);
+      if (!(page_ok & sees(t, rlo, rhi, sinks))) vt.clear(i);
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
@@ -231,8 +231,9 @@ __device__ __forceinline__ void store_out(void* out, size_t at, f32x4 o) {
   }
 }
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+// (l is 0 or at least about 1: m is never above the largest score)
 __device__ __forceinline__ float log_sum(float m, float l) {
-  return l == 0.0f ? -INFINITY : m + kLn2 * log2f(l);
+  return l == 0.0f ? -INFINITY : m + kLn2 * __builtin_amdgcn_logf(l);
 }
 
 // ---------------------------------------------------------------------------
@@ -314,7 +315,7 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
 #pragma unroll
         for (int i = 0; i < NZ; ++i) {
           const int t = t0 + tile_token<BF>(c, i);
-          if (!(page_ok && t < hi && (t >= lo || t < sinks))) z[i] = -INFINITY;
+          z[i] = page_ok & sees(t, lo, hi, sinks) ? z[i] : -INFINITY;
         }
       }
       float tmax = z[0];
@@ -333,7 +334,7 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
 #pragma unroll
         for (int i = 0; i < NZ; ++i) {
           const int t = t0 + tile_token<BF>(c, i);
-          if (!(page_ok && t < u.hi && (t >= u.lo || t < sinks))) vt.clear(i);
+          if (!(page_ok & sees(t, u.lo, u.hi, sinks))) vt.clear(i);
         }
         later = __any(vt.any_nonfinite());
       }
@@ -382,7 +383,7 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
     for (int v = 0; v < NW; ++v) {
       const float lv = sh.ml[v][r][1];
       if (lv == 0.0f) continue;
-      const float f = exp2f((sh.ml[v][r][0] - M) * kLog2e);
+      const float f = __builtin_amdgcn_exp2f((sh.ml[v][r][0] - M) * kLog2e);
       ls += f * lv;
       o += f * *reinterpret_cast<const f32x4*>(&sh.o[v][r][d]);
     }
@@ -551,7 +552,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
 #pragma unroll
             for (int i = 0; i < NZ; ++i) {
               const int tt = t0 + tile_token<BF>(c, i);
-              if (!(page_ok && tt < hi[t] && (tt >= lo[t] || tt < sinks))) p[t][i] = -INFINITY;
+              p[t][i] = page_ok & sees(tt, lo[t], hi[t], sinks) ? p[t][i] : -INFINITY;
             }
           }
           tmax[t] = p[t][0];
@@ -580,7 +581,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
 #pragma unroll
           for (int i = 0; i < NZ; ++i) {
             const int tt = t0 + tile_token<BF>(c, i);
-            if (!(page_ok && tt < u.hi && (tt >= u.lo || tt < sinks))) vt.clear(i);
+            if (!(page_ok & sees(tt, u.lo, u.hi, sinks))) vt.clear(i);
           }
           later = __any(vt.any_nonfinite());
         }
@@ -632,8 +633,8 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
     for (int e = 0; e < kRowGroups - 1; ++e) {
       const float me = sh.ml[e][wave][t][rl][0], le = sh.ml[e][wave][t][rl][1];
       const float mn = le == 0.0f ? m[t] : l[t] == 0.0f ? me : fmaxf(m[t], me);
-      const float f = l[t] == 0.0f ? 0.0f : exp2f((m[t] - mn) * kLog2e);
-      const float fe = le == 0.0f ? 0.0f : exp2f((me - mn) * kLog2e);
+      const float f = l[t] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((m[t] - mn) * kLog2e);
+      const float fe = le == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((me - mn) * kLog2e);
       l[t] = f * l[t] + fe * le;
 #pragma unroll
       for (int n = 0; n < kAcc; ++n) acc[t][n] = f * acc[t][n] + fe * sh.o[e][wave][t][n][lane];
@@ -724,14 +725,14 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const float* __restr
         if (s0 + e * SG >= slots) x[e] = f32x2{-FLT_MAX, 0.0f};
         if (!(x[e][1] == 0.0f)) mn = fmaxf(mn, x[e][0]);
       }
-      const float f = exp2f((M - mn) * kLog2e);
+      const float f = __builtin_amdgcn_exp2f((M - mn) * kLog2e);
       l *= f;
       o *= f;
       M = mn;
 #pragma unroll
       for (int e = 0; e < U; ++e) {
         if (x[e][1] == 0.0f) continue;
-        const float g = exp2f((x[e][0] - M) * kLog2e);
+        const float g = __builtin_amdgcn_exp2f((x[e][0] - M) * kLog2e);
         l += g * x[e][1];
         o += g * y[e];
       }
@@ -755,7 +756,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const float* __restr
     for (int e = 0; e < SG; ++e) {
       const float le = sml[rr][e][1];
       if (le == 0.0f) continue;
-      const float g = exp2f((sml[rr][e][0] - mn) * kLog2e);
+      const float g = __builtin_amdgcn_exp2f((sml[rr][e][0] - mn) * kLog2e);
       l += g * le;
       o += g * so[rr][e][d4];
     }

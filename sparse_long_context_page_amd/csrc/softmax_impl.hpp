@@ -26,6 +26,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // Tokens of one tile: two 16-token score tiles for bf16 caches (the 32 k
 // indices of one V^T P^T instruction), one for float32 caches. A tile starts
@@ -345,13 +346,13 @@ struct VTile<true, D> {
   __device__ __forceinline__ void clear(int j) { f[j] = vec(0); }
   // An infinity or NaN among the values held?
   __device__ __forceinline__ bool any_nonfinite() const {
-    bool bad = false;
+    u16x2 big = {0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int e = 0; e < D / 32; ++e)
-        bad |= (f[j][e] & 0x7f800000u) == 0x7f800000u || (f[j][e] & 0x7f80u) == 0x7f80u;
-    return bad;
+        big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, f[j][e] & 0x7fff7fffu));
+    return big[0] >= 0x7f80 || big[1] >= 0x7f80;
   }
   // acc[n] += V^T P^T, instruction n
   template <int PP>
@@ -400,15 +401,14 @@ struct VTile<false, D> {
     for (int h = 0; h < D / 64; ++h) f[j][h] = f32x4{0, 0, 0, 0};
   }
   __device__ __forceinline__ bool any_nonfinite() const {
-    bool bad = false;
+    uint32_t big = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          bad |= (__float_as_uint(f[j][h][e]) & 0x7f800000u) == 0x7f800000u;
-    return bad;
+        for (int e = 0; e < 4; ++e) big = max(big, __float_as_uint(f[j][h][e]) & 0x7fffffffu);
+    return big >= 0x7f800000u;
   }
   template <int PP>
   __device__ __forceinline__ f32x4 mul(int n, const PFrag<false, PP>& p, f32x4 o) const {
@@ -432,6 +432,11 @@ struct TileSpan {
   int ns, mt0, n;
   __device__ __forceinline__ int tile(int v) const { return v < ns ? v : v - ns + mt0; }
 };
+
+// (bitwise: one compare and mask operation each, no branch)
+__device__ __forceinline__ bool sees(int t, int lo, int hi, int sinks) {
+  return (t < hi) & ((t >= lo) | (t < sinks));
+}
 
 template <int TT>
 __device__ __forceinline__ TileSpan tile_span(int lo, int hi, int sinks) {
