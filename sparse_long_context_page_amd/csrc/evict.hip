@@ -113,7 +113,7 @@ __device__ __forceinline__ void weights_of(const WeightArgs& a, int b, int g, in
         wait_vmcnt<0>();
       }
       KTile<BF, D> kt;
-      kt.read(buf[j & 1], 0, lane);
+      kt.read(lds_addr(buf[j & 1]), 0, lane);
       float z[NZ];
       kt.template scores<PARTS>(q, z);
       const bool page_ok = (!BF || c < 2 ? pc.p0 : pc.p1) >= 0;
@@ -135,7 +135,7 @@ __device__ __forceinline__ void weights_of(const WeightArgs& a, int b, int g, in
 template <bool BF, int D, int PARTS, int POW>
 __global__ __launch_bounds__(kWeightWaves* kWave) void weights_kernel(WeightArgs a) {
   constexpr int TT = kTile<BF>;
-  __shared__ __align__(16) char buf[kWeightWaves][2][WaveTile<BF, D>::kBytes];
+  __shared__ __align__(1024) char buf[kWeightWaves][2][WaveTile<BF, D>::kBytes];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   // KV heads first: what runs together reads neighbouring parts of a page

@@ -180,7 +180,8 @@ __device__ __forceinline__ void raise(float tmax, float& m, float& l, f32x4 (&ac
 // A tile in which the rows see different tokens and some value is not finite,
 // which must not meet the zero weight of a row that does not see it: one row
 // at a time, on the values that it sees. (The weights are in l already.)
-template <bool BF, int D, int PARTS, int PP, int N>
+// kStage: acc lies as the many-rows form keeps it.
+template <bool BF, int D, int PARTS, int PP, bool kStage, int N>
 __device__ __forceinline__ void late_tile(const Views& x, TilePages pg, int t0, int lane,
                                           const QFrag<BF, D, PARTS>& q, int lo, int hi, int sinks,
                                           float m, f32x4 (&acc)[N]) {
@@ -194,25 +195,30 @@ __device__ __forceinline__ void late_tile(const Views& x, TilePages pg, int t0, 
 #pragma unroll
   for (int i = 0; i < NZ; ++i) {
     const int t = t0 + tile_token<BF>(c, i);
-    const bool see = page_ok & sees(t, lo, hi, sinks);
-    p[i] = see ? weight<PARTS>(p[i], m) : 0.0f;
+    p[i] = page_ok & sees(t, lo, hi, sinks) ? weight<PARTS>(p[i], m) : 0.0f;
   }
   PFrag<BF, PP> pf;
   pf.set(p);
-  VTile<BF, D> vt;
 #pragma unroll 1
   for (int r = 0; r < 16; ++r) {
     const int rlo = __shfl(lo, r, kWave), rhi = __shfl(hi, r, kWave);
-    vt.template load<true>(x.v, pg, t0, lane);
+    unsigned see = 0;
 #pragma unroll
-    for (int i = 0; i < NZ; ++i) {
-      const int t = t0 + tile_token<BF>(c, i);
-      if (!(page_ok & sees(t, rlo, rhi, sinks))) vt.clear(i);
-    }
+    for (int i = 0; i < NZ; ++i)
+      see |= (unsigned)(page_ok & sees(t0 + tile_token<BF>(c, i), rlo, rhi, sinks)) << i;
+    if constexpr (kStage) {
+      StageV<BF, D>::template add_slow<PP>(x.v, pg, t0, lane, pf, see, rl == r, acc);
+    } else {
+      VTile<BF, D> vt;
+      vt.template load<true>(x.v, pg, t0, lane);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const f32x4 o = vt.template mul<PP>(n, pf, f32x4{0, 0, 0, 0});
-      if (rl == r) acc[n] += o;
+      for (int i = 0; i < NZ; ++i)
+        if (!(see >> i & 1)) vt.clear(i);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const f32x4 o = vt.template mul<PP>(n, pf, f32x4{0, 0, 0, 0});
+        if (rl == r) acc[n] += o;
+      }
     }
   }
 }
@@ -353,7 +359,7 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
     while (put_off) {
       const int j = __builtin_ctzll(put_off);
       put_off &= put_off - 1;
-      late_tile<BF, D, PARTS, PP>(x, pages(j), start(j), lane, q, lo, hi, sinks, m, acc);
+      late_tile<BF, D, PARTS, PP, false>(x, pages(j), start(j), lane, q, lo, hi, sinks, m, acc);
     }
   }
 
@@ -424,7 +430,7 @@ struct RowsLds {
     f32x4 o[kRowGroups - 1][kRowWaves][kRowTiles<BF, PARTS>][VTile<BF, D>::kAcc][kWave];
   };
   float ml[kRowGroups - 1][kRowWaves][kRowTiles<BF, PARTS>][16][2];
-  int ok[kRowGroups][2][kRowWaves];  // is that quarter of the stage in a physical page?
+  __align__(16) int ok[kRowGroups][2][kRowWaves];  // 1: that quarter of the stage is in a physical page
 };
 
 template <bool BF, int D, int PARTS>
@@ -489,6 +495,48 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
     from[i] = r * St::kRow + ((slot ^ St::swizzle(wave * (ST / kRowWaves) + r)) << 4);
   }
 
+  // page of this wave's quarter of each of the next stages, one stage per lane
+  int base = v0, ns = 0, pg = -1;
+  auto look = [&](int done) {
+    base = v0 + done;
+    ns = min(kChunk, max(mine - done, 0));
+    pg = -1;
+    if (lane < ns)
+      pg = page_at(a, x.table, npages,
+                   (span.tile(base + lane) * ST + wave * (ST / kRowWaves)) >> a.ps_bits);
+  };
+  auto stage = [&](int j) {
+    const int p = __builtin_amdgcn_readlane(pg, j);
+    const int t = span.tile(base + j) * ST + wave * (ST / kRowWaves);
+    const size_t off =
+        (size_t)max(p, 0) * x.k.page_bytes + (size_t)(t & ((1 << a.ps_bits) - 1)) * St::kRow;
+    char* dst = sh.st[grp][j & 1][0] + wave * (St::kBytes / kRowWaves);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      __builtin_amdgcn_global_load_lds(x.k.base + off + from[i], dst + i * 1024, 16, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      __builtin_amdgcn_global_load_lds(x.v.base + off + from[i], dst + St::kBytes + i * 1024, 16, 0,
+                                       0);
+    if (lane == 0) sh.ok[grp][j & 1][wave] = p >= 0 ? 1 : 0;
+  };
+  // Before a stage is used: rows of this wave's quarter that no row of the
+  // block sees hold whatever the page holds; as values they are cleared
+  // (their weight is 0, but 0 times an infinity is not).
+  auto settle = [&](int j) {
+    wait_vmcnt<0>();
+    const int p = __builtin_amdgcn_readlane(pg, j);
+    constexpr int R = ST / kRowWaves;
+    const int t = span.tile(base + j) * ST + wave * R;
+    if (p >= 0 && t + R <= all.hi && (t >= all.lo || t + R <= sinks)) return;
+    constexpr int kPer = kWave / R;  // lanes a row
+    const int r = lane / kPer;
+    if ((p >= 0) & sees(t + r, all.lo, all.hi, sinks)) return;
+    char* dst = sh.st[grp][j & 1][1] + (wave * R + r) * St::kRow + lane % kPer * 16;
+#pragma unroll
+    for (int i = 0; i < St::kRow; i += kPer * 16)
+      *reinterpret_cast<u32x4*>(dst + i) = u32x4{0, 0, 0, 0};
+  };
   f32x4 acc[RT][kAcc];
   float m[RT], l[RT];
 #pragma unroll
@@ -500,101 +548,85 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   }
 
   for (int done = 0; done < steps; done += kChunk) {
-    const int base = v0 + done;
-    const int ns = min(kChunk, max(mine - done, 0)), nb = min(kChunk, steps - done);
-    // page of this wave's quarter of each stage, one stage per lane
-    int pg = -1;
-    if (lane < ns)
-      pg = page_at(a, x.table, npages,
-                   (span.tile(base + lane) * ST + wave * (ST / kRowWaves)) >> a.ps_bits);
-    auto stage = [&](int j) {
-      const int p = __builtin_amdgcn_readlane(pg, j);
-      const int t = span.tile(base + j) * ST + wave * (ST / kRowWaves);
-      const size_t off =
-          (size_t)max(p, 0) * x.k.page_bytes + (size_t)(t & ((1 << a.ps_bits) - 1)) * St::kRow;
-      char* dst = sh.st[grp][j & 1][0] + wave * (St::kBytes / kRowWaves);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        __builtin_amdgcn_global_load_lds(x.k.base + off + from[i], dst + i * 1024, 16, 0, 0);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        __builtin_amdgcn_global_load_lds(x.v.base + off + from[i], dst + St::kBytes + i * 1024, 16,
-                                         0, 0);
-      if (lane == 0) sh.ok[grp][j & 1][wave] = p >= 0;
-    };
-    if (ns > 0) stage(0);
-    wait_vmcnt<0>();
+    const int nb = min(kChunk, steps - done);
+    look(done);
+    if (ns > 0) {
+      stage(0);
+      settle(0);
+    }
     __syncthreads();
     uint64_t put_off = 0;  // two tiles a stage
     for (int j = 0; j < nb; ++j) {
       if (j + 1 < ns) stage(j + 1);
-      const int ts = j < ns ? span.tile(base + j) * ST : INT32_MAX - ST;  // past every row
-      const char* kst = sh.st[grp][j & 1][0];
-      const char* vst = sh.st[grp][j & 1][1];
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        const int t0 = ts + sub * TT;
-        // a tile none of this wave's rows sees
-        if (t0 >= u.hi || (t0 + TT <= u.lo && t0 >= sinks)) continue;
-        const bool ok0 = sh.ok[grp][j & 1][2 * sub] != 0, ok1 = sh.ok[grp][j & 1][2 * sub + 1] != 0;
-        const bool full = __builtin_amdgcn_readfirstlane(ok0 && ok1) &&
-                          t0 + TT <= u.fhi && (t0 >= u.flo || t0 + TT <= sinks);
-        const bool page_ok = c < 2 ? ok0 : ok1;
+      const int ts = j < ns ? span.tile(base + j) * ST : 0;
+      const lds_at kst = lds_addr(sh.st[grp][j & 1][0]), vst = kst + St::kBytes;
+      // a stage that some of this wave's rows sees
+      if (j < ns && ts < u.hi && (ts + ST > u.lo || ts < sinks)) {
+        const int4 ok = *reinterpret_cast<const int4*>(sh.ok[grp][j & 1]);
+        const bool full = __builtin_amdgcn_readfirstlane(ok.x & ok.y & ok.z & ok.w) &&
+                          ts + ST <= u.fhi && (ts >= u.flo || ts + ST <= sinks);
         KTile<BF, D> kt;
-        kt.read(kst, sub, lane);
-        float p[RT][NZ];
-        float tmax[RT];
-        bool rise = false;
+        kt.read(kst, 0, lane);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          kt.template scores<PARTS>(q[t], p[t]);
+        for (int sub = 0; sub < 2; ++sub) {
+          float p[RT][NZ];
+#pragma unroll
+          for (int t = 0; t < RT; ++t) kt.template scores<PARTS>(q[t], p[t]);
+          __builtin_amdgcn_s_setprio(0);
+          // the values, and the next tile's keys, are on their way while the
+          // weights are formed
+          if (sub == 0) kt.read(kst, 1, lane);
+          StageV<BF, D> v;
+#pragma unroll
+          for (int n = 0; n < kAcc; ++n) v.read(vst, sub, lane, n);
+          bool later = false;
           if (!full) {
+            const int lowq = sub ? ok.z : ok.x, highq = sub ? ok.w : ok.y;
+            const bool page_ok = (c < 2 ? lowq : highq) != 0;
 #pragma unroll
             for (int i = 0; i < NZ; ++i) {
-              const int tt = t0 + tile_token<BF>(c, i);
-              p[t][i] = page_ok & sees(tt, lo[t], hi[t], sinks) ? p[t][i] : -INFINITY;
+              const int tt = ts + sub * TT + tile_token<BF>(c, i);
+#pragma unroll
+              for (int t = 0; t < RT; ++t)
+                p[t][i] = page_ok & sees(tt, lo[t], hi[t], sinks) ? p[t][i] : -INFINITY;
             }
+            later = __any(stage_nonfinite<BF, D>(vst, sub, lane));
+            if (later) put_off |= 1ull << (2 * j + sub);
           }
-          tmax[t] = p[t][0];
+          float tmax[RT];
+          bool rise = false;
 #pragma unroll
-          for (int i = 1; i < NZ; ++i) tmax[t] = fmaxf(tmax[t], p[t][i]);
-          rise |= tmax[t] > m[t] + kSlack;
-        }
-        if (__any(rise)) {
+          for (int t = 0; t < RT; ++t) {
+            tmax[t] = p[t][0];
 #pragma unroll
-          for (int t = 0; t < RT; ++t) raise(tmax[t], m[t], l[t], acc[t]);
-        }
-        PFrag<BF, PP> pf[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-#pragma unroll
-          for (int i = 0; i < NZ; ++i) {
-            p[t][i] = weight<PARTS>(p[t][i], m[t]);
-            l[t] += p[t][i];
+            for (int i = 1; i < NZ; ++i) tmax[t] = fmaxf(tmax[t], p[t][i]);
+            rise |= tmax[t] > m[t] + kSlack;
           }
-          pf[t].set(p[t]);
-        }
-        VTile<BF, D> vt;
-        vt.read(vst, sub, lane);
-        bool later = false;
-        if (!full) {
+          if (__any(rise)) {
 #pragma unroll
-          for (int i = 0; i < NZ; ++i) {
-            const int tt = t0 + tile_token<BF>(c, i);
-            if (!(page_ok & sees(tt, u.lo, u.hi, sinks))) vt.clear(i);
+            for (int t = 0; t < RT; ++t) raise(tmax[t], m[t], l[t], acc[t]);
           }
-          later = __any(vt.any_nonfinite());
-        }
-        if (later) {
-          put_off |= 1ull << (2 * j + sub);
-        } else {
+          PFrag<BF, PP> pf[RT];
 #pragma unroll
-          for (int n = 0; n < kAcc; ++n)
+          for (int t = 0; t < RT; ++t) {
 #pragma unroll
-            for (int t = 0; t < RT; ++t) acc[t][n] = vt.template mul<PP>(n, pf[t], acc[t][n]);
+            for (int i = 0; i < NZ; ++i) {
+              p[t][i] = weight<PARTS>(p[t][i], m[t]);
+              l[t] += p[t][i];
+            }
+            pf[t].set(p[t]);
+          }
+          // matrix instructions before the other wave's exponentials: the two
+          // waves of a SIMD, in step after each barrier, then alternate
+          // (8192-token window 203 -> 190 us)
+          __builtin_amdgcn_s_setprio(1);
+          if (!__builtin_expect(later, 0)) {
+#pragma unroll
+            for (int n = 0; n < kAcc; ++n) v.template add<PP, RT>(pf, acc, n);
+          }
         }
       }
-      wait_vmcnt<0>();
+      if (j + 1 < ns) settle(j + 1);
       __syncthreads();
     }
     while (put_off) {
@@ -606,7 +638,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
       if (BF && a.ps_bits == 4) pp.p1 = page_at(a, x.table, npages, (t0 >> a.ps_bits) + 1);
 #pragma unroll
       for (int t = 0; t < RT; ++t)
-        late_tile<BF, D, PARTS, PP>(x, pp, t0, lane, q[t], lo[t], hi[t], sinks, m[t], acc[t]);
+        late_tile<BF, D, PARTS, PP, true>(x, pp, t0, lane, q[t], lo[t], hi[t], sinks, m[t], acc[t]);
     }
   }
 
@@ -652,20 +684,13 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
         a.part_ml[2 * part + 1] = ls;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int n = 0; n < kAcc; n += 4)
-          *reinterpret_cast<f32x4*>(a.part_o + part * D + VTile<BF, D>::coord(c, n, i)) =
-              f32x4{acc[t][n][i], acc[t][n + 1][i], acc[t][n + 2][i], acc[t][n + 3][i]};
+      for (int n = 0; n < kAcc; ++n)
+        *reinterpret_cast<f32x4*>(a.part_o + part * D + StageV<BF, D>::coord(c, n)) = acc[t][n];
     } else {
       const float inv = inverse(ls);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int n = 0; n < kAcc; n += 4)
-          store_out<PARTS>(a.out, (size_t)row[t] * D + VTile<BF, D>::coord(c, n, i),
-                           f32x4{acc[t][n][i], acc[t][n + 1][i], acc[t][n + 2][i],
-                                 acc[t][n + 3][i]} * inv);
+      for (int n = 0; n < kAcc; ++n)
+        store_out<PARTS>(a.out, (size_t)row[t] * D + StageV<BF, D>::coord(c, n), acc[t][n] * inv);
       if (c == 0 && a.lse) a.lse[row[t]] = log_sum(m[t], ls);
     }
   }
@@ -677,7 +702,7 @@ constexpr int att_waves(bool rows) { return rows ? kRowWaves * kRowGroups : 4; }
 
 template <bool BF, int D, int PARTS, bool ROWS>
 __global__ __launch_bounds__(att_waves(ROWS) * kWave, 2) void attend_kernel(AttendArgs a) {
-  extern __shared__ __align__(16) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   const Block w = block_of(a, blockIdx.x);
   if constexpr (ROWS) {
     if (w.pre ? a.pre_rows : a.own_rows) {

@@ -95,10 +95,21 @@ __device__ __forceinline__ bf16x8 as_bf(const u32x4& v) { return __builtin_bit_c
 // ---------------------------------------------------------------------------
 // Tiles staged in LDS for several waves
 
+// Byte addresses in LDS, as the 32-bit numbers that they are.
+typedef uint32_t lds_at;
+#define EKV_LDS __attribute__((address_space(3)))
+__device__ __forceinline__ lds_at lds_addr(const void* p) {
+  return (lds_at)(uintptr_t)(EKV_LDS const char*)p;
+}
+template <typename T>
+__device__ __forceinline__ T lds_read(lds_at p) {
+  return *(EKV_LDS const T*)p;
+}
+
 // A stage is two tiles of K and the same of V. Row r of 16-byte chunks lies at
 // r * row bytes, chunk ch at slot ch ^ swizzle(r): the 16 tokens that a score
 // operand reads at one chunk fall on different banks (without it all 16 hit
-// the same ones), and a value row is still read whole.
+// the same ones), and so do the 4 rows x 2 chunks of a transposing read.
 template <bool BF, int D>
 struct Stage {
   static constexpr int kTokens = 2 * kTile<BF>;
@@ -106,11 +117,14 @@ struct Stage {
   static constexpr int kChunks = kRow / 16;
   static constexpr int kBytes = kTokens * kRow;  // of K, and of V
   __device__ __forceinline__ static int swizzle(int r) {
-    return (BF ? ((r >> 3) & 3) << 2 | (r & 3) : r & 15) & (kChunks - 1);
+    return (BF ? (r & 3) << 1 | ((r >> 3) & 1) | ((r >> 4) & 1) << 3 : r & 15) & (kChunks - 1);
   }
   __device__ __forceinline__ static int at(int r, int ch) {
     return r * kRow + ((ch ^ swizzle(r)) << 4);
   }
+  // The place of chunk ch | by from that of chunk ch (no common bits; rows
+  // are aligned to their length): one operation, no register per chunk.
+  __device__ __forceinline__ static lds_at on(lds_at p, int by) { return p ^ (unsigned)(by << 4); }
 };
 
 // One K tile streamed into LDS by one wave for itself, whole rows at a time
@@ -214,14 +228,15 @@ struct KTile<true, D> {
     }
   }
   // tile `sub` of a stage
-  __device__ __forceinline__ void read(const char* st, int sub, int lane) {
+  __device__ __forceinline__ void read(lds_at st, int sub, int lane) {
+    typedef Stage<true, D> St;
     const int m = lane & 15, c = lane >> 4;
+    const lds_at r = st + St::at(((m >> 2) << 3) + (m & 3), c);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int s = 0; s < D / 32; ++s)
 #pragma unroll
-      for (int s = 0; s < D / 32; ++s)
-        f[u][s] = *reinterpret_cast<const u32x4*>(
-            st + Stage<true, D>::at(sub * 32 + ((m >> 2) << 3) + u * 4 + (m & 3), c + s * 4));
+      for (int u = 0; u < 2; ++u)  // 4 rows further: the same swizzle
+        f[u][s] = lds_read<u32x4>(St::on(r, 4 * s) + sub * (St::kBytes / 2) + u * 4 * St::kRow);
   }
   template <int PARTS>
   __device__ __forceinline__ void scores(const QFrag<true, D, PARTS>& q, float (&z)[8]) const {
@@ -249,11 +264,12 @@ struct KTile<false, D> {
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) f[s] = load_vec<kStream, f32x4>(r + s * 64);
   }
-  __device__ __forceinline__ void read(const char* st, int sub, int lane) {
+  __device__ __forceinline__ void read(lds_at st, int sub, int lane) {
+    typedef Stage<false, D> St;
+    const lds_at r = st + St::at(lane & 15, lane >> 4);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s)
-      f[s] = *reinterpret_cast<const f32x4*>(
-          st + Stage<false, D>::at(sub * 16 + (lane & 15), (lane >> 4) + s * 4));
+      f[s] = lds_read<f32x4>(St::on(r, 4 * s) + sub * (St::kBytes / 2));
   }
   template <int PARTS>
   __device__ __forceinline__ void scores(const QFrag<false, D, PARTS>& q, float (&z)[4]) const {
@@ -332,17 +348,6 @@ struct VTile<true, D> {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = load_vec<kStream, vec>(r + j * (D * 2));
   }
-  __device__ __forceinline__ void read(const char* st, int sub, int lane) {
-    const int m = lane & 15, c = lane >> 4;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = sub * 32 + c * 8 + j;
-      if constexpr (D == 128)
-        f[j] = *reinterpret_cast<const vec*>(st + Stage<true, D>::at(r, m));
-      else
-        f[j] = *reinterpret_cast<const vec*>(st + Stage<true, D>::at(r, m >> 1) + (m & 1) * 8);
-    }
-  }
   __device__ __forceinline__ void clear(int j) { f[j] = vec(0); }
   // An infinity or NaN among the values held?
   __device__ __forceinline__ bool any_nonfinite() const {
@@ -387,15 +392,6 @@ struct VTile<false, D> {
       for (int h = 0; h < D / 64; ++h)
         f[j][h] = load_vec<kStream, f32x4>(r + j * (D * 4) + h * 256);
   }
-  __device__ __forceinline__ void read(const char* st, int sub, int lane) {
-    const int m = lane & 15, c = lane >> 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-        f[j][h] = *reinterpret_cast<const f32x4*>(
-            st + Stage<false, D>::at(sub * 16 + c * 4 + j, m + h * 16));
-  }
   __device__ __forceinline__ void clear(int j) {
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) f[j][h] = f32x4{0, 0, 0, 0};
@@ -421,6 +417,131 @@ struct VTile<false, D> {
     return (n >> 2) * 64 + (c * 4 + i) * 4 + (n & 3);
   }
 };
+
+// ---------------------------------------------------------------------------
+// Value tiles of a stage, used by several row tiles of a wave
+
+template <bool BF, int D>
+struct StageV;
+
+// The transposing LDS read gives lane n of 16 the column n of 4 rows x 16
+// columns: two make the 8 tokens of a group at coordinate 16 n + m, so acc[n][i]
+// holds coordinate 16 n + 4 c + i, and nothing is shuffled in registers.
+template <int D>
+struct StageV<true, D> {
+  static constexpr int kAcc = D / 16;
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  bf16x8 f[kAcc];
+  __device__ __forceinline__ void read(lds_at st, int sub, int lane, int n) {
+    typedef Stage<true, D> St;
+    const int m = lane & 15, c = lane >> 4;
+    const int r = c * 8 + (m >> 2);  // and the row 4 further: the same swizzle
+    const lds_at at =
+        St::on(st + St::at(r, (m >> 1) & 1) + (m & 1) * 8, 2 * n) + sub * (St::kBytes / 2);
+    const s16x4 a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EKV_LDS s16x4*)at);
+    const s16x4 a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((EKV_LDS s16x4*)(at + 4 * St::kRow));
+    f[n] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  template <int PP, int RT>
+  __device__ __forceinline__ void add(const PFrag<true, PP> (&p)[RT], f32x4 (&acc)[RT][kAcc],
+                                      int n) const {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int s = PP - 1; s >= 0; --s)
+        acc[t][n] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[n], as_bf(p[t].b[s]), acc[t][n], 0, 0, 0);
+  }
+  // acc[n] += V^T P^T of tile t0 read from memory, on the tokens `see` says
+  // (a bit per token of this lane's group), where `mine`
+  template <int PP>
+  __device__ __forceinline__ static void add_slow(const KvView& v, const TilePages& pg, int t0,
+                                                  int lane, const PFrag<true, PP>& p,
+                                                  unsigned see, bool mine, f32x4 (&acc)[kAcc]) {
+    const int m = lane & 15, c = lane >> 4;
+    const char* r = row_ptr<true, D>(v, pg, t0, c * 8) + m * 2;
+#pragma unroll 1
+    for (int n = 0; n < kAcc; ++n) {
+      u32x4 a = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = *reinterpret_cast<const uint16_t*>(r + j * (D * 2) + n * 32);
+        a[j / 2] |= (see >> j & 1 ? x : 0u) << (j % 2 * 16);
+      }
+      f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = PP - 1; s >= 0; --s)
+        o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(a), as_bf(p.b[s]), o, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < kAcc; ++k)
+        if (k == n && mine) acc[k] += o;
+    }
+  }
+  __device__ __forceinline__ static int coord(int c, int n) { return n * 16 + c * 4; }
+};
+
+template <int D>
+struct StageV<false, D> {
+  static constexpr int kAcc = D / 16;
+  float f[kAcc][4];
+  __device__ __forceinline__ void read(lds_at st, int sub, int lane, int n) {
+    typedef Stage<false, D> St;
+    const int m = lane & 15, c = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      f[n][j] = lds_read<float>(St::on(st + St::at(c * 4 + j, m >> 2) + (m & 3) * 4, 4 * n) +
+                                sub * (St::kBytes / 2));
+  }
+  template <int PP, int RT>
+  __device__ __forceinline__ void add(const PFrag<false, PP> (&p)[RT], f32x4 (&acc)[RT][kAcc],
+                                      int n) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[n][j], p[t].b[j], acc[t][n], 0, 0, 0);
+  }
+  template <int PP>
+  __device__ __forceinline__ static void add_slow(const KvView& v, const TilePages& pg, int t0,
+                                                  int lane, const PFrag<false, PP>& p,
+                                                  unsigned see, bool mine, f32x4 (&acc)[kAcc]) {
+    const int m = lane & 15, c = lane >> 4;
+    const char* r = row_ptr<false, D>(v, pg, t0, c * 4) + m * 4;
+#pragma unroll 1
+    for (int n = 0; n < kAcc; ++n) {
+      f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = *reinterpret_cast<const float*>(r + j * (D * 4) + n * 64);
+        o = __builtin_amdgcn_mfma_f32_16x16x4f32(see >> j & 1 ? x : 0.0f, p.b[j], o, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < kAcc; ++k)
+        if (k == n && mine) acc[k] += o;
+    }
+  }
+  __device__ __forceinline__ static int coord(int c, int n) { return n * 16 + c * 4; }
+};
+
+// An infinity or NaN among the values of tile `sub`?
+template <bool BF, int D>
+__device__ __forceinline__ bool stage_nonfinite(lds_at st, int sub, int lane) {
+  constexpr int kTileBytes = Stage<BF, D>::kBytes / 2;
+  uint32_t big = 0;
+  u16x2 bh = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kTileBytes / 1024; ++i) {
+    const u32x4 x = lds_read<u32x4>(st + sub * kTileBytes + i * 1024 + lane * 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (BF)
+        bh = __builtin_elementwise_max(bh, __builtin_bit_cast(u16x2, x[e] & 0x7fff7fffu));
+      else
+        big = max(big, x[e] & 0x7fffffffu);
+    }
+  }
+  return BF ? bh[0] >= 0x7f80 || bh[1] >= 0x7f80 : big >= 0x7f800000u;
+}
 
 // ---------------------------------------------------------------------------
 // The tokens a block of rows sees
