@@ -286,7 +286,7 @@ hipError_t launch_tau_pv_f32(const LaunchShape& s, const SplitPlan& p, const voi
 constexpr int kAttMaxSplits = 256;  // parts of a row block
 constexpr int kAttManyRows = 33;    // rows of a KV head from which the many-rows form runs
 struct AttendPlan {
-  long long rows = 0, items = 0, pre_items = 0;
+  long long rows = 0, items = 0, own_items = 0;
   int pre_block = 0, pre_splits = 0, row_block = 0, row_blocks = 0, splits = 0, slots = 0;
   bool pre_rows = false, own_rows = false;  // the many-rows form, per part
   size_t ml_off = 0, ws_bytes = 0;

@@ -45,10 +45,10 @@ struct AttendArgs {
   int batch, H, Hkv, g_bits, n, ps_bits, max_pages, num_phys;  // 2^g_bits heads a KV head
   int window, sinks;
   int prefix;                                  // tokens of the shared prefix (0: none)
-  int pre_block, pre_splits, pre_items;        // rows per block and splits of the prefix part
+  int pre_block, pre_splits;                   // rows per block and splits of the prefix part
   int row_block, row_blocks, splits;           // of the sequences' own part
   int slots;                                   // parts per row
-  bool pre_rows, own_rows;                     // parts of the many-rows form
+  int own_items;                               // workgroups of that part: the first
 };
 
 // What one workgroup works on. Items go over the KV heads first: the blocks
@@ -63,8 +63,8 @@ struct Block {
 
 __device__ __forceinline__ Block block_of(const AttendArgs& a, int item) {
   Block w;
-  w.pre = item < a.pre_items;
-  if (!w.pre) item -= a.pre_items;
+  w.pre = item >= a.own_items;
+  if (w.pre) item -= a.own_items;
   w.g = item % a.Hkv;
   int x = item / a.Hkv;
   if (w.pre) {
@@ -81,7 +81,7 @@ __device__ __forceinline__ Block block_of(const AttendArgs& a, int item) {
     w.b = x / a.row_blocks;
     w.nrows = min(a.row_block, (a.n << a.g_bits) - w.r0);
     w.splits = a.splits;
-    w.slot = a.pre_items ? a.pre_splits + w.split : w.split;
+    w.slot = a.pre_splits + w.split;
   }
   return w;
 }
@@ -417,23 +417,24 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
 template <bool BF, int PARTS>
 constexpr int kRowTiles = BF && PARTS == 1 ? 2 : 1;
 
-// Two groups of four waves: each group takes half of the workgroup's stages
-// for all of its rows, so a CU's eight waves finish a row block with one part
-// (four waves and twice the splits: 14 us more in the join of 32768 rows).
+// GR groups of four waves: each group takes its share of the workgroup's
+// stages for all of its rows. A chunk of a prompt runs with two: a CU's eight
+// waves finish a row block with one part (four waves and twice the splits: 14
+// us more in the join of 32768 rows). A shared prefix runs with one, beside a
+// workgroup that reads the sequences' own tokens.
 constexpr int kRowWaves = 4;
-constexpr int kRowGroups = 2;
 
-template <bool BF, int D, int PARTS>
+template <bool BF, int D, int PARTS, int GR>
 struct RowsLds {
   union {
-    char st[kRowGroups][2][2][Stage<BF, D>::kBytes];  // [group][buffer][K, V]
-    f32x4 o[kRowGroups - 1][kRowWaves][kRowTiles<BF, PARTS>][VTile<BF, D>::kAcc][kWave];
+    char st[GR][2][2][Stage<BF, D>::kBytes];  // [group][buffer][K, V]
+    f32x4 o[GR > 1 ? GR - 1 : 1][kRowWaves][kRowTiles<BF, PARTS>][VTile<BF, D>::kAcc][kWave];
   };
-  float ml[kRowGroups - 1][kRowWaves][kRowTiles<BF, PARTS>][16][2];
-  __align__(16) int ok[kRowGroups][2][kRowWaves];  // 1: that quarter of the stage is in a physical page
+  float ml[GR > 1 ? GR - 1 : 1][kRowWaves][kRowTiles<BF, PARTS>][16][2];
+  __align__(16) int ok[GR][2][kRowWaves];  // 1: that quarter of the stage is in a physical page
 };
 
-template <bool BF, int D, int PARTS>
+template <bool BF, int D, int PARTS, int GR>
 __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w, char* smem) {
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
@@ -447,7 +448,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   constexpr int ST = St::kTokens;
   constexpr int kChunk = 32;                          // stages between two looks at the table
   constexpr int kLoads = St::kBytes / kRowWaves / 1024;  // of K a wave and stage, and of V
-  RowsLds<BF, D, PARTS>& sh = *reinterpret_cast<RowsLds<BF, D, PARTS>*>(smem);
+  RowsLds<BF, D, PARTS, GR>& sh = *reinterpret_cast<RowsLds<BF, D, PARTS, GR>*>(smem);
 
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wid = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -480,7 +481,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   const int per = (span.n + w.splits - 1) / w.splits;
   const int b0 = min(w.split * per, span.n), b1 = min(b0 + per, span.n);
   // stages of this group, and steps that every group makes
-  const int steps = (b1 - b0 + kRowGroups - 1) / kRowGroups;
+  const int steps = (b1 - b0 + GR - 1) / GR;
   const int v0 = min(b0 + grp * steps, b1), mine = min(steps, b1 - v0);
   const int npages = (all.hi + (1 << a.ps_bits) - 1) >> a.ps_bits;
   const Views x = views_of<BF, D>(a, w);
@@ -646,7 +647,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   // stage has been read: the loop ends with a barrier)
 #pragma unroll
   for (int t = 0; t < RT; ++t) l[t] = group_sum(l[t]);
-  if (grp > 0) {
+  if (GR > 1 && grp > 0) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
 #pragma unroll
@@ -657,12 +658,12 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
       }
     }
   }
-  __syncthreads();
+  if (GR > 1) __syncthreads();
   if (grp > 0) return;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
 #pragma unroll
-    for (int e = 0; e < kRowGroups - 1; ++e) {
+    for (int e = 0; e < GR - 1; ++e) {
       const float me = sh.ml[e][wave][t][rl][0], le = sh.ml[e][wave][t][rl][1];
       const float mn = le == 0.0f ? m[t] : l[t] == 0.0f ? me : fmaxf(m[t], me);
       const float f = l[t] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f((m[t] - mn) * kLog2e);
@@ -696,21 +697,30 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   }
 }
 
-// Waves of a workgroup: eight where the many-rows form is among the parts,
-// else four.
-constexpr int att_waves(bool rows) { return rows ? kRowWaves * kRowGroups : 4; }
+// What a launch runs: the few-rows form alone; the many-rows form alone (a
+// window, two groups a workgroup); or the many-rows form over a shared prefix
+// and the few-rows form over the rest. The last starts with the rest: its
+// short workgroups, bound by memory, end one by one, and those of the prefix,
+// which start in their places, are then out of step with each other (128
+// sequences of 32K + 500 tokens: 143 us, the prefix first 153, dealt out among
+// each other 167: a CU is filled before the next, so pairs of one kind meet).
+enum { kFewRows = 0, kManyRows = 1, kBesides = 2 };
+constexpr int att_waves(int mode) { return mode == kManyRows ? 2 * kRowWaves : kRowWaves; }
 
-template <bool BF, int D, int PARTS, bool ROWS>
-__global__ __launch_bounds__(att_waves(ROWS) * kWave, 2) void attend_kernel(AttendArgs a) {
+template <bool BF, int D, int PARTS, int MODE>
+__global__ __launch_bounds__(att_waves(MODE) * kWave, 2) void attend_kernel(AttendArgs a) {
   extern __shared__ __align__(1024) char smem[];
   const Block w = block_of(a, blockIdx.x);
-  if constexpr (ROWS) {
-    if (w.pre ? a.pre_rows : a.own_rows) {
-      attend_rows<BF, D, PARTS>(a, w, smem);
-      return;
-    }
+  if constexpr (MODE == kManyRows) {
+    attend_rows<BF, D, PARTS, 2>(a, w, smem);
+  } else if constexpr (MODE == kBesides) {
+    if (w.pre)
+      attend_rows<BF, D, PARTS, 1>(a, w, smem);
+    else
+      attend_tokens<BF, D, PARTS, kRowWaves>(a, w, smem);
+  } else {
+    attend_tokens<BF, D, PARTS, kRowWaves>(a, w, smem);
   }
-  attend_tokens<BF, D, PARTS, att_waves(ROWS)>(a, w, smem);
 }
 
 // Joins the parts of each row. D/4 threads hold 4 coordinates each of a row's
@@ -806,22 +816,25 @@ hipError_t raise_lds(const void* kernel, size_t bytes, std::atomic<uint64_t>& do
   return hipSuccess;
 }
 
-template <bool BF, int D, int PARTS>
-hipError_t launch(const AttendArgs& a, long long items, hipStream_t st) {
-  if (a.pre_rows || a.own_rows) {
-    auto* f = attend_kernel<BF, D, PARTS, true>;
-    constexpr size_t few = sizeof(TokensLds<D, att_waves(true)>);
-    constexpr size_t many = sizeof(RowsLds<BF, D, PARTS>);
-    constexpr size_t lds = few > many ? few : many;
+template <bool BF, int D, int PARTS, int MODE>
+hipError_t launch_mode(const AttendArgs& a, long long items, hipStream_t st) {
+  constexpr size_t few = sizeof(TokensLds<D, kRowWaves>);
+  constexpr size_t many = sizeof(RowsLds<BF, D, PARTS, MODE == kManyRows ? 2 : 1>);
+  constexpr size_t lds = MODE == kFewRows || few > many ? few : many;
+  auto* f = attend_kernel<BF, D, PARTS, MODE>;
+  if (lds > 64 * 1024) {
     static std::atomic<uint64_t> raised{0};  // devices whose kernel has the limit
     if (hipError_t e = raise_lds(reinterpret_cast<const void*>(f), lds, raised)) return e;
-    hipLaunchKernelGGL(f, dim3((unsigned)items), dim3(att_waves(true) * kWave), lds, st, a);
-  } else {
-    hipLaunchKernelGGL((attend_kernel<BF, D, PARTS, false>), dim3((unsigned)items),
-                       dim3(att_waves(false) * kWave), sizeof(TokensLds<D, att_waves(false)>), st,
-                       a);
   }
+  hipLaunchKernelGGL(f, dim3((unsigned)items), dim3(att_waves(MODE) * kWave), lds, st, a);
   return hipGetLastError();
+}
+
+template <bool BF, int D, int PARTS>
+hipError_t launch(const AttendArgs& a, const AttendPlan& p, hipStream_t st) {
+  if (p.own_rows) return launch_mode<BF, D, PARTS, kManyRows>(a, p.items, st);
+  if (p.pre_rows) return launch_mode<BF, D, PARTS, kBesides>(a, p.items, st);
+  return launch_mode<BF, D, PARTS, kFewRows>(a, p.items, st);
 }
 
 template <int D, int PARTS>
@@ -861,10 +874,10 @@ AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int
   const int many = kRowWaves * 16 * (s.bf16 && q_bf16 ? kRowTiles<true, 1> : kRowTiles<true, 3>);
   p.rows = (long long)s.batch * n * s.num_q_heads;
   const int own = n * s.group, pre = s.batch * s.group;
-  p.own_rows = own >= kAttManyRows;
+  p.own_rows = own >= kAttManyRows;  // (a window's: at most 8 rows beside a prefix)
   p.pre_rows = prefix_pages > 0 && pre >= kAttManyRows;
   // eight waves a CU, four or eight a workgroup
-  const int waves = att_waves(p.own_rows || p.pre_rows);
+  const int waves = att_waves(p.own_rows ? kManyRows : kFewRows);
   const long long want = (long long)8 / waves * kNumCUs;
   p.row_block = p.own_rows ? many : 16;
   p.row_blocks = (own + p.row_block - 1) / p.row_block;
@@ -874,17 +887,18 @@ AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int
   const long long tiles = (seen + TT - 1) / TT + 1 + (sinks + TT - 1) / TT;
   const long long blocks = (long long)s.batch * s.num_kv_heads * p.row_blocks;
   // a workgroup's tokens: at least one tile a wave, or two stages a group
-  const int few = waves, many_tiles = 4 * kRowGroups;
+  const int few = waves, many_tiles = waves;
   if (prefix_pages > 0) {
     p.pre_block = p.pre_rows ? many : 16;
     const long long pre_blocks =
         (long long)s.num_kv_heads * ((pre + p.pre_block - 1) / p.pre_block);
     p.pre_splits = splits_for(pre_blocks, (prefix + TT - 1) / TT, want,
                               p.pre_rows ? many_tiles : few);
-    p.pre_items = pre_blocks * p.pre_splits;
+    p.items = pre_blocks * p.pre_splits;
   }
   p.splits = total > prefix ? splits_for(blocks, tiles, want, p.own_rows ? many_tiles : few) : 0;
-  p.items = p.pre_items + blocks * p.splits;
+  p.own_items = blocks * p.splits;
+  p.items += p.own_items;
   p.slots = p.pre_splits + p.splits;
   if (p.slots > 1) {
     const size_t parts = (size_t)p.rows * p.slots;
@@ -923,19 +937,17 @@ hipError_t launch_attend(const LaunchShape& s, const AttendPlan& p, const void* 
   a.prefix = prefix_pages * s.page_size;
   a.pre_block = p.pre_block;
   a.pre_splits = p.pre_splits;
-  a.pre_items = (int)p.pre_items;
   a.row_block = p.row_block;
   a.row_blocks = p.row_blocks;
   a.splits = p.splits;
   a.slots = p.slots;
-  a.pre_rows = p.pre_rows;
-  a.own_rows = p.own_rows;
-  if (!s.bf16) return s.head_dim == 64 ? launch<false, 64, 3>(a, p.items, st)
-                                       : launch<false, 128, 3>(a, p.items, st);
-  if (q_bf16) return s.head_dim == 64 ? launch<true, 64, 1>(a, p.items, st)
-                                      : launch<true, 128, 1>(a, p.items, st);
-  return s.head_dim == 64 ? launch<true, 64, 3>(a, p.items, st)
-                          : launch<true, 128, 3>(a, p.items, st);
+  a.own_items = (int)p.own_items;
+  if (!s.bf16) return s.head_dim == 64 ? launch<false, 64, 3>(a, p, st)
+                                       : launch<false, 128, 3>(a, p, st);
+  if (q_bf16) return s.head_dim == 64 ? launch<true, 64, 1>(a, p, st)
+                                      : launch<true, 128, 1>(a, p, st);
+  return s.head_dim == 64 ? launch<true, 64, 3>(a, p, st)
+                          : launch<true, 128, 3>(a, p, st);
 }
 
 hipError_t launch_join(const LaunchShape& s, const AttendPlan& p, bool q_bf16, void* out,

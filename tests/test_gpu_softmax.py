@@ -295,9 +295,10 @@ def test_prefix(kv, qt, D, ps, Hkv, G, B, pages):
     check(c, q, out, lse, *reference(c, q, lens, 1 << 30, 0, B * G))
 
 
-def test_prefix_is_the_whole_table():
+@pytest.mark.parametrize("times", [1, 15])
+def test_prefix_is_the_whole_table(times):
     P = 4 * 16
-    c = Cache(12, [P, P, 20], 1, 64, 16, "bf16", prefix_pages=4, max_pages=4)
+    c = Cache(12, [P, P, 20] * times, 1, 64, 16, "bf16", prefix_pages=4, max_pages=4)
     q = c.query(1, 4, "f32")
     announce("prefix whole table")
     out, lse = run_prefix(c, q, 4)
