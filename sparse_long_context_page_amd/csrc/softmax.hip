@@ -855,10 +855,16 @@ hipError_t join(const AttendPlan& p, const float* o, const float* ml, void* out,
 
 }  // namespace
 
-// Parts of a row block's tokens: enough workgroups for `want` in all, each of
-// at least `least` tiles.
+// Parts of a row block's tokens: as many as make `want` workgroups in all (a
+// full CU each), of at least `least` tiles. One part more where the CUs then
+// share the blocks out more evenly by a fifth (300 blocks: 3 halves instead of
+// 2 wholes on the fullest CU). Never just over `want` (56 blocks of the float32
+// window in 10 parts, 560 workgroups: 18.6 us, in 9: 15.9).
 static int splits_for(long long blocks, long long tiles, long long want, int least) {
-  long long s = (want + blocks - 1) / blocks;
+  const auto share = [&](long long s) { return (double)((blocks * s + kNumCUs - 1) / kNumCUs) / s; };
+  long long s = want / blocks;
+  if (s < 1) s = 1;
+  if (share(s + 1) < 0.8 * share(s)) ++s;
   const long long most = (tiles + least - 1) / least;
   if (s > most) s = most;
   if (s > kAttMaxSplits) s = kAttMaxSplits;
