@@ -289,6 +289,7 @@ struct AttendPlan {
   long long rows = 0, items = 0, own_items = 0;
   int pre_block = 0, pre_splits = 0, row_block = 0, row_blocks = 0, splits = 0, slots = 0;
   bool pre_rows = false, own_rows = false;  // the many-rows form, per part
+  bool alone = false;                       // few rows and tokens: nothing to join
   size_t ml_off = 0, ws_bytes = 0;
 };
 AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int sinks,

@@ -30,6 +30,7 @@ namespace ekv {
 namespace {
 
 constexpr float kSlack = 6.0f;
+constexpr long long kAloneBytes = 160 * 1024;
 
 struct AttendArgs {
   const void* q;
@@ -704,8 +705,10 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
 // which start in their places, are then out of step with each other (128
 // sequences of 32K + 500 tokens: 143 us, the prefix first 153, dealt out among
 // each other 167: a CU is filled before the next, so pairs of one kind meet).
-enum { kFewRows = 0, kManyRows = 1, kBesides = 2 };
-constexpr int att_waves(int mode) { return mode == kManyRows ? 2 * kRowWaves : kRowWaves; }
+enum { kFewRows = 0, kManyRows = 1, kBesides = 2, kFewAlone = 3 };
+constexpr int att_waves(int mode) {
+  return mode == kManyRows || mode == kFewAlone ? 2 * kRowWaves : kRowWaves;
+}
 
 template <bool BF, int D, int PARTS, int MODE>
 __global__ __launch_bounds__(att_waves(MODE) * kWave, 2) void attend_kernel(AttendArgs a) {
@@ -719,7 +722,7 @@ __global__ __launch_bounds__(att_waves(MODE) * kWave, 2) void attend_kernel(Atte
     else
       attend_tokens<BF, D, PARTS, kRowWaves>(a, w, smem);
   } else {
-    attend_tokens<BF, D, PARTS, kRowWaves>(a, w, smem);
+    attend_tokens<BF, D, PARTS, att_waves(MODE)>(a, w, smem);
   }
 }
 
@@ -818,9 +821,9 @@ hipError_t raise_lds(const void* kernel, size_t bytes, std::atomic<uint64_t>& do
 
 template <bool BF, int D, int PARTS, int MODE>
 hipError_t launch_mode(const AttendArgs& a, long long items, hipStream_t st) {
-  constexpr size_t few = sizeof(TokensLds<D, kRowWaves>);
+  constexpr size_t few = sizeof(TokensLds<D, MODE == kFewAlone ? att_waves(MODE) : kRowWaves>);
   constexpr size_t many = sizeof(RowsLds<BF, D, PARTS, MODE == kManyRows ? 2 : 1>);
-  constexpr size_t lds = MODE == kFewRows || few > many ? few : many;
+  constexpr size_t lds = MODE == kFewRows || MODE == kFewAlone || few > many ? few : many;
   auto* f = attend_kernel<BF, D, PARTS, MODE>;
   if (lds > 64 * 1024) {
     static std::atomic<uint64_t> raised{0};  // devices whose kernel has the limit
@@ -834,6 +837,7 @@ template <bool BF, int D, int PARTS>
 hipError_t launch(const AttendArgs& a, const AttendPlan& p, hipStream_t st) {
   if (p.own_rows) return launch_mode<BF, D, PARTS, kManyRows>(a, p.items, st);
   if (p.pre_rows) return launch_mode<BF, D, PARTS, kBesides>(a, p.items, st);
+  if (p.alone) return launch_mode<BF, D, PARTS, kFewAlone>(a, p.items, st);
   return launch_mode<BF, D, PARTS, kFewRows>(a, p.items, st);
 }
 
@@ -903,6 +907,12 @@ AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int
     p.items = pre_blocks * p.pre_splits;
   }
   p.splits = total > prefix ? splits_for(blocks, tiles, want, p.own_rows ? many_tiles : few) : 0;
+  // few tokens (K and V of a block in one or two loads of eight waves): one
+  // part, of a workgroup of eight waves, and no join (window of 64 at 128 bf16
+  // dims 8.1 -> 6.2 us, of 256 8.6 -> 8.0; of 512 8.9 against 10.0)
+  p.alone = !prefix_pages && !p.own_rows && p.splits > 1 &&
+            tiles * (2 * TT * s.head_dim * (s.bf16 ? 2 : 4)) <= kAloneBytes;
+  if (p.alone) p.splits = 1;
   p.own_items = blocks * p.splits;
   p.items += p.own_items;
   p.slots = p.pre_splits + p.splits;

@@ -142,6 +142,11 @@ def run_window(c, q, window, sinks, **kw):
     ("bf16", "f32", 64, 32, 2, 2, 70, 2**31 - 1, 0),
     ("f32", "f32", 64, 16, 1, 8, 9, 100, 17),
     ("bf16", "bf16", 128, 32, 1, 1, 140, 64, 1),
+    # few tokens a block: one part, eight waves
+    ("bf16", "bf16", 128, 16, 1, 4, 1, 200, 4),
+    ("bf16", "f32", 64, 32, 2, 8, 1, 300, 0),
+    ("f32", "f32", 128, 16, 1, 2, 2, 60, 1),
+    ("f32", "f32", 64, 64, 1, 4, 1, 1, 0),
 ])
 def test_window(kv, qt, D, ps, Hkv, G, n, window, sinks):
     # lengths of 0 and 1, around a page, a tile and several splits
