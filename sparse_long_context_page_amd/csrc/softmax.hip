@@ -32,6 +32,20 @@ namespace {
 constexpr float kSlack = 6.0f;
 constexpr long long kAloneBytes = 160 * 1024;
 
+// Division of x < 2^31 by a positive constant: the quotient from the
+// reciprocal is at most one short.
+struct Divisor {
+  uint32_t d, r;
+};
+Divisor divisor(int d) {
+  const uint64_t r = (1ull << 32) / (uint32_t)(d < 1 ? 1 : d);
+  return Divisor{(uint32_t)(d < 1 ? 1 : d), r > 0xffffffffull ? 0xffffffffu : (uint32_t)r};
+}
+__device__ __forceinline__ int quotient(int x, const Divisor& v) {
+  const uint32_t q = __umulhi((uint32_t)x, v.r);
+  return (int)(q + ((uint32_t)x - q * v.d >= v.d ? 1u : 0u));
+}
+
 struct AttendArgs {
   const void* q;
   const void* k_pool;
@@ -47,6 +61,7 @@ struct AttendArgs {
   int window, sinks;
   int prefix;                                  // tokens of the shared prefix (0: none)
   int pre_block, pre_splits;                   // rows per block and splits of the prefix part
+  Divisor by_hkv, by_pre_splits, by_blocks, by_splits;
   int row_block, row_blocks, splits;           // of the sequences' own part
   int slots;                                   // parts per row
   int own_items;                               // workgroups of that part: the first
@@ -66,20 +81,21 @@ __device__ __forceinline__ Block block_of(const AttendArgs& a, int item) {
   Block w;
   w.pre = item >= a.own_items;
   if (w.pre) item -= a.own_items;
-  w.g = item % a.Hkv;
-  int x = item / a.Hkv;
+  int x = quotient(item, a.by_hkv);
+  w.g = item - x * a.Hkv;
   if (w.pre) {
+    const int y = quotient(x, a.by_pre_splits);
     w.b = 0;
-    w.split = x % a.pre_splits;
-    w.r0 = x / a.pre_splits * a.pre_block;
+    w.split = x - y * a.pre_splits;
+    w.r0 = y * a.pre_block;
     w.nrows = min(a.pre_block, (a.batch << a.g_bits) - w.r0);
     w.splits = a.pre_splits;
     w.slot = w.split;
   } else {
-    w.split = x % a.splits;
-    x /= a.splits;
-    w.r0 = x % a.row_blocks * a.row_block;
-    w.b = x / a.row_blocks;
+    const int y = quotient(x, a.by_splits);
+    w.split = x - y * a.splits;
+    w.b = quotient(y, a.by_blocks);
+    w.r0 = (y - w.b * a.row_blocks) * a.row_block;
     w.nrows = min(a.row_block, (a.n << a.g_bits) - w.r0);
     w.splits = a.splits;
     w.slot = a.pre_splits + w.split;
@@ -138,10 +154,10 @@ template <bool BF, int D>
 __device__ __forceinline__ Views views_of(const AttendArgs& a, const Block& w) {
   constexpr int kElem = BF ? 2 : 4;
   Views x;
-  const size_t head_off = (size_t)((w.g << a.ps_bits) * D) * kElem;
+  const size_t head_off = ((size_t)w.g << a.ps_bits) * (D * kElem);
   x.k.base = static_cast<const char*>(a.k_pool) + head_off;
   x.v.base = static_cast<const char*>(a.v_pool) + head_off;
-  x.k.page_bytes = x.v.page_bytes = (size_t)((a.Hkv << a.ps_bits) * D) * kElem;
+  x.k.page_bytes = x.v.page_bytes = ((size_t)a.Hkv << a.ps_bits) * (D * kElem);
   x.k.page_size = x.v.page_size = 1 << a.ps_bits;
   x.table = w.pre ? a.prefix_table : a.block_table + (size_t)w.b * a.max_pages;
   return x;
@@ -272,7 +288,7 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
   const int sinks = a.sinks;
   const Span u = w.pre ? span_of_prefix(hi, rl < w.nrows) : span_of(a, L, w.r0, w.nrows);
   const TileSpan span = tile_span<TT>(u.lo, u.hi, sinks);
-  const int per = (span.n + w.splits - 1) / w.splits;
+  const int per = quotient(span.n + w.splits - 1, w.pre ? a.by_pre_splits : a.by_splits);
   const int v0 = min(w.split * per, span.n), v1 = min(v0 + per, span.n);
   const int npages = (u.hi + (1 << a.ps_bits) - 1) >> a.ps_bits;
   const Views x = views_of<BF, D>(a, w);
@@ -479,7 +495,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
   Span all = {0, a.prefix, 0, 0};
   if (!w.pre) all = span_of(a, L, w.r0, w.nrows);
   const TileSpan span = tile_span<ST>(all.lo, all.hi, sinks);
-  const int per = (span.n + w.splits - 1) / w.splits;
+  const int per = quotient(span.n + w.splits - 1, w.pre ? a.by_pre_splits : a.by_splits);
   const int b0 = min(w.split * per, span.n), b1 = min(b0 + per, span.n);
   // stages of this group, and steps that every group makes
   const int steps = (b1 - b0 + GR - 1) / GR;
@@ -956,6 +972,10 @@ hipError_t launch_attend(const LaunchShape& s, const AttendPlan& p, const void* 
   a.row_block = p.row_block;
   a.row_blocks = p.row_blocks;
   a.splits = p.splits;
+  a.by_hkv = divisor(s.num_kv_heads);
+  a.by_pre_splits = divisor(p.pre_splits);
+  a.by_blocks = divisor(p.row_blocks);
+  a.by_splits = divisor(p.splits);
   a.slots = p.slots;
   a.own_items = (int)p.own_items;
   if (!s.bf16) return s.head_dim == 64 ? launch<false, 64, 3>(a, p, st)

@@ -232,6 +232,112 @@ def test_evict_long(L, keep):
     check_evict(c, w, keep, 0, 0)
 
 
+def test_evict_pool_beyond_32_bits():
+    """Old pages at the end of a 4.9 GB pool, new ones before them."""
+    pages, ps, D, L, keep = 300000, 64, 128, 1000, 200
+    k, v = (torch.empty(pages, 1, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    c = Cache(45, (L,), 1, D, ps, "bf16")
+    far = torch.arange(pages - c.mp, pages, dtype=torch.int32)[None]
+    for dst, src in ((k, c.k), (v, c.v)):
+        dst[far[0].long().cuda()] = src[torch.from_numpy(c.table[0]).long()].cuda()
+    shape = E().make_shape(1, 1, 1, D, ps, c.mp, pages, "bf16")
+    nt = torch.full((1, c.mp), -1, dtype=torch.int32)
+    nt[0, :4] = torch.arange(pages - c.mp - 9, pages - c.mp - 5)
+    w = c.rng.random((1, 1, c.mp * ps)).astype(np.float32)
+    kept = torch.empty(1, 1, keep, dtype=torch.int32, device="cuda")
+    nl = torch.empty(1, dtype=torch.int32, device="cuda")
+    ln = torch.tensor([L], dtype=torch.int32, device="cuda")
+    announce("evict large pool")
+    q = c.query(1, 1, "f32")
+    got = torch.zeros(1, 1, c.mp * ps, device="cuda")
+    tau = taus(c, q, 1.0)
+    E().entmaxkv_accumulate_weights(shape, q[:, 0].contiguous().cuda(), k, far.cuda(), ln, 1.0,
+                                    torch.from_numpy(tau).cuda(), 1.0, None, got)
+    E().entmaxkv_evict(shape, k, v, far.cuda(), ln, torch.from_numpy(w).cuda(), keep, 2, 5,
+                       nt.cuda(), kept, nl)
+    torch.cuda.synchronize()
+    ref = S.weights(q[:, 0].double().numpy(), c.np64()[0], c.table, (L,), 1.0,
+                    tau.astype(np.float64), 1 << 30, 0, 1.0, np.zeros_like(w))
+    assert (np.abs(got.double().cpu().numpy() - ref)
+            <= weight_tolerance(c, q, 1.0, ref, np.zeros_like(w), 1.0)).all()
+    want = S.evict_kept(w[0, 0], L, keep, 2, 5)
+    assert kept[0, 0].tolist() == want.tolist() and nl.tolist() == [keep]
+    for x, src in ((k, c.k), (v, c.v)):
+        new = x[nt[0, :4].long().cuda(), 0].cpu().reshape(-1, D)[:keep]
+        old = src[torch.from_numpy(c.table[0, want // ps]).long(), 0, torch.from_numpy(want % ps)]
+        assert torch.equal(new.view(torch.int16), old.view(torch.int16))
+
+
+def test_weights_many_sequences():
+    """More than 64 sequences (the lengths are summed in groups of 64), most of
+    them empty or short, a few long: every workgroup's share crosses ends."""
+    lens = [0] * 70 + [700] + [b % 4 for b in range(80)] + [333, 0, 1200]
+    c = Cache(34, lens, 2, 64, 32, "bf16")
+    q = c.query(1, 4, "bf16")
+    tau = taus(c, q, 1.0)
+    announce("weights many sequences")
+    got = run_weights(c, q, 1.0, tau, None, 1.0)
+    zero = np.zeros(got.shape)
+    ref = S.weights(q[:, 0].double().numpy(), c.np64()[0], c.table, lens, 1.0,
+                    tau.astype(np.float64), 1 << 30, 0, 1.0, zero)
+    tol = weight_tolerance(c, q, 1.0, ref, zero, 1.0)
+    for b, L in enumerate(lens):
+        assert (np.abs(got[b, :, :L] - ref[b, :, :L]) <= tol[b, :, :L]).all(), b
+        assert (got[b, :, L:] == -7.0).all()
+
+
+def test_weights_and_evict_in_a_graph():
+    """Captured once, replayed with other weights and lengths, eager calls in
+    between."""
+    c = Cache(35, (300, 80, 511), 2, 64, 16, "bf16")
+    B, keep, need = 3, 64, 4
+    k, v, bt, ln = c.dev("k", "v", "table", "lens")
+    grow = torch.zeros(B * need, *k.shape[1:], dtype=k.dtype, device="cuda")
+    k, v = torch.cat([k, grow]), torch.cat([v, grow])
+    nt = torch.full((B, c.mp), -1, dtype=torch.int32)
+    nt[:, :need] = torch.arange(c.pages, c.pages + B * need).view(B, need)
+    nt = nt.cuda()
+    shape = E().make_shape(B, 4, 2, 64, 16, c.mp, k.shape[0], "bf16")
+    q = c.query(1, 4, "f32")[:, 0].contiguous().cuda()
+    tau = torch.full((B, 4), 3.0, device="cuda")
+    w = torch.zeros(B, 2, c.mp * 16, device="cuda")
+    kept = torch.empty(B, 2, keep, dtype=torch.int32, device="cuda")
+    nl, nw = torch.empty(B, dtype=torch.int32, device="cuda"), torch.empty_like(w)
+
+    def calls():
+        return [E().Prepared("accumulate_weights", shape, q, k, bt, ln, 1.0, tau, 0.5, w, w),
+                E().Prepared("evict", shape, k, v, bt, ln, w, keep, 2, 9, nt, kept, nl, nw)]
+
+    announce("weights and evict graph")
+    eager = calls()
+    for call in eager:
+        call()
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        captured = calls()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=side):
+            for call in captured:
+                call()
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    for step in range(4):
+        start = torch.rand(w.shape, device="cuda", generator=gen) * 0.1
+        q.normal_(0, 0.3, generator=gen)
+        ln.copy_(torch.tensor([300 - step, 80, 511 - 7 * step], dtype=torch.int32))
+        got = []
+        for run in (g.replay, lambda: [call() for call in eager]):
+            w.copy_(start)
+            k[c.pages:].zero_()
+            v[c.pages:].zero_()
+            torch.cuda.synchronize()
+            run()
+            torch.cuda.synchronize()
+            got.append([x.clone() for x in (w, kept, nl, nw, k[c.pages:], v[c.pages:])])
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+
+
 def test_evict_bad_pages_and_no_weights():
     """A table entry outside the pool, old or new: its slots are not copied."""
     c = Cache(44, (100, 100), 1, 64, 16, "f32")

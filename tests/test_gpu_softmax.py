@@ -235,6 +235,43 @@ def test_pages_that_are_not_there():
     check(c, q, out, lse, ref, ref_lse)
 
 
+@pytest.mark.parametrize("kv,qt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_pages_that_are_not_there_many_rows(kv, qt):
+    """The same for a chunk of queries and for a shared prefix."""
+    L, n = 150, 40
+    c = Cache(8, (L,), 1, 64, 16, kv)
+    gone = (1, 4, 8)
+    for j, bad in zip(gone, (-1, c.pages, 1 << 30)):
+        c.table[0, j] = bad
+    q = c.query(n, 1, qt)
+    announce(f"window invalid pages, many rows {kv}/{qt}")
+    out, lse = run_window(c, q, 90, 3)
+    kk, vv = c.np64()
+    ref, ref_lse, mean_abs = np.zeros(q.shape), np.zeros(q.shape[:-1]), np.zeros(q.shape)
+    for i in range(n):
+        t = np.array([t for t in S.visible(L - n + i, L, 90, 3) if t // 16 not in gone])
+        k, v = S.rows(kk, c.table[0], 0, t), S.rows(vv, c.table[0], 0, t)
+        qi = q[0, i, 0].double().numpy()
+        ref[0, i, 0], ref_lse[0, i, 0] = S.attend(qi, k, v)
+        mean_abs[0, i, 0] = S.attend(qi, k, np.abs(v))[0]
+    check(c, q, out, lse, ref, ref_lse, mean_abs)
+
+    B, P = 36, 6
+    c = Cache(9, [P * 16 + 20] * B, 1, 64, 16, kv, prefix_pages=P)
+    q = c.query(1, 1, qt)
+    c.prefix_table[2], c.prefix_table[5] = -3, c.pages + 5
+    out, lse = run_prefix(c, q, P)
+    kk, vv = c.np64()
+    t = np.array([t for t in range(P * 16 + 20) if t // 16 not in (2, 5)])
+    ref, ref_lse, mean_abs = np.zeros(q.shape), np.zeros(q.shape[:-1]), np.zeros(q.shape)
+    for b in range(B):
+        k, v = S.rows(kk, c.table[b], 0, t), S.rows(vv, c.table[b], 0, t)
+        qb = q[b, 0, 0].double().numpy()
+        ref[b, 0, 0], ref_lse[b, 0, 0] = S.attend(qb, k, v)
+        mean_abs[b, 0, 0] = S.attend(qb, k, np.abs(v))[0]
+    check(c, q, out, lse, ref, ref_lse, mean_abs)
+
+
 def test_extreme_scores():
     """Scores of +-60000 and all equal; a row of zeros."""
     c = Cache(6, (90,), 1, 64, 16, "f32")
@@ -262,6 +299,44 @@ def test_scores_that_rise_late():
         announce(f"window ramp {step}")
         out, lse = run_window(c, q, L, 0)
         check(c, q, out, lse, *S.window_decode(q.double().numpy(), *c.np64(), c.table, (L,), L, 0))
+
+
+@pytest.mark.parametrize("kv,qt,n", [("bf16", "f32", 1), ("bf16", "bf16", 40), ("f32", "f32", 1),
+                                     ("f32", "f32", 35)])
+def test_one_long_sequence_among_many_short(kv, qt, n):
+    """As many row blocks as workgroups are wanted, so one part each: the long
+    one's waves go through their page lists several times."""
+    lens = [9001] + [n + b % 3 for b in range(519 if n == 1 else 299)]
+    c = Cache(24, lens, 1, 64, 16, kv, max_pages=-(-9001 // 16))
+    q = c.query(n, 1, qt)
+    announce(f"window long among short {kv}/{qt} n{n}")
+    out, lse = run_window(c, q, 1 << 30, 0)
+    some = [0, 1, 2, len(lens) - 1]
+    few = Cache.__new__(Cache)
+    few.__dict__.update(c.__dict__)
+    few.lens, few.table = [lens[b] for b in some], c.table[some]
+    check(few, q[some], out[some], lse[some], *reference(few, q[some], few.lens, 1 << 30, 0, n))
+
+
+def test_pool_beyond_32_bits():
+    """Pages at the end of a 4.9 GB pool (2.4e9 values a pool)."""
+    pages, ps, D, L = 300000, 64, 128, 500
+    k, v = (torch.empty(pages, 1, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(25)
+    c = Cache(25, (L,), 1, D, ps, "bf16")
+    far = torch.arange(pages - c.mp, pages, dtype=torch.int32)[None]
+    for dst, src in ((k, c.k), (v, c.v)):
+        dst[far[0].long().cuda()] = src[torch.from_numpy(c.table[0]).long()].cuda()
+    shape = E().make_shape(1, 4, 1, D, ps, c.mp, pages, "bf16")
+    bt, lens = far.cuda(), torch.tensor([L], dtype=torch.int32, device="cuda")
+    announce("softmax large pool")
+    for n, rows in ((1, 4), (20, 80)):
+        q = c.query(n, 4, "f32")
+        out = torch.empty(q.shape, device="cuda")
+        lse = torch.empty(q.shape[:-1], device="cuda")
+        E().entmaxkv_softmax_window(shape, q.cuda(), k, v, bt, lens, 300, 4, out, lse, q_tokens=n)
+        torch.cuda.synchronize()
+        check(c, q, out, lse, *reference(c, q, (L,), 300, 4, rows))
 
 
 # ---------------------------------------------------------------------------
@@ -345,6 +420,34 @@ def test_prefix_equals_window_over_the_same_pages():
     assert torch.allclose(a, b, atol=2e-5, rtol=0) and torch.allclose(la, lb, atol=1e-5, rtol=0)
 
 
+@pytest.mark.parametrize("qt", ["bf16", "f32"])
+def test_long_prefix_for_many(qt):
+    """Workgroups of the prefix part go through their page list more than
+    once; against the window call over each sequence, within both calls'
+    tolerance (bf16: two roundings of the output and one of each weight)."""
+    P, B = 6000 if qt == "f32" else 11300, 900
+    c = Cache(15, [P * 16 + b % 5 for b in range(2)], 1, 64, 16, "bf16", prefix_pages=P)
+    table = np.concatenate([np.tile(c.prefix_table, (B, 1)),
+                            np.tile(c.table[:1, P:], (B, 1))], 1)
+    lens = torch.tensor([P * 16 - 37 * (b % 7) for b in range(B)], dtype=torch.int32).cuda()
+    gen = torch.Generator().manual_seed(3)
+    q = (torch.randn(B, 1, 64, generator=gen) * 0.3).to(
+        torch.bfloat16 if qt == "bf16" else torch.float32).cuda()
+    k, v, pt = c.dev("k", "v", "prefix_table")
+    bt = torch.from_numpy(table.astype(np.int32)).cuda()
+    shape = E().make_shape(B, 1, 1, 64, 16, c.mp, c.pages, "bf16")
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    la, lb = (torch.empty(B, 1, device="cuda") for _ in range(2))
+    announce(f"prefix long {qt}")
+    E().entmaxkv_softmax_prefix(shape, q, k, v, pt, P, bt, lens, a, la)
+    E().entmaxkv_softmax_window(shape, q, k, v, bt, lens, 1 << 30, 0, b, lb)
+    torch.cuda.synchronize()
+    assert torch.allclose(la, lb, atol=2e-5, rtol=0)
+    err = (a.double() - b.double()).abs()
+    # the outputs average about 1e5 values of size 1: |out| is about 1e-2
+    assert err.max() <= (2e-5 if qt == "f32" else 2.0**-7 * b.abs().max().item() + 2.0**-8)
+
+
 # ---------------------------------------------------------------------------
 # how it is called
 
@@ -409,6 +512,27 @@ def test_graph_replays_follow_the_inputs():
             call()
         torch.cuda.synchronize()
         assert torch.equal(got[0], out) and torch.equal(got[1], out2)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with a workspace of its own."""
+    c = Cache(26, [1200 + 9 * b for b in range(12)], 2, 128, 16, "bf16", prefix_pages=20)
+    q = c.query(1, 8, "bf16")
+    announce("softmax two streams")
+    want, _ = run_window(c, q, 700, 4)
+    want2, _ = run_prefix(c, q, 20)
+    k, v, bt, lens, pt = c.dev("k", "v", "table", "lens", "prefix_table")
+    qd = q.cuda()
+    q3 = qd[:, 0].contiguous()
+    outs = [(torch.empty_like(qd), torch.empty_like(q3)) for _ in range(6)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for o, o2 in outs:
+        E().entmaxkv_softmax_window(c.shape(8), qd, k, v, bt, lens, 700, 4, o, stream=streams[0])
+        E().entmaxkv_softmax_prefix(c.shape(8), q3, k, v, pt, 20, bt, lens, o2, stream=streams[1])
+    torch.cuda.synchronize()
+    for o, o2 in outs:
+        assert torch.equal(o, want) and torch.equal(o2, want2[:, 0])
 
 
 def test_full_window_is_the_softmax_full_decode():
