@@ -687,6 +687,100 @@ def gauss_report(args):
                       "cells": cells}))
 
 
+def softmax_report(args):
+    """The softmax and eviction calls on a workload's cache: the full-cache
+    softmax decode beside the full-cache alpha-entmax decode (the comparison
+    the efficiency section of the EntmaxKV page is about), a 4096-token window
+    with 4 sinks, the attention weights of both decodes, and the eviction of
+    three quarters of every cache by them. A sampled head of each decode is
+    re-checked against the oracle."""
+    import torch
+    from oracle import softmax_oracle as S
+    from sparse_long_context_page_amd import entmaxkv as E
+    w = synth.WORKLOADS[args.workload]
+    log = lambda m: (sys.stderr.write(f"[report] {m}\n"), sys.stderr.flush())
+    inp = synth.generate(w, synth.WORKLOAD_SEEDS[w.name])
+    log(f"generated {w.name}")
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    bf16 = w.kv_dtype == "bf16"
+    B, H, G, D, ps = w.batch, w.num_q_heads, w.num_kv_heads, w.head_dim, w.page_size
+    pages, mp = int(inp["num_phys_pages"]), int(inp["max_pages"])
+    lens_np = np.asarray(inp["seq_lens"], np.int64)
+    keep, sinks, recent = max(int(lens_np.max()) // 4, 8), 4, min(64, int(lens_np.max()) // 8)
+    fresh = B * -(-keep // ps)
+
+    def pool(a):
+        t = torch.from_numpy(a.view(np.int16)).to(dev).view(torch.bfloat16) if bf16 else \
+            torch.from_numpy(a).to(dev)
+        return torch.cat([t, torch.zeros((fresh, *t.shape[1:]), dtype=t.dtype, device=dev)])
+
+    q = torch.from_numpy(inp["q"]).to(dev)
+    k, v = pool(inp["k_pool"]), pool(inp["v_pool"])
+    bt = torch.from_numpy(inp["block_table"]).to(dev)
+    lens = torch.from_numpy(inp["seq_lens"]).to(dev)
+    nt = torch.full((B, mp), -1, dtype=torch.int32, device=dev)
+    nt[:, :fresh // B] = torch.arange(pages, pages + fresh, device=dev).view(B, -1)
+    shape = E.make_shape(B, H, G, D, ps, mp, pages + fresh, w.kv_dtype)
+    alpha = args.alpha or w.alphas[0]
+    out, lse = torch.empty((B, 1, H, D), device=dev), torch.empty((B, 1, H), device=dev)
+    oute, tau = torch.empty((B, H, D), device=dev), torch.empty((B, H), device=dev)
+    weights = torch.zeros((B, G, mp * ps), device=dev)
+    kept = torch.empty((B, G, keep), dtype=torch.int32, device=dev)
+    nl, nw = torch.empty((B,), dtype=torch.int32, device=dev), torch.empty_like(weights)
+    ws = E.workspace(shape, 0, E.ENTMAXKV_WS_FULL, dev)
+    window = 4096
+    calls = {
+        "entmax_full": E.Prepared("decode_full", shape, q, k, v, bt, lens, alpha, oute, tau, ws=ws),
+        "softmax_full": E.Prepared("softmax_window", shape, q, k, v, bt, lens, E.FULL_WINDOW, 0,
+                                   out, lse=lse),
+        "weights_entmax": E.Prepared("accumulate_weights", shape, q, k, bt, lens, alpha, tau, 1.0,
+                                     None, weights),
+        "weights_softmax": E.Prepared("accumulate_weights", shape, q, k, bt, lens, 1.0, lse, 1.0,
+                                      weights, weights),
+        "evict": E.Prepared("evict", shape, k, v, bt, lens, weights, keep, sinks, recent, nt, kept,
+                            nl, new_weights=nw),
+        "softmax_window_4096": E.Prepared("softmax_window", shape, q, k, v, bt, lens, window, sinks,
+                                          out, lse=lse),
+    }
+    ev = E.HipEvents(2)
+    flush = torch.empty(1 << 30, dtype=torch.uint8, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    rng = np.random.default_rng(0)
+    kn, vn = (np.asarray(inp[x]) for x in ("k_pool", "v_pool"))
+    if bf16:
+        widen = lambda a: (a.astype(np.uint32) << 16).view(np.float32)
+    else:
+        widen = lambda a: a
+    seen = {"softmax_full": (E.FULL_WINDOW, 0), "softmax_window_4096": (window, sinks)}
+    us, worst = {}, 0.0
+    for name, call in calls.items():
+        ts = []
+        for i in range(args.warmup + args.steps):
+            flush.fill_(i & 255)
+            ev.record(0, stream)
+            call()
+            ev.record(1, stream)
+            torch.cuda.synchronize()
+            ts.append(ev.elapsed_ms(0, 1) * 1e3)
+        us[name] = round(float(np.median(ts[args.warmup:])), 2)
+        log(f"{name}: {us[name]} us")
+        if name in seen:
+            b, h = int(rng.integers(0, B)), int(rng.integers(0, H))
+            t = S.visible(int(lens_np[b]) - 1, int(lens_np[b]), *seen[name])
+            rows = [widen(S.rows(x, inp["block_table"][b], h // (H // G), t)) for x in (kn, vn)]
+            ref, _ = S.attend(inp["q"][b, h], *rows)
+            err = float(np.abs(out[b, 0, h].cpu().numpy() - ref).max())
+            worst = max(worst, err / float(np.linalg.norm(ref)))
+    s = 2 if bf16 else 4
+    rows = {"softmax_full": lens_np, "softmax_window_4096": np.minimum(lens_np, window + sinks)}
+    print(json.dumps({"report": "softmax", "workload": w.name, "data": "synthetic", "alpha": alpha,
+                      "steps": args.steps, "warmup": args.warmup, "us": us,
+                      "kv_gbs": {n: round(2 * int(r.sum()) * G * D * s / us[n] / 1e3, 1)
+                                 for n, r in rows.items()},
+                      "kept_tokens": keep, "worst_error_rel_norm": worst}))
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -703,14 +797,18 @@ def main():
                          "(the caches are left holding its dirty lines); 'write_read' fills it "
                          "and then reads a second 1 GiB buffer (the caches are left holding "
                          "clean lines of unrelated data)")
-    ap.add_argument("--report", choices=["containment", "gauss", "mass", "sweep"], default=None,
+    ap.add_argument("--report", choices=["containment", "gauss", "mass", "softmax", "sweep"],
+                    default=None,
                     help="instead of the timed step: 'containment', the alpha/budget sweep "
                          "report of how often the selected pages contain the full-cache support "
                          "(default workload alpha_sweep_64k); 'gauss', the same for the "
                          "Gaussian-aware selection over a grid of margins and caps, with its "
                          "times (default workload long_128k); 'mass', the probability mass "
                          "alpha-entmax and softmax drop outside the selected pages and their "
-                         "output errors, per (alpha, budget) cell; 'sweep', the sparse path "
+                         "output errors, per (alpha, budget) cell; 'softmax', the softmax decode "
+                         "(full and windowed), the attention weights and the eviction by them, "
+                         "timed beside the full alpha-entmax decode (default workload long_128k); "
+                         "'sweep', the sparse path "
                          "timed on every (alpha, budget) cell and the full path on every alpha "
                          "(default workload alpha_sweep_64k); each prints its own JSON line")
     ap.add_argument("--copy-calibration", action="store_true",
@@ -730,6 +828,9 @@ def main():
         return
     if args.report == "gauss":
         gauss_report(args)
+        return
+    if args.report == "softmax":
+        softmax_report(args)
         return
     if args.report == "sweep":
         if "--workload" not in sys.argv:
