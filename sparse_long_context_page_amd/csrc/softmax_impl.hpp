@@ -117,7 +117,7 @@ struct Stage {
   static constexpr int kChunks = kRow / 16;
   static constexpr int kBytes = kTokens * kRow;  // of K, and of V
   __device__ __forceinline__ static int swizzle(int r) {
-    return (BF ? (r & 3) << 1 | ((r >> 3) & 1) | ((r >> 4) & 1) << 3 : r & 15) & (kChunks - 1);
+    return (BF ? (r & 3) << 1 | ((r >> 4) & 1) | ((r >> 3) & 1) << 3 : r & 15) & (kChunks - 1);
   }
   __device__ __forceinline__ static int at(int r, int ch) {
     return r * kRow + ((ch ^ swizzle(r)) << 4);
