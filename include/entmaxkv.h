@@ -338,7 +338,8 @@ int entmaxkv_decode_full(const entmaxkv_shape* shape, const float* q, const void
  * one whose visible scores are all -inf. What lies in hidden tokens' rows, in
  * page tails and in pages that no query sees has no effect, NaN and
  * infinities included; a visible key or value that is not finite makes the
- * outputs it enters not finite.
+ * outputs it enters not finite. Scores of bf16 queries stay below 2^127 in
+ * magnitude (their product with log2 e is formed by itself).
  *   q        q_dtype [batch, q_tokens, num_q_heads, head_dim]
  *   q_dtype  ENTMAXKV_F32, or ENTMAXKV_BF16 with a BF16 cache (else
  *            ENTMAXKV_ERR_UNSUPPORTED)
@@ -420,8 +421,9 @@ int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int3
  * one the first `sinks` tokens, the last `recent` tokens and, of those
  * between, the keep - sinks - recent with the largest weights stay (ties to
  * the lower token; -0 equals +0, a NaN counts as the largest).
- *   keep         1 .. 2^25; sinks, recent >= 0 with sinks + recent <= keep (else
- *                ENTMAXKV_ERR_INVALID)
+ *   keep         >= 1; sinks, recent >= 0 with sinks + recent <= keep (else
+ *                ENTMAXKV_ERR_INVALID); keep <= 2^25 (else
+ *                ENTMAXKV_ERR_UNSUPPORTED)
  *   weights      float32 [batch, num_kv_heads, max_pages_per_seq * page_size]
  *                (16-byte aligned)
  *   new_table    int32 [batch, max_pages_per_seq], the block table afterwards:

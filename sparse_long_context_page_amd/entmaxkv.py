@@ -406,21 +406,29 @@ def _q_dtype(shape: Shape, q) -> int:
                     "bf16 cache")
 
 
+def _int32(value) -> int:
+    """`value` as an int that the C argument holds (ctypes would wrap it)."""
+    value = int(value)
+    if not -2**31 <= value < 2**31:
+        raise ValueError(f"{value} is beyond int32")
+    return value
+
+
 def _max_tokens(shape: Shape) -> int:
     return shape.max_pages_per_seq * shape.page_size
 
 
 def entmaxkv_softmax_window_ws(shape: Shape, q_tokens: int, window: int, sinks: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(lib.entmaxkv_softmax_window_ws(ctypes.byref(shape), int(q_tokens), int(window),
-                                          int(sinks), ctypes.byref(out)),
+    _check(lib.entmaxkv_softmax_window_ws(ctypes.byref(shape), _int32(q_tokens), _int32(window),
+                                          _int32(sinks), ctypes.byref(out)),
            "entmaxkv_softmax_window_ws")
     return int(out.value)
 
 
 def entmaxkv_softmax_prefix_ws(shape: Shape, prefix_pages: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(lib.entmaxkv_softmax_prefix_ws(ctypes.byref(shape), int(prefix_pages),
+    _check(lib.entmaxkv_softmax_prefix_ws(ctypes.byref(shape), _int32(prefix_pages),
                                           ctypes.byref(out)), "entmaxkv_softmax_prefix_ws")
     return int(out.value)
 
@@ -466,8 +474,8 @@ def _args_softmax_window(shape: Shape, q, k_pool, v_pool, block_table, seq_lens,
     need = 0 if ws is not None else entmaxkv_softmax_window_ws(shape, q_tokens, window, sinks)
     pw, nw, ws = _given_or_new(ws, need, q, stream)
     return lib.entmaxkv_softmax_window, [
-        ctypes.byref(shape), pq, qd, int(q_tokens), pk, pv, pbt, pl, int(window), int(sinks), po,
-        pe, pw, nw, _stream(stream, q.device), None], ws
+        ctypes.byref(shape), pq, qd, _int32(q_tokens), pk, pv, pbt, pl, _int32(window),
+        _int32(sinks), po, pe, pw, nw, _stream(stream, q.device), None], ws
 
 
 def _args_softmax_prefix(shape: Shape, q, k_pool, v_pool, prefix_table, prefix_pages,
@@ -480,7 +488,7 @@ def _args_softmax_prefix(shape: Shape, q, k_pool, v_pool, prefix_table, prefix_p
     need = 0 if ws is not None else entmaxkv_softmax_prefix_ws(shape, prefix_pages)
     pw, nw, ws = _given_or_new(ws, need, q, stream)
     return lib.entmaxkv_softmax_prefix, [
-        ctypes.byref(shape), pq, qd, pk, pv, ppt, int(prefix_pages), pbt, pl, po, pe, pw, nw,
+        ctypes.byref(shape), pq, qd, pk, pv, ppt, _int32(prefix_pages), pbt, pl, po, pe, pw, nw,
         _stream(stream, q.device), None], ws
 
 
@@ -499,8 +507,8 @@ def _args_accumulate_weights(shape: Shape, q, k_pool, block_table, seq_lens, alp
     _one_device(q=q, k_pool=k_pool, block_table=block_table, seq_lens=seq_lens, tau=tau,
                 weights_in=weights_in, weights_out=weights_out)
     return lib.entmaxkv_accumulate_weights, [
-        ctypes.byref(shape), pq, qd, pk, pbt, pl, float(alpha), pt, int(window), int(sinks),
-        float(decay), pi, po, _stream(stream, q.device), None]
+        ctypes.byref(shape), pq, qd, pk, pbt, pl, float(alpha), pt, _int32(window),
+        _int32(sinks), float(decay), pi, po, _stream(stream, q.device), None]
 
 
 def _args_evict(shape: Shape, k_pool, v_pool, block_table, seq_lens, weights, keep, sinks, recent,
@@ -520,8 +528,8 @@ def _args_evict(shape: Shape, k_pool, v_pool, block_table, seq_lens, weights, ke
     _one_device(k_pool=k_pool, v_pool=v_pool, block_table=block_table, seq_lens=seq_lens,
                 weights=weights, new_table=new_table, kept=kept, new_lens=new_lens,
                 new_weights=new_weights)
-    return lib.entmaxkv_evict, [ctypes.byref(shape), *ptrs, int(keep), int(sinks), int(recent),
-                                *outs, _stream(stream, k_pool.device), None]
+    return lib.entmaxkv_evict, [ctypes.byref(shape), *ptrs, _int32(keep), _int32(sinks),
+                                _int32(recent), *outs, _stream(stream, k_pool.device), None]
 
 
 def _run(name, fn, args, events):

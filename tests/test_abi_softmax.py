@@ -171,3 +171,27 @@ def test_bf16_queries_need_a_bf16_cache(ek):
     t.update(q=t["q"].bfloat16(), k=t["k"].float(), v=t["v"].float())
     with pytest.raises(TypeError):
         CALLS["window"](ek, f, t)
+
+
+@pytest.mark.parametrize("x", [2**31, -2**31 - 1, 2**32 + 8])
+def test_numbers_beyond_int32_are_refused(ek, x):
+    # (a C argument would hold 2^32 + 8 as a window of 8)
+    s = shape(ek)
+    for call in (lambda: ek.entmaxkv_softmax_window_ws(s, x, 8, 2),
+                 lambda: ek.entmaxkv_softmax_window_ws(s, 1, x, 2),
+                 lambda: ek.entmaxkv_softmax_window_ws(s, 1, 8, x),
+                 lambda: ek.entmaxkv_softmax_prefix_ws(s, x)):
+        with pytest.raises(ValueError, match="int32"):
+            call()
+
+
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_evict_numbers_beyond_int32_are_refused(ek, at, monkeypatch):
+    s, t = _tensors(ek)
+    monkeypatch.setattr(ek, "_one_device", lambda **kw: None)  # host tensors
+    monkeypatch.setattr(ek, "_ptr", lambda *a, **kw: None)
+    n = [20, 2, 3]
+    n[at] += 2**32
+    with pytest.raises(ValueError, match="int32"):
+        ek.entmaxkv_evict(s, t["k"], t["v"], t["bt"], t["lens"], t["w"], *n, t["nt"], t["kept"],
+                          t["nl"])
