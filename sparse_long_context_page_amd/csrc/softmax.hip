@@ -207,7 +207,7 @@ __device__ __forceinline__ void late_tile(const Views& x, TilePages pg, int t0, 
   const bool page_ok = (!BF || c < 2 ? pg.p0 : pg.p1) >= 0;
   KTile<BF, D> kt;
   float p[NZ];
-  kt.template load<true>(x.k, pg, t0, lane);
+  kt.load(x.k, pg, t0, lane);
   kt.template scores<PARTS>(q, p);
 #pragma unroll
   for (int i = 0; i < NZ; ++i) {
@@ -227,7 +227,7 @@ __device__ __forceinline__ void late_tile(const Views& x, TilePages pg, int t0, 
       StageV<BF, D>::template add_slow<PP>(x.v, pg, t0, lane, pf, see, rl == r, acc);
     } else {
       VTile<BF, D> vt;
-      vt.template load<true>(x.v, pg, t0, lane);
+      vt.load(x.v, pg, t0, lane);
 #pragma unroll
       for (int i = 0; i < NZ; ++i)
         if (!(see >> i & 1)) vt.clear(i);
@@ -318,8 +318,8 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
     auto start = [&](int j) { return span.tile(base + j * NW) * TT; };
     TilePages pc = pages(0);
     int t0 = start(0);
-    kt.template load<true>(x.k, pc, t0, lane);
-    vt.template load<true>(x.v, pc, t0, lane);
+    kt.load(x.k, pc, t0, lane);
+    vt.load(x.v, pc, t0, lane);
     uint64_t put_off = 0;
     for (int j = 0; j < nt; ++j) {
       float z[NZ];
@@ -329,7 +329,7 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
       if (j + 1 < nt) {
         pn = pages(j + 1);
         tn = start(j + 1);
-        kt.template load<true>(x.k, pn, tn, lane);
+        kt.load(x.k, pn, tn, lane);
       }
       const bool full = pc.p0 >= 0 && pc.p1 >= 0 &&
                         (t0 + TT <= u.fhi && (t0 >= u.flo || t0 + TT <= sinks));
@@ -369,7 +369,7 @@ __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& 
 #pragma unroll
         for (int n = 0; n < kAcc; ++n) acc[n] = vt.template mul<PP>(n, pf, acc[n]);
       }
-      if (j + 1 < nt) vt.template load<true>(x.v, pn, tn, lane);
+      if (j + 1 < nt) vt.load(x.v, pn, tn, lane);
       pc = pn;
       t0 = tn;
     }

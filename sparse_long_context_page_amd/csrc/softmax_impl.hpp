@@ -59,10 +59,10 @@ __device__ __forceinline__ const char* row_ptr(const KvView& v, const TilePages&
   return v.base + (size_t)max(pg, 0) * v.page_bytes + (size_t)row * kRow;
 }
 
-template <bool kStream, typename T>
+// Read once, so not kept in the caches.
+template <typename T>
 __device__ __forceinline__ T load_vec(const char* p) {
-  if constexpr (kStream) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
-  return *reinterpret_cast<const T*>(p);
+  return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
 }
 
 // ---------------------------------------------------------------------------
@@ -129,7 +129,8 @@ struct Stage {
 
 // One K tile streamed into LDS by one wave for itself, whole rows at a time
 // (a score operand loaded straight from memory touches 64 bytes of 16 rows at
-// once: 5.0 TB/s against 6.x for whole rows). Same layout as a stage.
+// once: the weights of 128K tokens in 51.6 us, 45.5 by whole rows). Same layout
+// as a stage.
 template <bool BF, int D>
 struct WaveTile {
   static constexpr int kBytes = Stage<BF, D>::kBytes / 2;
@@ -217,14 +218,13 @@ struct KTile;
 template <int D>
 struct KTile<true, D> {
   u32x4 f[2][D / 32];
-  template <bool kStream>
   __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0, int lane) {
     const int m = lane & 15, c = lane >> 4;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const char* r = row_ptr<true, D>(v, p, t0, ((m >> 2) << 3) + u * 4 + (m & 3)) + c * 16;
 #pragma unroll
-      for (int s = 0; s < D / 32; ++s) f[u][s] = load_vec<kStream, u32x4>(r + s * 64);
+      for (int s = 0; s < D / 32; ++s) f[u][s] = load_vec<u32x4>(r + s * 64);
     }
   }
   // tile `sub` of a stage
@@ -258,11 +258,10 @@ struct KTile<true, D> {
 template <int D>
 struct KTile<false, D> {
   f32x4 f[D / 16];
-  template <bool kStream>
   __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0, int lane) {
     const char* r = row_ptr<false, D>(v, p, t0, lane & 15) + (lane >> 4) * 16;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) f[s] = load_vec<kStream, f32x4>(r + s * 64);
+    for (int s = 0; s < D / 16; ++s) f[s] = load_vec<f32x4>(r + s * 64);
   }
   __device__ __forceinline__ void read(lds_at st, int sub, int lane) {
     typedef Stage<false, D> St;
@@ -341,12 +340,11 @@ struct VTile<true, D> {
   static constexpr int kAcc = D / 16;
   typedef typename std::conditional<D == 128, u32x4, u32x2>::type vec;
   vec f[8];
-  template <bool kStream>
   __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0, int lane) {
     const int m = lane & 15, c = lane >> 4;
     const char* r = row_ptr<true, D>(v, p, t0, c * 8) + m * (D / 8);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = load_vec<kStream, vec>(r + j * (D * 2));
+    for (int j = 0; j < 8; ++j) f[j] = load_vec<vec>(r + j * (D * 2));
   }
   __device__ __forceinline__ void clear(int j) { f[j] = vec(0); }
   // An infinity or NaN among the values held?
@@ -382,7 +380,6 @@ template <int D>
 struct VTile<false, D> {
   static constexpr int kAcc = D / 16;
   f32x4 f[4][D / 64];
-  template <bool kStream>
   __device__ __forceinline__ void load(const KvView& v, const TilePages& p, int t0, int lane) {
     const int m = lane & 15, c = lane >> 4;
     const char* r = row_ptr<false, D>(v, p, t0, c * 4) + m * 16;
@@ -390,7 +387,7 @@ struct VTile<false, D> {
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
-        f[j][h] = load_vec<kStream, f32x4>(r + j * (D * 4) + h * 256);
+        f[j][h] = load_vec<f32x4>(r + j * (D * 4) + h * 256);
   }
   __device__ __forceinline__ void clear(int j) {
 #pragma unroll
