@@ -61,7 +61,7 @@ struct AttendArgs {
   int window, sinks;
   int prefix;                                  // tokens of the shared prefix (0: none)
   int pre_block, pre_splits;                   // rows per block and splits of the prefix part
-  Divisor by_hkv, by_pre_splits, by_blocks, by_splits;
+  Divisor by_hkv, by_pre_splits, by_pre_blocks, by_blocks, by_splits;
   int row_block, row_blocks, splits;           // of the sequences' own part
   int slots;                                   // parts per row
   int own_items;                               // workgroups of that part: the first
@@ -84,10 +84,10 @@ __device__ __forceinline__ Block block_of(const AttendArgs& a, int item) {
   int x = quotient(item, a.by_hkv);
   w.g = item - x * a.Hkv;
   if (w.pre) {
-    const int y = quotient(x, a.by_pre_splits);
+    // the row blocks that read the same tokens follow each other
+    w.split = quotient(x, a.by_pre_blocks);
     w.b = 0;
-    w.split = x - y * a.pre_splits;
-    w.r0 = y * a.pre_block;
+    w.r0 = (x - w.split * (int)a.by_pre_blocks.d) * a.pre_block;
     w.nrows = min(a.pre_block, (a.batch << a.g_bits) - w.r0);
     w.splits = a.pre_splits;
     w.slot = w.split;
@@ -974,6 +974,8 @@ hipError_t launch_attend(const LaunchShape& s, const AttendPlan& p, const void* 
   a.splits = p.splits;
   a.by_hkv = divisor(s.num_kv_heads);
   a.by_pre_splits = divisor(p.pre_splits);
+  a.by_pre_blocks = divisor(
+      p.pre_block ? (s.batch * s.group + p.pre_block - 1) / p.pre_block : 1);
   a.by_blocks = divisor(p.row_blocks);
   a.by_splits = divisor(p.splits);
   a.slots = p.slots;
