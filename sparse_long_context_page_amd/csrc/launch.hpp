@@ -285,6 +285,17 @@ hipError_t launch_tau_pv_f32(const LaunchShape& s, const SplitPlan& p, const voi
 // by a second kernel when there is more than one per row.
 constexpr int kAttMaxSplits = 256;  // parts of a row block
 constexpr int kAttManyRows = 33;    // rows of a KV head from which the many-rows form runs
+// ... if the few-rows form would have more than so many tiles of 16 rows and
+// 32 tokens (float32: 16). Its workgroups start and end sooner; with 4 query
+// heads a KV head, 8 KV heads, 128 dims, few against many rows in us:
+// 36 rows, window 64 (72 tiles): 7.2 / 11.4 bf16, 9.2 / 16.4 float32; 256 rows,
+// window 256 (1408): 12.7 / 16.7; 36 rows, window 4096 (3096): 16.3 / 15.6; 8
+// sequences, 256 rows, window 64 (5120): 17.2 / 15.0, window 1024: 54.6 / 33.3.
+// Over a shared prefix: 64 rows, 256 tokens (256): 9.9 / 10.8, 1024 tokens
+// (1024): 12.4 / 12.9, 4096 tokens: 19.6 / 17.6; 256 rows of 1 KV head, 4096
+// tokens (2048): 18.2 / 15.7.
+constexpr int kAttFewTiles = 4096;
+constexpr int kAttFewPrefixTiles = 1024;
 struct AttendPlan {
   long long rows = 0, items = 0, own_items = 0;
   int pre_block = 0, pre_splits = 0, row_block = 0, row_blocks = 0, splits = 0, slots = 0;

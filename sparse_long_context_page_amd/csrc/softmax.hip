@@ -12,7 +12,7 @@
 // stays below e^kSlack * tokens, far inside float32, and almost no tile pays
 // for a rescale or a reduction across lanes.
 //
-// Two forms of a workgroup:
+// Two forms of a workgroup (chosen by kAttManyRows and the two bounds after it):
 //  - few rows (attend_tokens): the waves share at most 16 rows and take turns
 //    at the tiles, loaded from memory straight into the operands' registers;
 //    bound by reading K and V.
@@ -900,17 +900,23 @@ AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int
   const int many = kRowWaves * 16 * (s.bf16 && q_bf16 ? kRowTiles<true, 1> : kRowTiles<true, 3>);
   p.rows = (long long)s.batch * n * s.num_q_heads;
   const int own = n * s.group, pre = s.batch * s.group;
-  p.own_rows = own >= kAttManyRows;  // (a window's: at most 8 rows beside a prefix)
-  p.pre_rows = prefix_pages > 0 && pre >= kAttManyRows;
+  // tiles that a block of `rows` of the sequences' own rows can see
+  const auto seen_by = [&](int rows) {
+    const long long span = (long long)window + rows / s.group + 1;
+    const long long seen = total - prefix < span ? total - prefix : span;
+    return (seen + TT - 1) / TT + 1 + (sinks + TT - 1) / TT;
+  };
+  // (a window's: at most 8 rows beside a prefix)
+  p.own_rows = own >= kAttManyRows && (long long)s.batch * s.num_kv_heads * ((own + 15) / 16) *
+                                              seen_by(16) > kAttFewTiles;
+  p.pre_rows = prefix_pages > 0 && pre >= kAttManyRows &&
+               s.num_kv_heads * ((pre + 15) / 16) * (prefix / TT) > kAttFewPrefixTiles;
   // eight waves a CU, four or eight a workgroup
   const int waves = att_waves(p.own_rows ? kManyRows : kFewRows);
   const long long want = (long long)8 / waves * kNumCUs;
   p.row_block = p.own_rows ? many : 16;
   p.row_blocks = (own + p.row_block - 1) / p.row_block;
-  // tokens a row block of the sequences' own part can see
-  const long long span = (long long)window + p.row_block / s.group + 1;
-  const long long seen = total - prefix < span ? total - prefix : span;
-  const long long tiles = (seen + TT - 1) / TT + 1 + (sinks + TT - 1) / TT;
+  const long long tiles = seen_by(p.row_block);
   const long long blocks = (long long)s.batch * s.num_kv_heads * p.row_blocks;
   // a workgroup's tokens: at least one tile a wave, or two stages a group
   const int few = waves, many_tiles = waves;

@@ -11,8 +11,9 @@ denominator), plus the rounding of the running sums: at most 16 per tile or
 part of a row's tokens, each 2^-24 of max |v|. The log of the sum is off by
 ez + 2^-22 plus the roundings of the sum and of the result. A bf16 output adds
 half a step, 2^-8 of its value. With bf16 queries the weights are used to 16
-bits (2^-16 of max |v|), in the many-rows form (33 rows of a KV head) to 8,
-each off by at most 2^-8 of itself: 2^-8 of the weighted mean of |v|.
+bits (2^-16 of max |v|), in the many-rows form (from 33 rows of a KV head, and
+enough work for it) to 8, each off by at most 2^-8 of itself: 2^-8 of the
+weighted mean of |v|. Small cases reach that form among empty sequences.
 """
 import math
 
@@ -105,7 +106,7 @@ def check(c, q, out, lse, ref, ref_lse, mean_abs=0.0):
 
 
 def reference(c, q, lens, window, sinks, rows):
-    """out, lse and, where the many-rows form rounds weights, the weighted mean of |v|."""
+    """out, lse and, where the many-rows form may round weights, the weighted mean of |v|."""
     k, v = c.np64()
     qn = q.double().numpy()
     out, lse = S.window_decode(qn, k, v, c.table, lens, window, sinks)
@@ -114,16 +115,37 @@ def reference(c, q, lens, window, sinks, rows):
                       if rounded else 0.0)
 
 
-def run_window(c, q, window, sinks, **kw):
+def empties(c, q, tiles):
+    """Sequences of length 0 that bring a batch over `tiles` tiles of 16 rows
+    in the few-rows form (at least 2 tiles a block of rows)."""
     n, H = q.shape[1:3]
-    k, v, bt, lens = c.dev("k", "v", "table", "lens")
-    qd = q.cuda()
+    return tiles // (2 * c.Hkv * max(1, n * H // c.Hkv // 16))
+
+
+def padded(c, q, empty):
+    """Shape, q, tables and lengths with `empty` more sequences of length 0."""
+    bt, lens, qd = *c.dev("table", "lens"), q.cuda()
+    bt = torch.cat([bt, bt.new_full((empty, c.mp), -1)])
+    lens = torch.cat([lens, lens.new_zeros(empty)])
+    qd = torch.cat([qd, qd[:1].expand(empty, *qd.shape[1:])])
+    shape = E().make_shape(len(lens), q.shape[2], c.Hkv, c.D, c.ps, c.mp, c.pages, c.kv)
+    return shape, qd, bt, lens
+
+
+def unpadded(B, out, lse):
+    assert (out[B:] == 0).all() and torch.isneginf(lse[B:]).all()
+    return out[:B], lse[:B]
+
+
+def run_window(c, q, window, sinks, empty=0, **kw):
+    k, v = c.dev("k", "v")
+    shape, qd, bt, lens = padded(c, q, empty)
     out = torch.full_like(qd, float("nan"))
-    lse = torch.full(q.shape[:-1], float("nan"), device="cuda")
-    E().entmaxkv_softmax_window(c.shape(H), qd, k, v, bt, lens, window, sinks, out, lse,
-                                q_tokens=n, **kw)
+    lse = torch.full(qd.shape[:-1], float("nan"), device="cuda")
+    E().entmaxkv_softmax_window(shape, qd, k, v, bt, lens, window, sinks, out, lse,
+                                q_tokens=q.shape[1], **kw)
     torch.cuda.synchronize()
-    return out, lse
+    return unpadded(len(q), out, lse)
 
 
 @pytest.mark.parametrize("kv,qt,D,ps,Hkv,G,n,window,sinks", [
@@ -154,8 +176,11 @@ def test_window(kv, qt, D, ps, Hkv, G, n, window, sinks):
     c = Cache(1, lens, Hkv, D, ps, kv)
     q = c.query(n, Hkv * G, qt)
     announce(f"window {kv}/{qt} D{D} ps{ps} Hkv{Hkv} G{G} n{n} W{window} S{sinks}")
-    out, lse = run_window(c, q, window, sinks)
-    check(c, q, out, lse, *reference(c, q, lens, window, sinks, n * G))
+    ref = reference(c, q, lens, window, sinks, n * G)
+    for empty in [0] + ([empties(c, q, 4200)] if n * G >= 33 else []):
+        announce(f"  and {empty} empty sequences")
+        out, lse = run_window(c, q, window, sinks, empty)
+        check(c, q, out, lse, *ref)
 
 
 @pytest.mark.parametrize("kv,qt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
@@ -202,19 +227,20 @@ def test_infinite_value_reaches_only_the_rows_that_see_it(kv, qt, G):
     first = L - n - window + 1
     for t, x in ((L - 1, math.inf), (first, math.nan)):
         c.v[c.table[0, t // 16], :, t % 16, 5] = x
-    announce(f"window infinite values {kv} G{G}")
-    out, lse = run_window(c, q, window, 0)
     ref, ref_lse = S.window_decode(q.double().numpy(), *c.np64(), c.table, (L,), window, 0)
-    o = out.double().cpu().numpy()
-    bad = np.zeros(o.shape, bool)
-    bad[0, 0, :, 5] = bad[0, n - 1, :, 5] = True
-    assert not np.isfinite(o[bad]).any()
-    assert np.isfinite(o[~bad]).all()
-    o[bad] = 0
-    ref = np.where(bad, 0, ref)
     mean_abs = S.window_decode(q.double().numpy(), c.np64()[0], np.abs(c.np64()[1]), c.table,
                                (L,), window, 0)[0] if n * G >= 33 else 0.0
-    check(c, q, torch.from_numpy(o), lse, ref, ref_lse, np.where(bad, 0, mean_abs))
+    for empty in [0] + ([empties(c, q, 4200)] if n * G >= 33 else []):
+        announce(f"window infinite values {kv} G{G}, {empty} empty sequences")
+        out, lse = run_window(c, q, window, 0, empty)
+        o = out.double().cpu().numpy()
+        bad = np.zeros(o.shape, bool)
+        bad[0, 0, :, 5] = bad[0, n - 1, :, 5] = True
+        assert not np.isfinite(o[bad]).any()
+        assert np.isfinite(o[~bad]).all()
+        o[bad] = 0
+        check(c, q, torch.from_numpy(o), lse, np.where(bad, 0, ref), ref_lse,
+              np.where(bad, 0, mean_abs))
 
 
 def test_pages_that_are_not_there():
@@ -245,7 +271,6 @@ def test_pages_that_are_not_there_many_rows(kv, qt):
         c.table[0, j] = bad
     q = c.query(n, 1, qt)
     announce(f"window invalid pages, many rows {kv}/{qt}")
-    out, lse = run_window(c, q, 90, 3)
     kk, vv = c.np64()
     ref, ref_lse, mean_abs = np.zeros(q.shape), np.zeros(q.shape[:-1]), np.zeros(q.shape)
     for i in range(n):
@@ -254,13 +279,14 @@ def test_pages_that_are_not_there_many_rows(kv, qt):
         qi = q[0, i, 0].double().numpy()
         ref[0, i, 0], ref_lse[0, i, 0] = S.attend(qi, k, v)
         mean_abs[0, i, 0] = S.attend(qi, k, np.abs(v))[0]
-    check(c, q, out, lse, ref, ref_lse, mean_abs)
+    for empty in (0, empties(c, q, 4200)):
+        out, lse = run_window(c, q, 90, 3, empty)
+        check(c, q, out, lse, ref, ref_lse, mean_abs)
 
     B, P = 36, 6
     c = Cache(9, [P * 16 + 20] * B, 1, 64, 16, kv, prefix_pages=P)
     q = c.query(1, 1, qt)
     c.prefix_table[2], c.prefix_table[5] = -3, c.pages + 5
-    out, lse = run_prefix(c, q, P)
     kk, vv = c.np64()
     t = np.array([t for t in range(P * 16 + 20) if t // 16 not in (2, 5)])
     ref, ref_lse, mean_abs = np.zeros(q.shape), np.zeros(q.shape[:-1]), np.zeros(q.shape)
@@ -269,7 +295,9 @@ def test_pages_that_are_not_there_many_rows(kv, qt):
         qb = q[b, 0, 0].double().numpy()
         ref[b, 0, 0], ref_lse[b, 0, 0] = S.attend(qb, k, v)
         mean_abs[b, 0, 0] = S.attend(qb, k, np.abs(v))[0]
-    check(c, q, out, lse, ref, ref_lse, mean_abs)
+    for empty in (0, 16 * 1100 // 3):
+        out, lse = run_prefix(c, q, P, empty)
+        check(c, q, out, lse, ref, ref_lse, mean_abs)
 
 
 def test_extreme_scores():
@@ -343,15 +371,16 @@ def test_pool_beyond_32_bits():
 # shared prefix
 
 
-def run_prefix(c, q, pages, **kw):
-    k, v, bt, lens, pt = c.dev("k", "v", "table", "lens", "prefix_table")
+def run_prefix(c, q, pages, empty=0, **kw):
+    k, v, pt = c.dev("k", "v", "prefix_table")
+    shape, qd, bt, lens = padded(c, q, empty)
     bt[:, :pages] = -1  # not read
-    qd = q[:, 0].contiguous().cuda()
+    qd = qd[:, 0].contiguous()
     out = torch.full_like(qd, float("nan"))
     lse = torch.full(qd.shape[:-1], float("nan"), device="cuda")
-    E().entmaxkv_softmax_prefix(c.shape(q.shape[2]), qd, k, v, pt, pages, bt, lens, out, lse, **kw)
+    E().entmaxkv_softmax_prefix(shape, qd, k, v, pt, pages, bt, lens, out, lse, **kw)
     torch.cuda.synchronize()
-    return out[:, None], lse[:, None]
+    return unpadded(len(q), out[:, None], lse[:, None])
 
 
 @pytest.mark.parametrize("kv,qt,D,ps,Hkv,G,B,pages", [
@@ -371,8 +400,11 @@ def test_prefix(kv, qt, D, ps, Hkv, G, B, pages):
     c = Cache(11, lens, Hkv, D, ps, kv, prefix_pages=pages)
     q = c.query(1, Hkv * G, qt)
     announce(f"prefix {kv}/{qt} D{D} ps{ps} Hkv{Hkv} G{G} B{B} pages{pages}")
-    out, lse = run_prefix(c, q, pages)
-    check(c, q, out, lse, *reference(c, q, lens, 1 << 30, 0, B * G))
+    # (as many rows as a KV head needs for the many-rows form, empty sequences)
+    rows = 16 * 1100 // (Hkv * max(1, P // 32))
+    for empty in (0, rows // G):
+        out, lse = run_prefix(c, q, pages, empty)
+        check(c, q, out, lse, *reference(c, q, lens, 1 << 30, 0, B * G + empty * G))
 
 
 @pytest.mark.parametrize("times", [1, 15])
@@ -381,7 +413,7 @@ def test_prefix_is_the_whole_table(times):
     c = Cache(12, [P, P, 20] * times, 1, 64, 16, "bf16", prefix_pages=4, max_pages=4)
     q = c.query(1, 4, "f32")
     announce("prefix whole table")
-    out, lse = run_prefix(c, q, 4)
+    out, lse = run_prefix(c, q, 4, 0 if times == 1 else 4 * 1100)
     check(c, q, out, lse, *S.window_decode(q.double().numpy(), *c.np64(), c.table, c.lens,
                                            1 << 30, 0))
 
@@ -397,8 +429,9 @@ def test_prefix_values_hidden_from_short_sequences(kv, qt, times):
     c.v[c.table[0, 60 // 16], 0, 60 % 16, 7] = math.inf
     q = c.query(1, 2, qt)
     announce(f"prefix infinite value {kv}")
-    out, lse = run_prefix(c, q, 6)
-    ref, ref_lse, mean_abs = reference(c, q, lens, 1 << 30, 0, 2 * len(lens))
+    empty = 0 if times == 1 else 16 * 1100 // 3
+    out, lse = run_prefix(c, q, 6, empty)
+    ref, ref_lse, mean_abs = reference(c, q, lens, 1 << 30, 0, 2 * (len(lens) + empty))
     o = out.double().cpu().numpy()
     sees = np.array(lens) > 60
     assert not np.isfinite(o[sees][..., 7]).any()
