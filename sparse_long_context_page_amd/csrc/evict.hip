@@ -636,9 +636,10 @@ hipError_t launch_evict(const LaunchShape& s, void* k_pool, void* v_pool, const 
   a.sinks = sinks;
   a.recent = recent;
   a.rows = s.batch * s.num_kv_heads;
-  // one workgroup a CU, of 64 slots at least
+  // one workgroup a CU (its registers fill it) and never a few more: 24 rows,
+  // 8000 of 16293 tokens, in 11 parts 70 us, in 10 53; of 64 slots at least
   const int slots = keep < s.max_pages * s.page_size ? keep : s.max_pages * s.page_size;
-  int splits = (kNumCUs + a.rows - 1) / a.rows;
+  int splits = a.rows > kNumCUs ? 1 : kNumCUs / a.rows;
   if (splits > (slots + 63) / 64) splits = (slots + 63) / 64;
   const dim3 grid((unsigned)(a.rows * splits)), block(kEvThreads);
   switch (s.head_dim * (s.bf16 ? 2 : 4)) {
