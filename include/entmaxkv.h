@@ -348,8 +348,11 @@ int entmaxkv_decode_full(const entmaxkv_shape* shape, const float* q, const void
  *   window   >= 1; sinks >= 0; q_tokens >= 1 (else ENTMAXKV_ERR_INVALID);
  *            batch * q_tokens * num_q_heads <= 2^24
  * Products and sums are float32; float32 queries and weights meet bf16 keys
- * and values in exact bf16 parts, so that no product is rounded. The result
- * does not depend on what else runs (no atomics).
+ * and values in exact bf16 parts, so that no product is rounded. With bf16
+ * queries a weight meets its value as two bf16 parts, each the nearest (2^-17
+ * of the weight off; the sum takes it whole), and exp's argument is one
+ * multiply-add (|z| 2^-24 off). Neither depends on the batch, the lengths or
+ * q_tokens, and the result not on what else runs (no atomics).
  * Workspace: entmaxkv_softmax_window_ws bytes for the same arguments (0: ws
  * may be null). Kernels launched: 2 (attention, join of the splits; the
  * second only when the workspace is not 0 bytes).

@@ -20,8 +20,7 @@
 //  - many rows (attend_rows): each wave has row tiles of its own and all walk
 //    the same tokens, staged once per workgroup in LDS by direct loads, one
 //    stage ahead; bound by the matrix cores and the exponentials (2 x 512
-//    queries of 32 heads over 2048 tokens: 34 GFLOP in 54 to 61 us, 0.6
-//    PFLOP/s).
+//    queries of 32 heads over 2048 tokens: 34 GFLOP in 63 us, 0.55 PFLOP/s).
 // The tokens of a row block are split over workgroups; the parts (m_s, l_s,
 // o_s) are joined by a second kernel: out = sum e^(m_s - M) o_s / sum e^(m_s -
 // M) l_s.
@@ -33,6 +32,13 @@ namespace ekv {
 namespace {
 
 constexpr float kSlack = 6.0f;
+
+// bf16 parts of a weight (PFrag) by those of a query, the same in both forms:
+// how a row is rounded does not depend on the batch that it is in. The sum l
+// is of the whole weights.
+template <int PARTS>
+constexpr int kWeightParts = PARTS == 1 ? 2 : 3;
+
 constexpr long long kAloneBytes = 160 * 1024;
 
 // Division of x < 2^31 by a positive constant: the quotient from the
@@ -275,8 +281,7 @@ template <bool BF, int D, int PARTS, int NW>
 __device__ __forceinline__ void attend_tokens(const AttendArgs& a, const Block& w, char* smem) {
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
-  // bf16 queries: weights to 16 bits (the instructions are free here)
-  constexpr int PP = PARTS == 3 ? 3 : 2;
+  constexpr int PP = kWeightParts<PARTS>;
   constexpr int QB = PARTS == 1 ? 2 : 4;
   constexpr int kAcc = VTile<BF, D>::kAcc;
   TokensLds<D, NW>& sh = *reinterpret_cast<TokensLds<D, NW>*>(smem);
@@ -458,9 +463,7 @@ template <bool BF, int D, int PARTS, int GR>
 __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w, char* smem) {
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
-  // bf16 queries: weights rounded to bf16, half a step of at most 2^-8 of
-  // each, as the output's own rounding; the sum l is of the unrounded ones
-  constexpr int PP = PARTS;
+  constexpr int PP = kWeightParts<PARTS>;
   constexpr int QB = PARTS == 1 ? 2 : 4;
   constexpr int RT = kRowTiles<BF, PARTS>;
   constexpr int kAcc = VTile<BF, D>::kAcc;
