@@ -398,6 +398,8 @@ int entmaxkv_softmax_prefix_ws(const entmaxkv_shape* shape, int32_t prefix_pages
  *     alpha > 1  p = [(alpha-1) z_t - tau]_+^(1/(alpha-1)), tau that of
  *                entmaxkv_decode_full (for a sparse decode it is the weight
  *                that its tau gives, on unselected pages too).
+ * A head whose decode saw nothing (alpha = 1: tau = -inf; alpha > 1: tau =
+ * NaN) has p = 0 everywhere.
  * Tokens outside the window and the sinks of position seq_lens[b] - 1 (as in
  * entmaxkv_softmax_window; window >= 1, any larger than the sequences for
  * none) and tokens of invalid pages have p = 0. The sums over heads are

@@ -70,6 +70,8 @@ def weights(q, k_pool, table, lens, alpha, tau, window, sinks, decay, old):
         for h in range(H):
             g = h // (H // G)
             z = rows(k_pool, table[b], g, t).astype(np.float64) @ q[b, h].astype(np.float64)
+            if np.isneginf(tau[b, h]) if alpha == 1.0 else np.isnan(tau[b, h]):
+                continue  # the decode saw nothing
             if alpha == 1.0:
                 p = np.exp(z - tau[b, h])
             else:

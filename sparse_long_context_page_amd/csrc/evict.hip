@@ -70,11 +70,13 @@ __device__ __forceinline__ void weights_of(const WeightArgs& a, int b, int g, in
   kv.page_bytes = (size_t)a.Hkv * a.ps * D * (BF ? 2 : 4);
   kv.page_size = a.ps;
 
-  const bool live = rl < a.G;
+  const bool head = rl < a.G;
   const size_t row = (size_t)b * a.H + g * a.G + rl;
   QFrag<BF, D, PARTS> q;
-  q.load(live ? static_cast<const char*>(a.q) + row * (D * QB) : nullptr, c);
-  const float tau = live ? a.tau[row] : 0.0f;
+  q.load(head ? static_cast<const char*>(a.q) + row * (D * QB) : nullptr, c);
+  const float tau = head ? a.tau[row] : 0.0f;
+  // a head whose decode saw nothing gave no token a weight (exp(z + inf) is not 0)
+  const bool live = head && !(POW == kPowSoftmax ? tau == -INFINITY : tau != tau);
 
   const size_t wrow = ((size_t)b * a.Hkv + g) * ((size_t)a.max_pages * a.ps);
   typedef Butterfly<NZ, 16> Sum;
