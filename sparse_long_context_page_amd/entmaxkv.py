@@ -688,8 +688,9 @@ class Prepared:
         self.name = "entmaxkv_" + name
         self.fn, self.args = r[0], r[1]
         self.keep = (args, kwargs, r[2:] if len(r) > 2 else ())  # keep tensors alive
-        tensors = [t for t in args if isinstance(t, torch.Tensor)]
-        self.device = tensors[0].device.index  # the device that the kernels are launched on
+        tensors = [t for t in (*args, *kwargs.values()) if isinstance(t, torch.Tensor)]
+        # the device that the kernels are launched on (None: there is no other)
+        self.device = tensors[0].device.index if torch.cuda.device_count() > 1 else None
         self._ev_cache = {}
 
     def __call__(self, events=None):
