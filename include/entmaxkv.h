@@ -346,7 +346,8 @@ int entmaxkv_decode_full(const entmaxkv_shape* shape, const float* q, const void
  *   out      q_dtype, the shape of q (16-byte aligned)
  *   lse      float32 [batch, q_tokens, num_q_heads] (nullable)
  *   window   >= 1; sinks >= 0; q_tokens >= 1 (else ENTMAXKV_ERR_INVALID);
- *            batch * q_tokens * num_q_heads <= 2^24
+ *            batch * q_tokens * num_q_heads <= 2^24, batch * num_kv_heads
+ *            < 2^24 (else ENTMAXKV_ERR_UNSUPPORTED)
  * Products and sums are float32; float32 queries and weights meet bf16 keys
  * and values in exact bf16 parts, so that no product is rounded. With bf16
  * queries a weight meets its value as two bf16 parts, each the nearest (2^-17
@@ -378,7 +379,9 @@ int entmaxkv_softmax_window_ws(const entmaxkv_shape* shape, int32_t q_tokens, in
  * page_size in prefix_table's pages; a sequence may be shorter than the
  * prefix, or empty (out = 0, lse = -inf). q and out are q_dtype [batch,
  * num_q_heads, head_dim], lse is [batch, num_q_heads]; everything else as for
- * entmaxkv_softmax_window with q_tokens = 1 and an unlimited window.
+ * entmaxkv_softmax_window with q_tokens = 1 and an unlimited window (batch *
+ * num_kv_heads < 2^23 fits one launch; ENTMAXKV_ERR_UNSUPPORTED where it does
+ * not).
  * Workspace: entmaxkv_softmax_prefix_ws bytes. Kernels launched: 2.
  */
 int entmaxkv_softmax_prefix(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
@@ -427,8 +430,8 @@ int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int3
  * between, the keep - sinks - recent with the largest weights stay (ties to
  * the lower token; -0 equals +0, a NaN counts as the largest).
  *   keep         >= 1; sinks, recent >= 0 with sinks + recent <= keep (else
- *                ENTMAXKV_ERR_INVALID); keep <= 2^25 (else
- *                ENTMAXKV_ERR_UNSUPPORTED)
+ *                ENTMAXKV_ERR_INVALID); keep <= 2^25, batch * num_kv_heads
+ *                < 2^22 (else ENTMAXKV_ERR_UNSUPPORTED)
  *   weights      float32 [batch, num_kv_heads, max_pages_per_seq * page_size]
  *                (16-byte aligned)
  *   new_table    int32 [batch, max_pages_per_seq], the block table afterwards:

@@ -317,9 +317,11 @@ int check_q_dtype(const LaunchShape& s, int32_t q_dtype) {
   return q_dtype == ENTMAXKV_BF16 && !s.bf16 ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
 }
 
-int check_plan(const AttendPlan& p) {
-  return p.items > 0x7fffffffLL ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
+// A launch holds fewer than 2^32 threads.
+int check_grid(long long groups, int threads) {
+  return groups * threads > 0xffffffffLL ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
 }
+int check_plan(const AttendPlan& p) { return check_grid(p.items, p.threads); }
 
 // The plan of a call; q_dtype < 0: of whichever query type needs the larger
 // workspace.
@@ -732,6 +734,7 @@ int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int3
   if ((rc = check_q_dtype(s, q_dtype))) return rc;
   if (!isfinite(alpha) || !(alpha >= 1.0f) || !isfinite(decay)) return ENTMAXKV_ERR_INVALID;
   if ((rc = check_window(&window, &sinks))) return rc;
+  if ((rc = check_grid(s.num_kv_heads, kWeightWaves * kWave))) return rc;
   if (!q || !k_pool || !block_table || !seq_lens || !tau || !weights_out)
     return ENTMAXKV_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(k_pool, 16)) return ENTMAXKV_ERR_INVALID;
@@ -755,6 +758,7 @@ int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
   if (keep <= 0 || sinks < 0 || recent < 0 || (long long)sinks + recent > keep)
     return ENTMAXKV_ERR_INVALID;
   if (keep > kMaxWindow) return ENTMAXKV_ERR_UNSUPPORTED;
+  if ((rc = check_grid((long long)s.batch * s.num_kv_heads, kEvThreads))) return rc;
   if (!k_pool || !v_pool || !block_table || !seq_lens || !weights || !new_table || !kept ||
       !new_lens)
     return ENTMAXKV_ERR_INVALID;

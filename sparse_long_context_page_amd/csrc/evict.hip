@@ -49,8 +49,6 @@ __device__ __forceinline__ float weight_of(float z, float tau, float am1, float 
   return x == 0.0f ? 0.0f : exp2f(m * log2f(x));
 }
 
-constexpr int kWeightWaves = 4;
-
 // Tiles [v0, v1) of sequence b.
 template <bool BF, int D, int PARTS, int POW>
 __device__ __forceinline__ void weights_of(const WeightArgs& a, int b, int g, int L, int v0,
@@ -193,7 +191,6 @@ __global__ __launch_bounds__(kWeightWaves* kWave) void weights_kernel(WeightArgs
 // again for each pass. The copy is bound by memory: kept rows of K and V read
 // and written once.
 
-constexpr int kEvThreads = 1024;
 constexpr int kEvWaves = kEvThreads / kWave;
 constexpr int kDigit = 11;
 constexpr int kBins = 1 << kDigit;

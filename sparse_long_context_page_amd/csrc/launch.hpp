@@ -301,6 +301,7 @@ struct AttendPlan {
   int pre_block = 0, pre_splits = 0, row_block = 0, row_blocks = 0, splits = 0, slots = 0;
   bool pre_rows = false, own_rows = false;  // the many-rows form, per part
   bool alone = false;                       // few rows and tokens: nothing to join
+  int threads = 0;                          // of a workgroup
   size_t ml_off = 0, ws_bytes = 0;
 };
 AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int sinks,
@@ -314,6 +315,8 @@ hipError_t launch_join(const LaunchShape& s, const AttendPlan& p, bool q_bf16, v
                        float* lse, void* ws, hipStream_t st);
 
 // Attention weights and eviction (evict.hip).
+constexpr int kWeightWaves = 4;
+constexpr int kEvThreads = 1024;
 hipError_t launch_weights(const LaunchShape& s, const void* q, bool q_bf16, const void* k_pool,
                           const int32_t* bt, const int32_t* lens, float alpha, const float* tau,
                           int window, int sinks, float decay, const float* w_in, float* w_out,

@@ -945,6 +945,10 @@ AttendPlan plan_attend(const LaunchShape& s, bool q_bf16, int n, int window, int
   p.alone = !prefix_pages && !p.own_rows && p.splits > 1 &&
             tiles * (2 * TT * s.head_dim * (s.bf16 ? 2 : 4)) <= kAloneBytes;
   if (p.alone) p.splits = 1;
+  p.threads = kWave * att_waves(p.own_rows  ? kManyRows
+                                : p.pre_rows ? kBesides
+                                : p.alone    ? kFewAlone
+                                             : kFewRows);
   p.own_items = blocks * p.splits;
   p.items += p.own_items;
   p.slots = p.pre_splits + p.splits;
