@@ -392,6 +392,21 @@ int entmaxkv_softmax_prefix(const entmaxkv_shape* shape, const void* q, int32_t 
 int entmaxkv_softmax_prefix_ws(const entmaxkv_shape* shape, int32_t prefix_pages, size_t* bytes);
 
 /*
+ * Which form of the attention kernel a call with these arguments runs:
+ * *form = ENTMAXKV_FORM_FEW_ROWS (a workgroup's waves share 16 rows; bound by
+ * memory) or ENTMAXKV_FORM_MANY_ROWS (every wave has rows of its own, K and V
+ * staged in LDS). prefix_pages = 0: entmaxkv_softmax_window; else
+ * entmaxkv_softmax_prefix, q_tokens, window and sinks ignored, the form that
+ * reads the shared pages. Both hold the precision stated above (the order of
+ * the sums differs); times and a profile's kernel names go by it. Errors as
+ * the calls' own.
+ */
+#define ENTMAXKV_FORM_FEW_ROWS 0
+#define ENTMAXKV_FORM_MANY_ROWS 1
+int entmaxkv_softmax_form(const entmaxkv_shape* shape, int32_t q_dtype, int32_t q_tokens,
+                          int32_t window, int32_t sinks, int32_t prefix_pages, int32_t* form);
+
+/*
  * Attention weight of every cached token, added to a decayed running sum:
  *     weights_out[b, g, t] = decay * weights_in[b, g, t]
  *                            + sum over the query heads h of KV head g of p(h, t)

@@ -722,6 +722,19 @@ int entmaxkv_softmax_prefix(const entmaxkv_shape* shape, const void* q, int32_t 
                        events);
 }
 
+int entmaxkv_softmax_form(const entmaxkv_shape* shape, int32_t q_dtype, int32_t q_tokens,
+                          int32_t window, int32_t sinks, int32_t prefix_pages, int32_t* form) {
+  LaunchShape s;
+  AttendPlan p;
+  int rc = prefix_pages ? prefix_plan(shape, q_dtype, prefix_pages, &s, &p)
+                        : window_plan(shape, q_dtype, q_tokens, &window, &sinks, &s, &p);
+  if (rc) return rc;
+  if ((rc = check_q_dtype(s, q_dtype))) return rc;
+  if (!form) return ENTMAXKV_ERR_INVALID;
+  *form = p.own_rows || p.pre_rows ? ENTMAXKV_FORM_MANY_ROWS : ENTMAXKV_FORM_FEW_ROWS;
+  return ENTMAXKV_OK;
+}
+
 int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
                                 const void* k_pool, const int32_t* block_table,
                                 const int32_t* seq_lens, float alpha, const float* tau,

@@ -12,7 +12,7 @@ The function names match the C ABI:
     entmaxkv_append_page_moments, entmaxkv_gauss_select, entmaxkv_softmax_window,
     entmaxkv_softmax_prefix, entmaxkv_accumulate_weights, entmaxkv_evict,
     entmaxkv_workspace_bytes, entmaxkv_softmax_window_ws, entmaxkv_softmax_prefix_ws,
-    entmaxkv_topk_kernels, entmaxkv_strerror
+    entmaxkv_softmax_form, entmaxkv_topk_kernels, entmaxkv_strerror
 """
 from __future__ import annotations
 
@@ -37,6 +37,8 @@ ENTMAXKV_WS_SPARSE = 1
 ENTMAXKV_WS_FULL = 2
 ENTMAXKV_WS_GAUSS = 3
 ENTMAXKV_WS_TOPK = 4
+ENTMAXKV_FORM_FEW_ROWS = 0
+ENTMAXKV_FORM_MANY_ROWS = 1
 
 # kernels each entry point launches (for per-kernel event timing)
 KERNELS = {"build_page_meta": 1, "append_page_meta": 1, "score_select": 2,
@@ -90,6 +92,7 @@ def _load() -> ctypes.CDLL:
     lib.entmaxkv_softmax_window_ws.argtypes = [SP, I32, I32, I32, ctypes.POINTER(SZ)]
     lib.entmaxkv_softmax_prefix.argtypes = [SP, P, I32, P, P, P, I32, P, P, P, P, P, SZ, P, P]
     lib.entmaxkv_softmax_prefix_ws.argtypes = [SP, I32, ctypes.POINTER(SZ)]
+    lib.entmaxkv_softmax_form.argtypes = [SP, I32, I32, I32, I32, I32, ctypes.POINTER(I32)]
     lib.entmaxkv_accumulate_weights.argtypes = [SP, P, I32, P, P, P, F32, P, I32, I32, F32, P, P,
                                                 P, P]
     lib.entmaxkv_evict.argtypes = [SP, P, P, P, P, P, I32, I32, I32, P, P, P, P, P, P]
@@ -104,7 +107,8 @@ def _load() -> ctypes.CDLL:
                  "entmaxkv_build_page_moments", "entmaxkv_append_page_moments",
                  "entmaxkv_gauss_select", "entmaxkv_softmax_window",
                  "entmaxkv_softmax_window_ws", "entmaxkv_softmax_prefix",
-                 "entmaxkv_softmax_prefix_ws", "entmaxkv_accumulate_weights", "entmaxkv_evict",
+                 "entmaxkv_softmax_prefix_ws", "entmaxkv_softmax_form",
+                 "entmaxkv_accumulate_weights", "entmaxkv_evict",
                  "entmaxkv_workspace_bytes", "entmaxkv_topk_kernels", "entmaxkv_version"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -430,6 +434,18 @@ def entmaxkv_softmax_prefix_ws(shape: Shape, prefix_pages: int) -> int:
     out = ctypes.c_size_t(0)
     _check(lib.entmaxkv_softmax_prefix_ws(ctypes.byref(shape), _int32(prefix_pages),
                                           ctypes.byref(out)), "entmaxkv_softmax_prefix_ws")
+    return int(out.value)
+
+
+def entmaxkv_softmax_form(shape: Shape, q_dtype: int, q_tokens: int = 1,
+                          window: int = FULL_WINDOW, sinks: int = 0,
+                          prefix_pages: int = 0) -> int:
+    """ENTMAXKV_FORM_FEW_ROWS or _MANY_ROWS: the form of the attention kernel
+    that such a window call (prefix_pages 0) or prefix call runs."""
+    out = ctypes.c_int32(0)
+    _check(lib.entmaxkv_softmax_form(ctypes.byref(shape), _int32(q_dtype), _int32(q_tokens),
+                                     _int32(window), _int32(sinks), _int32(prefix_pages),
+                                     ctypes.byref(out)), "entmaxkv_softmax_form")
     return int(out.value)
 
 
