@@ -6,7 +6,7 @@ import torch
 
 from oracle import softmax_oracle as S
 from parity_util import announce
-from test_gpu_evict import run_weights, weight_tolerance
+from test_gpu_evict import check_evict, run_weights, weight_tolerance
 from test_gpu_softmax import Cache, E, run_window
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +48,51 @@ def test_weights_of_heads_that_saw_nothing(kv):
     got = run_weights(c, q3[:, None], 1.5, tau.cpu().numpy(), None, 1.0)
     assert (got[0, :, :L] == 0).all() and np.isfinite(got[1, :, :5]).all()
     assert got[1, 0, :5].sum() > H - 1e-3
+
+
+# ---------------------------------------------------------------------------
+# rows whose keys do not fit the registers (over 32768 competing tokens)
+
+
+def many_kinds(rng, kind, shape):
+    """Weights in which the boundary falls among equals, or among values that
+    need care."""
+    n = shape[-1]
+    w = rng.integers(0, 3, size=shape).astype(np.float32)
+    if kind == "zero":
+        w[:] = 0.0
+        w[..., ::2] = -0.0
+    elif kind == "special":
+        for x in (np.nan, np.inf, -np.inf, -3.0, 1e-42, -1e-42):
+            w[..., rng.integers(0, n, size=n // 9)] = x
+        w[..., 5] = -np.nan
+    elif kind == "wide":
+        w = np.exp2((rng.random(shape) * 80 - 40).astype(np.float32)).astype(np.float32)
+    elif kind == "few digits":  # many equal keys beside close ones
+        w = (1.0 + rng.integers(0, 700, size=shape) * 2.0**-23).astype(np.float32)
+    return w
+
+
+@pytest.mark.parametrize("kind", ["ties", "zero", "special", "wide", "few digits"])
+@pytest.mark.parametrize("L,keep,sinks,recent", [(33007, 9001, 3, 17), (70001, 30000, 7, 1),
+                                                 (70001, 70000, 6, 300)])
+def test_evict_long_rows_of_every_kind(kind, L, keep, sinks, recent):
+    """Competing tokens that begin and end inside a lane's four, ranks among
+    equals across waves, two KV heads, a short sequence beside."""
+    c = Cache(46, (L, 300), 2, 64, 64, "bf16")
+    w = many_kinds(c.rng, kind, (2, 2, c.mp * 64))
+    announce(f"evict long {kind} L{L} keep{keep} sinks{sinks} recent{recent}")
+    check_evict(c, w, keep, sinks, recent)
+
+
+@pytest.mark.parametrize("sinks", [0, 3, 4])
+@pytest.mark.parametrize("over", [-1, 0, 1, 2])
+def test_evict_at_the_register_limit(sinks, over):
+    """From the multiple of 4 at or below `sinks` to the last of the competing
+    tokens: 32768 fit, one more does not."""
+    recent = 5
+    L = 32768 + over + (sinks & ~3) + recent
+    c = Cache(47, (L,), 1, 64, 16, "bf16")
+    w = many_kinds(c.rng, "ties", (1, 1, c.mp * 16))
+    announce(f"evict register limit {over:+d} sinks{sinks}")
+    check_evict(c, w, 12345, sinks, recent)
