@@ -335,7 +335,8 @@ int entmaxkv_decode_full(const entmaxkv_shape* shape, const float* q, const void
  * A window of at least every sequence's length is full attention; sinks may
  * be 0. A query that sees nothing (p < 0: a padded sequence, or q_tokens >
  * seq_lens[b]; every page invalid) gets out = 0 and lse = -inf, and so does
- * one whose visible scores are all -inf. What lies in hidden tokens' rows, in
+ * one whose visible scores are all -inf, of finite queries and keys by
+ * overflow. What lies in hidden tokens' rows, in
  * page tails and in pages that no query sees has no effect, NaN and
  * infinities included; a visible key or value that is not finite makes the
  * outputs it enters not finite. Scores of bf16 queries stay below 2^127 in
@@ -354,9 +355,9 @@ int entmaxkv_decode_full(const entmaxkv_shape* shape, const float* q, const void
  * of the weight off; the sum takes it whole), and exp's argument is one
  * multiply-add (|z| 2^-24 off). Neither depends on the batch, the lengths or
  * q_tokens, and the result not on what else runs (no atomics).
- * Workspace: entmaxkv_softmax_window_ws bytes for the same arguments (0: ws
- * may be null). Kernels launched: 2 (attention, join of the splits; the
- * second only when the workspace is not 0 bytes).
+ * Workspace: entmaxkv_softmax_window_ws bytes for the same arguments (enough
+ * for either query type; 0: ws may be null). Kernels launched: 1 (attention),
+ * or 2 where a row's tokens are in several parts (and a join of them).
  */
 int entmaxkv_softmax_window(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
                             int32_t q_tokens, const void* k_pool, const void* v_pool,
@@ -372,8 +373,10 @@ int entmaxkv_softmax_window_ws(const entmaxkv_shape* shape, int32_t q_tokens, in
  * prompt, a document). The shared pages are read once for the whole batch,
  * every sequence's queries as rows of one product.
  *   prefix_table  int32 [prefix_pages]: physical pages of the prefix
- *   block_table   as elsewhere, over whole sequences; its first prefix_pages
- *                 columns are not read
+ *   block_table   as elsewhere, over whole sequences; what its first
+ *                 prefix_pages columns hold has no effect (a workgroup may
+ *                 look them up at the end of the prefix or of a sequence
+ *                 shorter than it, and then hides their tokens)
  *   prefix_pages  1 .. max_pages_per_seq (else ENTMAXKV_ERR_INVALID)
  * Sequence b sees its tokens t < seq_lens[b], token t < prefix_pages *
  * page_size in prefix_table's pages; a sequence may be shorter than the
@@ -421,7 +424,7 @@ int entmaxkv_softmax_form(const entmaxkv_shape* shape, int32_t q_dtype, int32_t 
  * Tokens outside the window and the sinks of position seq_lens[b] - 1 (as in
  * entmaxkv_softmax_window; window >= 1, any larger than the sequences for
  * none) and tokens of invalid pages have p = 0. The sums over heads are
- * float32.
+ * float32. K is read for every token, also for those that the window hides.
  *   q            q_dtype [batch, num_q_heads, head_dim] (types as above)
  *   alpha        >= 1 and finite; decay finite (else ENTMAXKV_ERR_INVALID)
  *   tau          float32 [batch, num_q_heads]

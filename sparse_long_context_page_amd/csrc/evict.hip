@@ -19,7 +19,9 @@ namespace {
 // heads of 128 bf16 dims in 44 us (6.2 TB/s), 8 sequences of 22K to 32K in 84
 // us (5.7 TB/s). The tiles of all sequences, end to end, are shared out evenly
 // over the workgroups of a KV head, whatever the lengths (an equal number of
-// workgroups a sequence: 89 us for the 8). No sum crosses a workgroup.
+// workgroups a sequence: 89 us for the 8). No sum crosses a workgroup. A window
+// hides tokens from the sums, not from the reads (the 8 sequences, window of
+// 4096: 86 us).
 
 struct WeightArgs {
   const void* q;
@@ -188,8 +190,9 @@ __global__ __launch_bounds__(kWeightWaves* kWave) void weights_kernel(WeightArgs
 // whole or holds so few keys that each can be ranked among them. Wave v holds the v-th
 // stretch of the row, four neighbouring tokens a lane and step, in registers
 // where it has at most kRegSteps steps (32768 tokens a row), else it reads it
-// again for each pass. The copy is bound by memory: kept rows of K and V read
-// and written once.
+// again for each pass (about six), in each of the row's workgroups: 32768 of
+// 131072 tokens of 4 sequences in 320 us, 3.5 TB/s of the least bytes. The copy
+// is bound by memory: kept rows of K and V read and written once.
 
 constexpr int kEvWaves = kEvThreads / kWave;
 constexpr int kDigit = 11;
@@ -635,8 +638,11 @@ hipError_t launch_evict(const LaunchShape& s, void* k_pool, void* v_pool, const 
   a.sinks = sinks;
   a.recent = recent;
   a.rows = s.batch * s.num_kv_heads;
-  // one workgroup a CU (its registers fill it) and never a few more: 24 rows,
-  // 8000 of 16293 tokens, in 11 parts 70 us, in 10 53; of 64 slots at least
+  // At most one workgroup a CU (its registers fill it) where the rows allow it:
+  // 24 rows, 8000 of 16293 tokens, in 11 parts 70 us, in 10 53; of 64 slots at
+  // least. From 129 rows a row is one workgroup, however many CUs stay free (4096
+  // of 16384 tokens: 128 rows 4.6 TB/s read and written, 136 rows 4.0), and what
+  // is over a multiple of the CUs runs by itself (256 rows 4.8, 264 rows 3.6).
   const int slots = keep < s.max_pages * s.page_size ? keep : s.max_pages * s.page_size;
   int splits = a.rows > kNumCUs ? 1 : kNumCUs / a.rows;
   if (splits > (slots + 63) / 64) splits = (slots + 63) / 64;

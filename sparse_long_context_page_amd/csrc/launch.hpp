@@ -287,13 +287,20 @@ constexpr int kAttMaxSplits = 256;  // parts of a row block
 constexpr int kAttManyRows = 33;    // rows of a KV head from which the many-rows form runs
 // ... if the few-rows form would have more than so many tiles of 16 rows and
 // 32 tokens (float32: 16). Its workgroups start and end sooner; with 4 query
-// heads a KV head, 8 KV heads, 128 dims, few against many rows in us:
-// 36 rows, window 64 (72 tiles): 7.2 / 11.4 bf16, 9.2 / 16.4 float32; 256 rows,
-// window 256 (1408): 12.7 / 16.7; 36 rows, window 4096 (3096): 16.3 / 15.6; 8
-// sequences, 256 rows, window 64 (5120): 17.2 / 15.0, window 1024: 54.6 / 33.3.
-// Over a shared prefix: 64 rows, 256 tokens (256): 9.9 / 10.8, 1024 tokens
-// (1024): 12.4 / 12.9, 4096 tokens: 19.6 / 17.6; 256 rows of 1 KV head, 4096
-// tokens (2048): 18.2 / 15.7.
+// heads a KV head, 8 KV heads, 128 dims, few against many rows in us, bf16
+// queries / float32 queries / float32 caches (which have about twice the
+// tiles):
+//   36 rows, window 64 (120 tiles)       7.1 : 11.9   7.9 : 11.1    9.0 : 15.6
+//   256 rows, window 256 (1408)         12.3 : 17.4  13.3 : 15.4   14.5 : 20.0
+//   36 rows, window 4096 (3144)         15.4 : 16.4  16.6 : 16.3   23.9 : 24.5
+//   8 x 256 rows, window 64 (5120)      17.7 : 16.3  20.3 : 14.8   30.3 : 21.7
+//   8 x 256 rows, window 1024 (35840)   58.0 : 38.4  60.8 : 39.2    136 : 99
+// over a shared prefix:
+//   64 rows, 256 tokens (256)            9.5 : 11.5  10.4 : 11.9   10.2 : 13.0
+//   64 rows, 1024 tokens (1024)         12.2 : 13.4  13.2 : 13.9   17.5 : 16.2
+//   64 rows, 4096 tokens (4096)         18.9 : 18.0  20.7 : 19.1   28.8 : 30.0
+//   256 rows of 1 KV head, 4096 (2048)  18.6 : 16.1  19.6 : 15.0   21.8 : 21.2
+// (64 dims were not measured: the bounds count tiles, not their bytes.)
 constexpr int kAttFewTiles = 4096;
 constexpr int kAttFewPrefixTiles = 1024;
 struct AttendPlan {

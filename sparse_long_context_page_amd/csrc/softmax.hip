@@ -642,7 +642,7 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
           }
           // matrix instructions before the other wave's exponentials: the two
           // waves of a SIMD, in step after each barrier, then alternate
-          // (8192-token window 203 -> 190 us)
+          // (2 x 512 queries, window of 8192: 224 -> 211 us)
           __builtin_amdgcn_s_setprio(1);
           if (!__builtin_expect(later, 0)) {
 #pragma unroll
@@ -725,8 +725,9 @@ __device__ __forceinline__ void attend_rows(const AttendArgs& a, const Block& w,
 // and the few-rows form over the rest. The last starts with the rest: its
 // short workgroups, bound by memory, end one by one, and those of the prefix,
 // which start in their places, are then out of step with each other (128
-// sequences of 32K + 500 tokens: 143 us, the prefix first 153, dealt out among
-// each other 167: a CU is filled before the next, so pairs of one kind meet).
+// sequences of 32K + 500 tokens: 139 us, the prefix first 149 to 168; dealt out
+// among each other it was a sixth slower too: a CU is filled before the next,
+// so pairs of one kind meet).
 enum { kFewRows = 0, kManyRows = 1, kBesides = 2, kFewAlone = 3 };
 constexpr int att_waves(int mode) {
   return mode == kManyRows || mode == kFewAlone ? 2 * kRowWaves : kRowWaves;
