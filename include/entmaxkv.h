@@ -475,6 +475,100 @@ int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
                    hipEvent_t* events);
 
 /*
+ * Pages, positions and slots for a step's new tokens, from the sequences'
+ * lengths (a step mixes prompt chunks and single tokens; the tokens of all
+ * sequences follow each other as rows, sequence by sequence). Sequence b has
+ * L = seq_lens[b] tokens and brings n = new_tokens[b] (below 0: 0):
+ *   rows         start_b = n_0 + .. + n_(b-1) up to end_b = start_b + n
+ *   needs        ceil((L + n) / page_size) - ceil(L / page_size) pages
+ *   fits         if L + n <= max_pages_per_seq * page_size and end_b <= num_tokens
+ *   is granted   if it fits and either needs no page or the needs of all
+ *                fitting sequences up to b together are within free_count
+ *                (those refused for want of pages counted: no later sequence
+ *                takes the pages that an earlier one lacked)
+ * The free pages are a stack: page i (from 0) needed by all fitting sequences
+ * together, in their order, is free_pages[free_count - 1 - i]; it is written to
+ * block_table at the first column behind the sequence's pages. A sequence that
+ * is not granted keeps its length and table; its rows have no slots.
+ *   num_tokens    rows of the per-token arrays, 1 .. 2^24 - 1
+ *   free_pages    int32 [free_capacity] (nullable if 0); free_count int32 [1],
+ *                 clamped to [0, free_capacity]
+ *   block_table   int32 [batch, max_pages_per_seq], written for the new pages
+ *   new_lens      int32 [batch]: L + n where granted, else L
+ *   token_starts  int32 [batch + 1]: min(start_b, num_tokens), the last one the
+ *                 rows in use; rows behind are padding
+ *   positions     int32 [num_tokens]: L + (row - start_b); 0 in padding
+ *   slots         int32 [num_tokens]: page * page_size + position % page_size;
+ *                 -1 in padding, for a sequence that is not granted and where
+ *                 the page is none of the pool's
+ *   free_left     int32 [1]: free_count minus the pages taken
+ * Of the shape: batch (<= 65536, else ENTMAXKV_ERR_UNSUPPORTED), page_size,
+ * max_pages_per_seq, num_phys_pages. new_lens may be neither seq_lens nor
+ * new_tokens, free_left not free_count (ENTMAXKV_ERR_INVALID). Kernels
+ * launched: 1.
+ */
+int entmaxkv_plan_tokens(const entmaxkv_shape* shape, int32_t num_tokens,
+                         const int32_t* seq_lens, const int32_t* new_tokens,
+                         const int32_t* free_pages, int32_t free_capacity,
+                         const int32_t* free_count, int32_t* block_table, int32_t* new_lens,
+                         int32_t* token_starts, int32_t* positions, int32_t* slots,
+                         int32_t* free_left, hipStream_t stream, hipEvent_t* events);
+
+/*
+ * New tokens' queries, keys and values from a projection's output: RMS norm of
+ * every head of q and k, rotation by position, scaled queries out, keys and
+ * values into their slots of the pools.
+ *   y = x / sqrt(mean(x^2) + eps) * weight   (per head; without weight: y = x)
+ *   pair i < rot_dim / 2 of a head turns by positions[axis_i, token] * freqs[i]:
+ *     (a, b) -> (a cos - b sin, a sin + b cos); a pair is (i, i + rot_dim / 2),
+ *     or (2i, 2i + 1) if interleaved; values from rot_dim on stay
+ *   q_out = q_scale * turned y of q;  K row = turned y of k;  V row = v
+ * in float32 (angles float64), each result rounded once; squares of a head add
+ * up in float32.
+ *   q, k, v       x_dtype [num_tokens, heads, head_dim]; heads of a token are
+ *                 dense, tokens are q_stride / k_stride / v_stride values apart
+ *                 (slices of one projection's output; >= heads * head_dim, else
+ *                 ENTMAXKV_ERR_INVALID); 16-byte aligned, strides too
+ *   q_weight,     float32 [head_dim] each; nullable: no norm
+ *   k_weight
+ *   eps           >= 0 and finite; q_scale finite
+ *   positions     int32 [axes, num_tokens]; axes 1 .. 8. One axis: text. More:
+ *                 say time, height and width of images and video; pair i uses
+ *                 axis pair_axis[i] (int32 [rot_dim / 2], clamped into range;
+ *                 nullable with one axis)
+ *   freqs         float64 [rot_dim / 2], radians a position (nullable if
+ *                 rot_dim is 0: no rotation)
+ *   rot_dim       0 .. head_dim, a multiple of 16 (else ENTMAXKV_ERR_UNSUPPORTED)
+ *   slots         int32 [num_tokens]: page * page_size + row of the page; a token
+ *                 whose slot lies outside the pool is not written there (its
+ *                 q_out is). Two tokens with one slot leave it undefined.
+ *   q_out         q_dtype [num_tokens, num_q_heads, head_dim]; may overlap no input
+ * x_dtype and q_dtype are ENTMAXKV_F32 or ENTMAXKV_BF16, independent of
+ * kv_dtype. Of the shape: the heads, head_dim, page_size, num_phys_pages,
+ * kv_dtype. Page boxes and moments follow by entmaxkv_append_page_meta /
+ * _moments. Kernels launched: 1.
+ */
+typedef struct {
+  int32_t num_tokens; /* 1 .. 2^24 - 1 */
+  int32_t x_dtype;    /* entmaxkv_dtype of q, k and v */
+  int32_t q_dtype;    /* entmaxkv_dtype of q_out */
+  int32_t rot_dim;
+  int32_t axes;
+  int32_t interleaved; /* 0 or 1 */
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  float eps;
+  float q_scale;
+} entmaxkv_append;
+
+int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* append, const void* q,
+                       const void* k, const void* v, const int32_t* positions,
+                       const int32_t* slots, const double* freqs, const int32_t* pair_axis,
+                       const float* q_weight, const float* k_weight, void* q_out, void* k_pool,
+                       void* v_pool, hipStream_t stream, hipEvent_t* events);
+
+/*
  * Workspace size in bytes for `which` (ENTMAXKV_WS_*) at this shape and
  * budget (budget is ignored for ENTMAXKV_WS_FULL). Writes *bytes and returns
  * ENTMAXKV_OK, or an error code for an invalid or unsupported shape.

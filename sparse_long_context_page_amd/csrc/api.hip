@@ -317,6 +317,18 @@ int check_q_dtype(const LaunchShape& s, int32_t q_dtype) {
   return q_dtype == ENTMAXKV_BF16 && !s.bf16 ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
 }
 
+// Token rows of a step, and what the plan and the append take beside them.
+constexpr int32_t kMaxTokens = (1 << 24) - 1;
+constexpr int kMaxPlanBatch = 65536;
+constexpr int kMaxAxes = 8;
+constexpr int64_t kMaxTokenStride = int64_t(1) << 32;
+
+int check_num_tokens(int32_t n) {
+  if (n <= 0) return ENTMAXKV_ERR_INVALID;
+  return n > kMaxTokens ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
+}
+bool known_dtype(int32_t t) { return t == ENTMAXKV_F32 || t == ENTMAXKV_BF16; }
+
 // A launch holds fewer than 2^32 threads.
 int check_grid(long long groups, int threads) {
   return groups * threads > 0xffffffffLL ? ENTMAXKV_ERR_UNSUPPORTED : ENTMAXKV_OK;
@@ -756,6 +768,93 @@ int entmaxkv_accumulate_weights(const entmaxkv_shape* shape, const void* q, int3
   if (launch_weights(s, q, q_dtype == ENTMAXKV_BF16, k_pool, block_table, seq_lens, alpha, tau,
                      window, sinks, decay, weights_in, weights_out, stream) != hipSuccess)
     return ENTMAXKV_ERR_HIP;
+  if (!ev.after(0)) return ENTMAXKV_ERR_HIP;
+  return ENTMAXKV_OK;
+}
+
+int entmaxkv_plan_tokens(const entmaxkv_shape* shape, int32_t num_tokens,
+                         const int32_t* seq_lens, const int32_t* new_tokens,
+                         const int32_t* free_pages, int32_t free_capacity,
+                         const int32_t* free_count, int32_t* block_table, int32_t* new_lens,
+                         int32_t* token_starts, int32_t* positions, int32_t* slots,
+                         int32_t* free_left, hipStream_t stream, hipEvent_t* events) {
+  LaunchShape s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if ((rc = check_num_tokens(num_tokens))) return rc;
+  if (s.batch > kMaxPlanBatch) return ENTMAXKV_ERR_UNSUPPORTED;
+  if (free_capacity < 0 || (free_capacity > 0 && !free_pages)) return ENTMAXKV_ERR_INVALID;
+  if (!seq_lens || !new_tokens || !free_count || !block_table || !new_lens || !token_starts ||
+      !positions || !slots || !free_left)
+    return ENTMAXKV_ERR_INVALID;
+  // outputs that every workgroup reads as inputs
+  if (new_lens == seq_lens || new_lens == new_tokens || free_left == free_count)
+    return ENTMAXKV_ERR_INVALID;
+  const Events ev{events, stream};
+  if (!ev.before(0)) return ENTMAXKV_ERR_HIP;
+  if (launch_plan_tokens(s, num_tokens, seq_lens, new_tokens, free_pages, free_capacity,
+                         free_count, block_table, new_lens, token_starts, positions, slots,
+                         free_left, stream) != hipSuccess)
+    return ENTMAXKV_ERR_HIP;
+  if (!ev.after(0)) return ENTMAXKV_ERR_HIP;
+  return ENTMAXKV_OK;
+}
+
+int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* append, const void* q,
+                       const void* k, const void* v, const int32_t* positions,
+                       const int32_t* slots, const double* freqs, const int32_t* pair_axis,
+                       const float* q_weight, const float* k_weight, void* q_out, void* k_pool,
+                       void* v_pool, hipStream_t stream, hipEvent_t* events) {
+  LaunchShape s;
+  int rc = check_shape(shape, &s);
+  if (rc) return rc;
+  if (!append) return ENTMAXKV_ERR_INVALID;
+  const entmaxkv_append& a = *append;
+  if ((rc = check_num_tokens(a.num_tokens))) return rc;
+  if (!known_dtype(a.x_dtype) || !known_dtype(a.q_dtype)) return ENTMAXKV_ERR_UNSUPPORTED;
+  if (a.rot_dim < 0 || a.rot_dim > s.head_dim || a.axes < 1 || a.axes > kMaxAxes)
+    return ENTMAXKV_ERR_INVALID;
+  if (a.rot_dim % 16) return ENTMAXKV_ERR_UNSUPPORTED;
+  if (a.interleaved != 0 && a.interleaved != 1) return ENTMAXKV_ERR_INVALID;
+  if (!isfinite(a.eps) || a.eps < 0.0f || !isfinite(a.q_scale)) return ENTMAXKV_ERR_INVALID;
+  if (!q || !k || !v || !slots || !q_out || !k_pool || !v_pool) return ENTMAXKV_ERR_INVALID;
+  if (a.rot_dim && (!positions || !freqs || (a.axes > 1 && !pair_axis)))
+    return ENTMAXKV_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(freqs, 8))
+    return ENTMAXKV_ERR_INVALID;
+  const int per16 = a.x_dtype == ENTMAXKV_BF16 ? 8 : 4;
+  const int64_t strides[3] = {a.q_stride, a.k_stride, a.v_stride};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t heads = i ? s.num_kv_heads : s.num_q_heads;
+    if (strides[i] < heads * s.head_dim || strides[i] > kMaxTokenStride || strides[i] % per16)
+      return ENTMAXKV_ERR_INVALID;
+  }
+  AppendParams p;
+  p.x[0] = q;
+  p.x[1] = k;
+  p.x[2] = v;
+  p.out[0] = q_out;
+  p.out[1] = k_pool;
+  p.out[2] = v_pool;
+  for (int i = 0; i < 3; ++i) p.stride[i] = strides[i];
+  p.positions = positions;
+  p.slots = slots;
+  p.freqs = freqs;
+  p.pair_axis = pair_axis;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.num_tokens = a.num_tokens;
+  p.rot_dim = a.rot_dim;
+  p.axes = a.axes;
+  p.interleaved = a.interleaved != 0;
+  p.x_bf16 = a.x_dtype == ENTMAXKV_BF16;
+  p.q_bf16 = a.q_dtype == ENTMAXKV_BF16;
+  p.eps = a.eps;
+  p.q_scale = a.q_scale;
+  const Events ev{events, stream};
+  if (!ev.before(0)) return ENTMAXKV_ERR_HIP;
+  if (launch_append_kv(s, p, stream) != hipSuccess) return ENTMAXKV_ERR_HIP;
   if (!ev.after(0)) return ENTMAXKV_ERR_HIP;
   return ENTMAXKV_OK;
 }

@@ -321,6 +321,28 @@ hipError_t launch_attend(const LaunchShape& s, const AttendPlan& p, const void* 
 hipError_t launch_join(const LaunchShape& s, const AttendPlan& p, bool q_bf16, void* out,
                        float* lse, void* ws, hipStream_t st);
 
+// New tokens into the cache (append.hip).
+hipError_t launch_plan_tokens(const LaunchShape& s, int num_tokens, const int32_t* seq_lens,
+                              const int32_t* new_tokens, const int32_t* free_pages,
+                              int free_capacity, const int32_t* free_count, int32_t* block_table,
+                              int32_t* new_lens, int32_t* token_starts, int32_t* positions,
+                              int32_t* slots, int32_t* free_left, hipStream_t st);
+struct AppendParams {
+  const void* x[3];   // queries, keys, values
+  int64_t stride[3];  // values from a token to the next
+  void* out[3];       // q_out, k_pool, v_pool
+  const int32_t* positions;
+  const int32_t* slots;
+  const double* freqs;
+  const int32_t* pair_axis;
+  const float* q_weight;
+  const float* k_weight;
+  int num_tokens, rot_dim, axes;
+  bool interleaved, x_bf16, q_bf16;
+  float eps, q_scale;
+};
+hipError_t launch_append_kv(const LaunchShape& s, const AppendParams& p, hipStream_t st);
+
 // Attention weights and eviction (evict.hip).
 constexpr int kWeightWaves = 4;
 constexpr int kEvThreads = 1024;

@@ -11,6 +11,7 @@ The function names match the C ABI:
     entmaxkv_decode_full, entmaxkv_build_page_moments,
     entmaxkv_append_page_moments, entmaxkv_gauss_select, entmaxkv_softmax_window,
     entmaxkv_softmax_prefix, entmaxkv_accumulate_weights, entmaxkv_evict,
+    entmaxkv_plan_tokens, entmaxkv_append_kv,
     entmaxkv_workspace_bytes, entmaxkv_softmax_window_ws, entmaxkv_softmax_prefix_ws,
     entmaxkv_softmax_form, entmaxkv_topk_kernels, entmaxkv_strerror
 """
@@ -45,7 +46,7 @@ KERNELS = {"build_page_meta": 1, "append_page_meta": 1, "score_select": 2,
            "score_select_noalloc": 2, "decode_sparse": 2, "decode_topk": 4,
            "decode_full": 2, "build_page_moments": 1, "append_page_moments": 1,
            "gauss_select": 2, "softmax_window": 2, "softmax_prefix": 2, "accumulate_weights": 1,
-           "evict": 1}
+           "evict": 1, "plan_tokens": 1, "append_kv": 1}
 
 FULL_WINDOW = 2**31 - 1  # a window that hides no token
 
@@ -60,6 +61,22 @@ class Shape(ctypes.Structure):
         ("max_pages_per_seq", ctypes.c_int32),
         ("num_phys_pages", ctypes.c_int32),
         ("kv_dtype", ctypes.c_int32),
+    ]
+
+
+class Append(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("q_dtype", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("q_scale", ctypes.c_float),
     ]
 
 
@@ -96,6 +113,8 @@ def _load() -> ctypes.CDLL:
     lib.entmaxkv_accumulate_weights.argtypes = [SP, P, I32, P, P, P, F32, P, I32, I32, F32, P, P,
                                                 P, P]
     lib.entmaxkv_evict.argtypes = [SP, P, P, P, P, P, I32, I32, I32, P, P, P, P, P, P]
+    lib.entmaxkv_plan_tokens.argtypes = [SP, I32, P, P, P, I32, P, P, P, P, P, P, P, P, P]
+    lib.entmaxkv_append_kv.argtypes = [SP, ctypes.POINTER(Append), *[P] * 14]
     lib.entmaxkv_workspace_bytes.argtypes = [SP, I32, I32, ctypes.POINTER(SZ)]
     lib.entmaxkv_topk_kernels.argtypes = [SP, I32, ctypes.POINTER(I32)]
     lib.entmaxkv_strerror.argtypes = [ctypes.c_int]
@@ -108,7 +127,8 @@ def _load() -> ctypes.CDLL:
                  "entmaxkv_gauss_select", "entmaxkv_softmax_window",
                  "entmaxkv_softmax_window_ws", "entmaxkv_softmax_prefix",
                  "entmaxkv_softmax_prefix_ws", "entmaxkv_softmax_form",
-                 "entmaxkv_accumulate_weights", "entmaxkv_evict",
+                 "entmaxkv_accumulate_weights", "entmaxkv_evict", "entmaxkv_plan_tokens",
+                 "entmaxkv_append_kv",
                  "entmaxkv_workspace_bytes", "entmaxkv_topk_kernels", "entmaxkv_version"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -548,6 +568,86 @@ def _args_evict(shape: Shape, k_pool, v_pool, block_table, seq_lens, weights, ke
                                 _int32(recent), *outs, _stream(stream, k_pool.device), None]
 
 
+def _args_plan_tokens(shape: Shape, seq_lens, new_tokens, free_pages, free_count, block_table,
+                      new_lens, token_starts, positions, slots, free_left, stream=None):
+    n = _Sizes(shape)
+    i32 = (torch.int32,)
+    tokens = _tensor(slots, "slots").numel()
+    capacity = 0 if free_pages is None else _tensor(free_pages, "free_pages").numel()
+    ins = [_ptr(seq_lens, "seq_lens", i32, numel=n.batch),
+           _ptr(new_tokens, "new_tokens", i32, numel=n.batch)]
+    pages = _ptr(free_pages, "free_pages", i32, nullable=True)
+    outs = [_ptr(free_count, "free_count", i32, numel=1),
+            _ptr(block_table, "block_table", i32, numel=n.block_table),
+            _ptr(new_lens, "new_lens", i32, numel=n.batch),
+            _ptr(token_starts, "token_starts", i32, numel=n.batch + 1),
+            _ptr(positions, "positions", i32, numel=tokens),
+            _ptr(slots, "slots", i32), _ptr(free_left, "free_left", i32, numel=1)]
+    _one_device(seq_lens=seq_lens, new_tokens=new_tokens, free_pages=free_pages,
+                free_count=free_count, block_table=block_table, new_lens=new_lens,
+                token_starts=token_starts, positions=positions, slots=slots, free_left=free_left)
+    return lib.entmaxkv_plan_tokens, [ctypes.byref(shape), _int32(tokens), *ins, pages,
+                                      _int32(capacity), *outs, _stream(stream, slots.device),
+                                      None]
+
+
+def _tensor(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    return t
+
+
+_DTYPES = {torch.float32: ENTMAXKV_F32, torch.bfloat16: ENTMAXKV_BF16}
+
+
+def _token_rows(t, name, heads, dim, tokens, dtype):
+    """(pointer, values from a token to the next) of [tokens, heads, dim] rows,
+    dense within a token."""
+    _tensor(t, name)
+    if t.dtype != dtype or dtype not in _DTYPES:
+        raise TypeError(f"{name} has dtype {t.dtype}; q, k and v are all float32 or all bfloat16")
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, dim)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    # one token's stride may be anything; it is never used
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if tokens > 1 else heads * dim
+
+
+def _args_append_kv(shape: Shape, q, k, v, positions, slots, q_out, k_pool, v_pool, freqs=None,
+                    pair_axis=None, interleaved=False, q_weight=None, k_weight=None, eps=1e-6,
+                    q_scale=1.0, stream=None):
+    n = _Sizes(shape)
+    tokens, D = _tensor(q, "q").shape[0], shape.head_dim
+    pq, sq = _token_rows(q, "q", shape.num_q_heads, D, tokens, q.dtype)
+    pk, sk = _token_rows(k, "k", shape.num_kv_heads, D, tokens, q.dtype)
+    pv, sv = _token_rows(v, "v", shape.num_kv_heads, D, tokens, q.dtype)
+    if _tensor(q_out, "q_out").dtype not in _DTYPES:
+        raise TypeError(f"q_out has dtype {q_out.dtype}, expected float32 or bfloat16")
+    half = 0 if freqs is None else _tensor(freqs, "freqs").numel()
+    axes = 1
+    if positions is not None:
+        axes = 1 if _tensor(positions, "positions").dim() == 1 else positions.shape[0]
+    if axes > 1 and half and pair_axis is None:
+        raise ValueError("pair_axis is required with several axes")
+    i32, f32 = (torch.int32,), (torch.float32,)
+    pos = _ptr(positions, "positions", i32, nullable=half == 0, numel=axes * tokens)
+    rest = [_ptr(slots, "slots", i32, numel=tokens),
+            _ptr(freqs, "freqs", (torch.float64,), nullable=True),
+            _ptr(pair_axis, "pair_axis", i32, nullable=True, numel=half),
+            _ptr(q_weight, "q_weight", f32, nullable=True, numel=D),
+            _ptr(k_weight, "k_weight", f32, nullable=True, numel=D),
+            _ptr(q_out, "q_out", numel=tokens * shape.num_q_heads * D),
+            _ptr(k_pool, "k_pool", _kv_dtypes(shape), numel=n.pool),
+            _ptr(v_pool, "v_pool", _kv_dtypes(shape), numel=n.pool)]
+    _one_device(q=q, k=k, v=v, positions=positions, slots=slots, freqs=freqs, pair_axis=pair_axis,
+                q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_pool=k_pool, v_pool=v_pool)
+    a = Append(_int32(tokens), _DTYPES[q.dtype], _DTYPES[q_out.dtype], 2 * half, axes,
+               int(bool(interleaved)), sq, sk, sv, float(eps), float(q_scale))
+    return lib.entmaxkv_append_kv, [ctypes.byref(shape), ctypes.byref(a), pq, pk, pv, pos, *rest,
+                                    _stream(stream, q.device), None]
+
+
 def _run(name, fn, args, events):
     if events is not None:
         ev = _events(events)
@@ -680,6 +780,28 @@ def entmaxkv_evict(shape: Shape, k_pool, v_pool, block_table, seq_lens, weights,
     _run_on(k_pool.device, "entmaxkv_evict", fn, args, events)
 
 
+def entmaxkv_plan_tokens(shape: Shape, seq_lens, new_tokens, free_pages, free_count, block_table,
+                         new_lens, token_starts, positions, slots, free_left, stream=None,
+                         events=None):
+    """Pages of the free list for new_tokens more tokens of every sequence;
+    row, position and slot of each. slots' length is the rows of the step."""
+    fn, args = _args_plan_tokens(shape, seq_lens, new_tokens, free_pages, free_count, block_table,
+                                 new_lens, token_starts, positions, slots, free_left, stream)
+    _run_on(slots.device, "entmaxkv_plan_tokens", fn, args, events)
+
+
+def entmaxkv_append_kv(shape: Shape, q, k, v, positions, slots, q_out, k_pool, v_pool, freqs=None,
+                       pair_axis=None, interleaved=False, q_weight=None, k_weight=None, eps=1e-6,
+                       q_scale=1.0, stream=None, events=None):
+    """Norm and rotation of the heads of q and k; queries to q_out, keys and
+    values to their slots. q, k, v: [tokens, heads, head_dim], slices of one
+    tensor allowed; positions: [tokens] or [axes, tokens]; freqs: float64, half
+    as many as the values rotated (None: no rotation)."""
+    fn, args = _args_append_kv(shape, q, k, v, positions, slots, q_out, k_pool, v_pool, freqs,
+                               pair_axis, interleaved, q_weight, k_weight, eps, q_scale, stream)
+    _run_on(q.device, "entmaxkv_append_kv", fn, args, events)
+
+
 class Prepared:
     """An entry point with its arguments marshalled once, for tight loops.
     The tensors must stay alive and unchanged in place while it is used.
@@ -697,7 +819,8 @@ class Prepared:
                "gauss_select": _args_gauss_select,
                "softmax_window": _args_softmax_window,
                "softmax_prefix": _args_softmax_prefix,
-               "accumulate_weights": _args_accumulate_weights, "evict": _args_evict}
+               "accumulate_weights": _args_accumulate_weights, "evict": _args_evict,
+               "plan_tokens": _args_plan_tokens, "append_kv": _args_append_kv}
 
     def __init__(self, name: str, *args, **kwargs):
         r = Prepared._makers[name](*args, **kwargs)
