@@ -569,6 +569,44 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
                        void* v_pool, hipStream_t stream, hipEvent_t* events);
 
 /*
+ * alpha-entmax attention of new tokens of a ragged batch over the paged cache:
+ * prompt chunks of any length beside single tokens ([EntmaxKV page] section 4's
+ * full-cache decode, of many queries at once). Sequence b brings the queries of
+ * its last n_b tokens, rows token_starts[b] .. token_starts[b + 1] - 1, whose
+ * keys and values are in the cache; the i-th is the token at position
+ * p = seq_lens[b] - n_b + i and sees the tokens t <= p. tau, out and support as
+ * for entmaxkv_decode_full: sum_t [(alpha-1) z_t - tau]_+^m = 1 over the seen
+ * tokens, out = sum p_t v_t / sum p_t.
+ *   q, out        q_dtype [num_tokens, num_q_heads, head_dim], 16-byte aligned;
+ *                 ENTMAXKV_F32, or ENTMAXKV_BF16 with a BF16 cache (else
+ *                 ENTMAXKV_ERR_UNSUPPORTED)
+ *   num_tokens    rows of q and out, 1 .. 2^24 - 1
+ *   token_starts  int32 [batch + 1], ascending, in [0, num_tokens] (clamped into
+ *                 it); rows behind the last sequence's are not read or written
+ *   seq_lens      tokens of each sequence, its new ones included
+ *   alpha         > 1, finite (else ENTMAXKV_ERR_INVALID)
+ *   tau           float32 [num_tokens, num_q_heads] (nullable)
+ *   support       int32 [num_tokens, num_q_heads] (nullable)
+ * A row that sees no token (n_b > seq_lens[b]; every page invalid) gets out = 0,
+ * tau = NaN, support = 0, and so does one whose scores are all -inf, by
+ * overflow. What lies in hidden tokens' rows and in page tails has no effect,
+ * NaN and infinities included, nor do values of zero weight; a seen score that
+ * is NaN or +inf makes its row's out and tau NaN. Scores are float32, as in
+ * entmaxkv_softmax_window; weights are used in float32 or to 2^-17 of
+ * themselves (bf16 queries). Results do not depend on what else runs (no
+ * atomics on results).
+ * Workspace: entmaxkv_entmax_chunk_ws bytes, for either query type and any
+ * alpha (0: ws may be null). Kernels launched: 1.
+ */
+int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
+                          int32_t num_tokens, const int32_t* token_starts, const void* k_pool,
+                          const void* v_pool, const int32_t* block_table,
+                          const int32_t* seq_lens, float alpha, void* out, float* tau,
+                          int32_t* support, void* ws, size_t ws_bytes, hipStream_t stream,
+                          hipEvent_t* events);
+int entmaxkv_entmax_chunk_ws(const entmaxkv_shape* shape, int32_t num_tokens, size_t* bytes);
+
+/*
  * Workspace size in bytes for `which` (ENTMAXKV_WS_*) at this shape and
  * budget (budget is ignored for ENTMAXKV_WS_FULL). Writes *bytes and returns
  * ENTMAXKV_OK, or an error code for an invalid or unsupported shape.

@@ -73,10 +73,11 @@ def rotate(x, positions, freqs, pair_axis=None, interleaved=False):
     return x
 
 
-def chunk(q, token_starts, k_pool, v_pool, table, seq_lens, alpha):
+def chunk(q, token_starts, k_pool, v_pool, table, seq_lens, alpha, each=None):
     """q [rows, heads, dim]; returns out, tau (NaN for a row that sees nothing),
     support, all of q's rows; rows of no sequence stay NaN. A page outside the
-    pool is empty."""
+    pool is empty. each(row, head, scores): called for every row that sees a
+    token."""
     N, H, D = q.shape
     P, G, ps, _ = k_pool.shape
     out = np.full(q.shape, np.nan)
@@ -96,6 +97,8 @@ def chunk(q, token_starts, k_pool, v_pool, table, seq_lens, alpha):
                     out[r, h] = 0.0
                     continue
                 z = k_pool[page, g, t % ps].astype(np.float64) @ q[r, h].astype(np.float64)
+                if each is not None:
+                    each(r, h, z)
                 tau[r, h] = O.entmax_threshold((alpha - 1.0) * z, alpha)
                 p = O.entmax_probs((alpha - 1.0) * z, tau[r, h], alpha)
                 live = p > 0

@@ -249,19 +249,6 @@ __device__ __forceinline__ void late_tile(const Views& x, TilePages pg, int t0, 
   }
 }
 
-// Four finished coordinates of a row.
-template <int PARTS>
-__device__ __forceinline__ void store_out(void* out, size_t at, f32x4 o) {
-  if constexpr (PARTS == 1) {
-    uint32_t h[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = bf16_round(o[e]);
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) =
-        u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-  } else {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = o;
-  }
-}
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 // (l is 0 or at least about 1: m is never above the largest score)
 __device__ __forceinline__ float log_sum(float m, float l) {

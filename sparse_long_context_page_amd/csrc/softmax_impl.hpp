@@ -1,5 +1,5 @@
 // Tiles of the paged cache in registers and their products on the matrix
-// cores, shared by the softmax decode and the attention-weight kernels.
+// cores, shared by the softmax decode, the attention-weight and the chunk kernels.
 //
 // Scores are computed transposed, S^T = K Q^T (A = K: 16 tokens, B = Q: 16
 // query rows), so that a lane holds the scores of ONE row (lane % 16) for the
@@ -548,6 +548,23 @@ __device__ __forceinline__ bool stage_nonfinite(lds_at st, int sub, int lane) {
     }
   }
   return BF ? bh[0] >= 0x7f80 || bh[1] >= 0x7f80 : big >= 0x7f800000u;
+}
+
+// ---------------------------------------------------------------------------
+// Outputs
+
+// Four finished coordinates of a row.
+template <int PARTS>
+__device__ __forceinline__ void store_out(void* out, size_t at, f32x4 o) {
+  if constexpr (PARTS == 1) {
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = bf16_round(o[e]);
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + at) =
+        u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+  } else {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = o;
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -11,7 +11,7 @@ The function names match the C ABI:
     entmaxkv_decode_full, entmaxkv_build_page_moments,
     entmaxkv_append_page_moments, entmaxkv_gauss_select, entmaxkv_softmax_window,
     entmaxkv_softmax_prefix, entmaxkv_accumulate_weights, entmaxkv_evict,
-    entmaxkv_plan_tokens, entmaxkv_append_kv,
+    entmaxkv_plan_tokens, entmaxkv_append_kv, entmaxkv_entmax_chunk, entmaxkv_entmax_chunk_ws,
     entmaxkv_workspace_bytes, entmaxkv_softmax_window_ws, entmaxkv_softmax_prefix_ws,
     entmaxkv_softmax_form, entmaxkv_topk_kernels, entmaxkv_strerror
 """
@@ -46,7 +46,7 @@ KERNELS = {"build_page_meta": 1, "append_page_meta": 1, "score_select": 2,
            "score_select_noalloc": 2, "decode_sparse": 2, "decode_topk": 4,
            "decode_full": 2, "build_page_moments": 1, "append_page_moments": 1,
            "gauss_select": 2, "softmax_window": 2, "softmax_prefix": 2, "accumulate_weights": 1,
-           "evict": 1, "plan_tokens": 1, "append_kv": 1}
+           "evict": 1, "plan_tokens": 1, "append_kv": 1, "entmax_chunk": 1}
 
 FULL_WINDOW = 2**31 - 1  # a window that hides no token
 
@@ -115,6 +115,9 @@ def _load() -> ctypes.CDLL:
     lib.entmaxkv_evict.argtypes = [SP, P, P, P, P, P, I32, I32, I32, P, P, P, P, P, P]
     lib.entmaxkv_plan_tokens.argtypes = [SP, I32, P, P, P, I32, P, P, P, P, P, P, P, P, P]
     lib.entmaxkv_append_kv.argtypes = [SP, ctypes.POINTER(Append), *[P] * 14]
+    lib.entmaxkv_entmax_chunk.argtypes = [SP, P, I32, I32, P, P, P, P, P, F32, P, P, P, P, SZ, P,
+                                          P]
+    lib.entmaxkv_entmax_chunk_ws.argtypes = [SP, I32, ctypes.POINTER(SZ)]
     lib.entmaxkv_workspace_bytes.argtypes = [SP, I32, I32, ctypes.POINTER(SZ)]
     lib.entmaxkv_topk_kernels.argtypes = [SP, I32, ctypes.POINTER(I32)]
     lib.entmaxkv_strerror.argtypes = [ctypes.c_int]
@@ -128,7 +131,7 @@ def _load() -> ctypes.CDLL:
                  "entmaxkv_softmax_window_ws", "entmaxkv_softmax_prefix",
                  "entmaxkv_softmax_prefix_ws", "entmaxkv_softmax_form",
                  "entmaxkv_accumulate_weights", "entmaxkv_evict", "entmaxkv_plan_tokens",
-                 "entmaxkv_append_kv",
+                 "entmaxkv_append_kv", "entmaxkv_entmax_chunk", "entmaxkv_entmax_chunk_ws",
                  "entmaxkv_workspace_bytes", "entmaxkv_topk_kernels", "entmaxkv_version"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -648,6 +651,39 @@ def _args_append_kv(shape: Shape, q, k, v, positions, slots, q_out, k_pool, v_po
                                     _stream(stream, q.device), None]
 
 
+def entmaxkv_entmax_chunk_ws(shape: Shape, num_tokens: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib.entmaxkv_entmax_chunk_ws(ctypes.byref(shape), _int32(num_tokens),
+                                        ctypes.byref(out)), "entmaxkv_entmax_chunk_ws")
+    return int(out.value)
+
+
+def _args_entmax_chunk(shape: Shape, q, token_starts, k_pool, v_pool, block_table, seq_lens, alpha,
+                       out, tau=None, support=None, ws=None, stream=None):
+    n = _Sizes(shape)
+    qd = _q_dtype(shape, q)
+    H, D = shape.num_q_heads, shape.head_dim
+    if q.dim() != 3 or tuple(q.shape[1:]) != (H, D):
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected (tokens, {H}, {D})")
+    tokens = q.shape[0]
+    ptrs = [_ptr(token_starts, "token_starts", (torch.int32,), numel=n.batch + 1),
+            _ptr(k_pool, "k_pool", _kv_dtypes(shape), numel=n.pool),
+            _ptr(v_pool, "v_pool", _kv_dtypes(shape), numel=n.pool),
+            _ptr(block_table, "block_table", (torch.int32,), numel=n.block_table),
+            _ptr(seq_lens, "seq_lens", (torch.int32,), numel=n.batch)]
+    outs = [_ptr(out, "out", (q.dtype,), numel=tokens * H * D),
+            _ptr(tau, "tau", (torch.float32,), nullable=True, numel=tokens * H),
+            _ptr(support, "support", (torch.int32,), nullable=True, numel=tokens * H)]
+    pq = _ptr(q, "q")
+    _one_device(q=q, token_starts=token_starts, k_pool=k_pool, v_pool=v_pool,
+                block_table=block_table, seq_lens=seq_lens, out=out, tau=tau, support=support)
+    need = 0 if ws is not None else entmaxkv_entmax_chunk_ws(shape, tokens)
+    pw, nw, ws = _given_or_new(ws, need, q, stream)
+    return lib.entmaxkv_entmax_chunk, [
+        ctypes.byref(shape), pq, qd, _int32(tokens), *ptrs, float(alpha), *outs, pw, nw,
+        _stream(stream, q.device), None], ws
+
+
 def _run(name, fn, args, events):
     if events is not None:
         ev = _events(events)
@@ -802,6 +838,16 @@ def entmaxkv_append_kv(shape: Shape, q, k, v, positions, slots, q_out, k_pool, v
     _run_on(q.device, "entmaxkv_append_kv", fn, args, events)
 
 
+def entmaxkv_entmax_chunk(shape: Shape, q, token_starts, k_pool, v_pool, block_table, seq_lens,
+                          alpha, out, tau=None, support=None, ws=None, stream=None, events=None):
+    """alpha-entmax attention of the new tokens of a ragged batch: sequence b's
+    are rows token_starts[b] .. token_starts[b + 1] - 1 of q and out, [tokens,
+    num_q_heads, head_dim], its last ones in the cache."""
+    fn, args, _ = _args_entmax_chunk(shape, q, token_starts, k_pool, v_pool, block_table, seq_lens,
+                                     alpha, out, tau, support, ws, stream)
+    _run_on(q.device, "entmaxkv_entmax_chunk", fn, args, events)
+
+
 class Prepared:
     """An entry point with its arguments marshalled once, for tight loops.
     The tensors must stay alive and unchanged in place while it is used.
@@ -820,7 +866,8 @@ class Prepared:
                "softmax_window": _args_softmax_window,
                "softmax_prefix": _args_softmax_prefix,
                "accumulate_weights": _args_accumulate_weights, "evict": _args_evict,
-               "plan_tokens": _args_plan_tokens, "append_kv": _args_append_kv}
+               "plan_tokens": _args_plan_tokens, "append_kv": _args_append_kv,
+               "entmax_chunk": _args_entmax_chunk}
 
     def __init__(self, name: str, *args, **kwargs):
         r = Prepared._makers[name](*args, **kwargs)
