@@ -596,7 +596,8 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
  * themselves (bf16 queries). Results do not depend on what else runs (no
  * atomics on results).
  * Workspace: entmaxkv_entmax_chunk_ws bytes, for either query type and any
- * alpha (0: ws may be null). Kernels launched: 1.
+ * alpha. Kernels launched: 3 (lists of the tokens that may have a weight; tau
+ * and the output; rows whose support is too long for a list).
  */
 int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
                           int32_t num_tokens, const int32_t* token_starts, const void* k_pool,

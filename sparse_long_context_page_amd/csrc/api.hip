@@ -366,12 +366,18 @@ int prefix_plan(const entmaxkv_shape* shape, int32_t q_dtype, int32_t prefix_pag
   return check_plan(*p);
 }
 
-int chunk_plan(const entmaxkv_shape* shape, int32_t num_tokens, LaunchShape* s, ChunkPlan* p) {
+// q_dtype < 0: of whichever query type needs the larger workspace
+int chunk_plan(const entmaxkv_shape* shape, int32_t q_dtype, int32_t num_tokens, LaunchShape* s,
+               ChunkPlan* p) {
   int rc = check_shape(shape, s);
   if (rc) return rc;
   if ((rc = check_num_tokens(num_tokens))) return rc;
-  *p = plan_chunk(*s, num_tokens);
-  return check_grid(p->items, p->threads);
+  *p = plan_chunk(*s, q_dtype == ENTMAXKV_BF16, num_tokens);
+  if (q_dtype < 0 && s->bf16) {
+    const ChunkPlan b = plan_chunk(*s, true, num_tokens);
+    if (b.ws_bytes > p->ws_bytes) *p = b;
+  }
+  return check_grid(p->items > p->tiles ? p->items : p->tiles, p->threads);
 }
 
 int attend_common(const LaunchShape& s, const AttendPlan& p, const void* q, int32_t q_dtype,
@@ -870,7 +876,7 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
 int entmaxkv_entmax_chunk_ws(const entmaxkv_shape* shape, int32_t num_tokens, size_t* bytes) {
   LaunchShape s;
   ChunkPlan p;
-  if (int rc = chunk_plan(shape, num_tokens, &s, &p)) return rc;
+  if (int rc = chunk_plan(shape, -1, num_tokens, &s, &p)) return rc;
   if (!bytes) return ENTMAXKV_ERR_INVALID;
   *bytes = p.ws_bytes;
   return ENTMAXKV_OK;
@@ -884,7 +890,7 @@ int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_
                           hipEvent_t* events) {
   LaunchShape s;
   ChunkPlan p;
-  int rc = chunk_plan(shape, num_tokens, &s, &p);
+  int rc = chunk_plan(shape, q_dtype == ENTMAXKV_BF16 ? q_dtype : ENTMAXKV_F32, num_tokens, &s, &p);
   if (rc) return rc;
   if ((rc = check_alpha(alpha))) return rc;
   if ((rc = check_q_dtype(s, q_dtype))) return rc;
@@ -892,16 +898,16 @@ int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_
     return ENTMAXKV_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16))
     return ENTMAXKV_ERR_INVALID;
-  if (p.ws_bytes) {
-    if (!ws || ws_bytes < p.ws_bytes) return ENTMAXKV_ERR_WORKSPACE;
-    if (!aligned(ws, 256)) return ENTMAXKV_ERR_INVALID;
-  }
+  if (!ws || ws_bytes < p.ws_bytes) return ENTMAXKV_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return ENTMAXKV_ERR_INVALID;
   const Events ev{events, stream};
-  if (!ev.before(0)) return ENTMAXKV_ERR_HIP;
-  if (launch_chunk(s, p, q, q_dtype == ENTMAXKV_BF16, num_tokens, token_starts, k_pool, v_pool,
-                   block_table, seq_lens, alpha, out, tau, support, ws, stream) != hipSuccess)
-    return ENTMAXKV_ERR_HIP;
-  if (!ev.after(0)) return ENTMAXKV_ERR_HIP;
+  for (int i = 0; i < kChunkKernels; ++i) {
+    if (!ev.before(i)) return ENTMAXKV_ERR_HIP;
+    if (launch_chunk(s, p, i, q, q_dtype == ENTMAXKV_BF16, num_tokens, token_starts, k_pool, v_pool,
+                     block_table, seq_lens, alpha, out, tau, support, ws, stream) != hipSuccess)
+      return ENTMAXKV_ERR_HIP;
+    if (!ev.after(i)) return ENTMAXKV_ERR_HIP;
+  }
   return ENTMAXKV_OK;
 }
 

@@ -5,6 +5,16 @@
 //
 // over the tokens up to the query's own position. Everything is computed from
 // y_t = x_t - max x <= 0, whose threshold lies in [-1, 0).
+//
+// tau grows with every token added, so the threshold of the tokens seen so far
+// (at first max x - 1) bounds the support from below: one pass over the scores
+// on the matrix cores keeps, per row, the few tokens above it, and V is read for
+// the support alone. Three kernels:
+//   list_kernel    scores, and each row's list of tokens above the running bound
+//   finish_kernel  a row's lists (one a part of its tokens) joined, tau solved,
+//                  the support's V rows gathered
+//   dense_kernel   rows whose support does not fit a list, by passes over all of
+//                  their scores; the other workgroups leave at once
 #include "softmax_impl.hpp"
 
 namespace ekv {
@@ -23,10 +33,23 @@ struct ChunkArgs {
   float* tau;        // nullable
   int32_t* support;  // nullable
   int N, B, H, Hkv, g_bits, ps_bits, max_pages, num_phys;
-  int tok_bits;  // 2^tok_bits tokens a block of rows
   float am1, m;  // alpha - 1 and 1 / (alpha - 1)
+  float window;  // of a score below the row's maximum that may have a weight
   int whole;     // m if it is 1, 2, 3 or 4, else 0
+  int splits;    // parts of a row's tokens
+  // workspace: per (row, part) the list and its length, and per 16 rows whether
+  // they need the dense kernel
+  uint64_t* lists;
+  int32_t* counts;
+  int32_t* dense;
 };
+
+// Entries of a list. 32 are more than twice what most rows hold with weights of
+// a few tokens; a tile can add 32, so a list above kCap - 32 is pruned.
+constexpr int kCap = 128;
+// Lengths that say why there is no list.
+constexpr int kLong = -1;    // the support does not fit
+constexpr int kNoNumber = -2;  // a score is NaN or +inf
 
 // A block of rows: tokens i0 .. of sequence b (rows tok0 .. of q) and the heads
 // of KV head g. rows = 0: none.
@@ -38,23 +61,24 @@ struct Rows {
 // + b: never fewer than it has, floor(starts[b+1] / TB) - floor(starts[b] / TB)
 // + 1 >= ceil(n / TB), so that a workgroup finds its block by a search alone.
 // 64 probes a step: two steps up to 4096 sequences.
-__device__ __forceinline__ Rows find_rows(const ChunkArgs& a, int id, int g, int lane) {
+__device__ __forceinline__ Rows find_rows(const ChunkArgs& a, int tok_bits, int id, int g,
+                                          int lane) {
   const auto start = [&](int b) { return clamp_len(a.starts[b], a.N); };
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const int step = (hi - lo + kWave - 1) / kWave, at = lo + lane * step;
-    const bool below = lane == 0 || (at < hi && (start(at) >> a.tok_bits) + at <= id);
+    const bool below = lane == 0 || (at < hi && (start(at) >> tok_bits) + at <= id);
     lo += (63 - __builtin_clzll(__ballot(below))) * step;
     hi = min(hi, lo + step);
   }
   Rows r;
-  const int s = start(lo), i0 = (id - (s >> a.tok_bits) - lo) << a.tok_bits;
+  const int s = start(lo), i0 = (id - (s >> tok_bits) - lo) << tok_bits;
   r.b = lo;
   r.g = g;
   r.n = start(lo + 1) - s;
   r.i0 = i0;
   r.tok0 = s + i0;
-  r.rows = i0 >= 0 && i0 < r.n ? min(1 << a.tok_bits, r.n - i0) << a.g_bits : 0;
+  r.rows = i0 >= 0 && i0 < r.n ? min(1 << tok_bits, r.n - i0) << a.g_bits : 0;
   r.L = clamp_len(a.seq_lens[lo], a.max_pages << a.ps_bits);
   return r;
 }
@@ -325,36 +349,642 @@ __device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, in
   __syncthreads();
 }
 
+// ---------------------------------------------------------------------------
+// Sums and maxima over the 16 lanes of a row of lanes, and over the four rows
+
+__device__ __forceinline__ float sum16(float x) {
+  x += partner<1>(x);
+  x += partner<2>(x);
+  x += partner<4>(x);
+  return x + partner<8>(x);
+}
+__device__ __forceinline__ float max16(float x) {
+  x = fmaxf(x, partner<1>(x));
+  x = fmaxf(x, partner<2>(x));
+  x = fmaxf(x, partner<4>(x));
+  return fmaxf(x, partner<8>(x));
+}
+// NaN if one is among them; no LDS traffic
+__device__ __forceinline__ float max_across(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  x = __builtin_elementwise_maximum(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const uint32_t v = __float_as_uint(x);
+  const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return __builtin_elementwise_maximum(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+
+// ---------------------------------------------------------------------------
+// Lists. An entry is (score, token).
+
+__device__ __forceinline__ uint64_t entry(float z, int t) {
+  return (uint64_t)(uint32_t)t << 32 | __float_as_uint(z);
+}
+__device__ __forceinline__ float entry_z(uint64_t e) { return __uint_as_float((uint32_t)e); }
+__device__ __forceinline__ int entry_t(uint64_t e) { return (int)(e >> 32); }
+
+// The threshold over a row's entries, y relative to the maximum mx, by 16
+// lanes; each(f) calls f(z) for the lane's own entries.
+template <typename Each>
+__device__ __forceinline__ float solve16(const ChunkArgs& a, float mx, bool any, Each each) {
+  Threshold th;
+  th.done = !any;
+  for (int i = 0; i < kSteps; ++i) {
+    float s = 0.0f, s1 = 0.0f;
+    each([&](float z) {
+      float pm, pm1;
+      powers(a, fmaxf((z - mx) * a.am1 - th.t, 0.0f), pm, pm1);
+      s += pm;
+      s1 += pm1;
+    });
+    s = sum16(s);
+    s1 = sum16(s1);
+    th.step(a, s, s1, i);
+    if (__all(th.done)) break;
+  }
+  return th.t;
+}
+// A score below every token of the support of threshold t, roundings included.
+__device__ __forceinline__ float bound_of(const ChunkArgs& a, float mx, float t) {
+  return mx + (t - 2.0e-6f) / a.am1 - 1.0e-6f * fabsf(mx);
+}
+
+// One row's running state, the same in the four lanes that hold its scores.
+struct Track {
+  float mx = -INFINITY, thr = -INFINITY;
+  int n = 0;
+};
+
+// Prunes the lists of the 16 rows of a tile to the tokens above the threshold
+// of what they hold: 4 rows at a time, 16 lanes a row, CAP / 16 entries a lane
+// in registers. at(row): its list.
+template <int CAP, typename At>
+__device__ __forceinline__ void prune(const ChunkArgs& a, Track& tr, int room, int lane, At at) {
+  const int sub = lane & 15;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const int row = k * 4 + (lane >> 4);
+    const int n = max(__shfl(tr.n, row, kWave), 0);
+    const float mx = __shfl(tr.mx, row, kWave);
+    uint64_t* list = at(row);
+    uint64_t e[CAP / 16];
+#pragma unroll
+    for (int i = 0; i < CAP / 16; ++i)
+      e[i] = i * 16 + sub < n ? list[i * 16 + sub] : entry(-INFINITY, 0);
+    const float t = solve16(a, mx, n > 0, [&](auto f) {
+#pragma unroll
+      for (int i = 0; i < CAP / 16; ++i) f(entry_z(e[i]));
+    });
+    const float thr = bound_of(a, mx, t);
+    int kept = 0;
+#pragma unroll
+    for (int i = 0; i < CAP / 16; ++i) {
+      const bool keep = i * 16 + sub < n && !(entry_z(e[i]) <= thr);
+      const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
+      if (keep) list[kept + __popc(all & ((1u << sub) - 1))] = e[i];
+      kept += __popc(all);
+    }
+    // back to the lanes that hold these rows' scores
+    const int from = ((lane & 3) << 4), mine = (lane & 15) >> 2;
+    const int kn = __shfl(kept, from, kWave);
+    const float kt = __shfl(thr, from, kWave);
+    if (mine == k && tr.n > 0) {
+      tr.n = kn;
+      tr.thr = fmaxf(tr.thr, kt);
+      if (kn > room) {
+        tr.n = kLong;
+        tr.thr = INFINITY;
+      }
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+}
+
+// One tile's scores of a row tile against the rows' bounds; tokens above them
+// to the lists, in the order of the tokens a lane holds, then of the lanes.
+template <bool BF, typename At>
+__device__ __forceinline__ void collect(const ChunkArgs& a, Track& tr,
+                                        const float (&z)[scores_per_lane<BF>()], float tmax, int t0,
+                                        int lane, At at) {
+  const int c = lane >> 4;
+  tr.mx = __builtin_elementwise_maximum(tr.mx, max_across(tmax));
+  tr.thr = fmaxf(tr.thr, tr.mx - a.window);
+  // this row's four lanes, and those of them below this one
+  const uint64_t row = 0x0001000100010001ull << (lane & 15), below = row & lanemask_below(lane);
+  uint64_t* list = at(lane & 15);
+#pragma unroll
+  for (int i = 0; i < scores_per_lane<BF>(); ++i) {
+    const bool hit = z[i] > tr.thr;
+    const uint64_t all = __ballot(hit);
+    if (all == 0) continue;
+    if (hit) list[tr.n + __popcll(all & below)] = entry(z[i], t0 + tile_token<BF>(c, i));
+    tr.n += __popcll(all & row);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ float max_of(const float (&z)[N]) {
+  float m = z[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = __builtin_elementwise_maximum(m, z[i]);
+  return m;
+}
+
+// The length to hand on.
+__device__ __forceinline__ int length_of(const Track& tr) {
+  return tr.mx < INFINITY ? tr.n : kNoNumber;  // (NaN too)
+}
+
+struct Cache {
+  KvView k;
+  const int32_t* table;
+  int npages;
+};
+template <bool BF, int D>
+__device__ __forceinline__ Cache cache_of(const ChunkArgs& a, const Rows& w, int top) {
+  constexpr int kElem = BF ? 2 : 4;
+  Cache x;
+  x.k = KvView{static_cast<const char*>(a.k_pool) + ((size_t)w.g << a.ps_bits) * (D * kElem),
+               ((size_t)a.Hkv << a.ps_bits) * (D * kElem), 1 << a.ps_bits};
+  x.table = a.block_table + (size_t)w.b * a.max_pages;
+  x.npages = (top + (1 << a.ps_bits) - 1) >> a.ps_bits;
+  return x;
+}
+
+// Row tiles a wave holds. bf16 queries: 64 rows share each K operand read from
+// LDS. Three parts of a float32 query, and float32 rows, take the registers of
+// more.
+template <bool BF, int PARTS>
+constexpr int kListTiles = BF && PARTS == 1 ? 4 : 2;
+
+constexpr int kFewCap = 96;  // of a wave's list in LDS
+
+template <bool BF, int D>
+union ListLds {
+  struct {
+    char st[2][Stage<BF, D>::kBytes];
+    __align__(16) int ok[2][kChunkWaves];
+  } many;
+  struct {
+    uint64_t list[kChunkWaves][16][kFewCap];
+    int n[kChunkWaves][16];
+  } few;
+};
+
+// More than 16 rows: every wave has row tiles of its own, K staged in LDS for
+// all of them by direct loads, one stage ahead.
 template <bool BF, int D, int PARTS>
-__global__ __launch_bounds__(kChunkWaves * kWave, 2) void chunk_kernel(ChunkArgs a) {
-  __shared__ DenseLds<D> sh;
-  const int id = blockIdx.x / a.Hkv, g = blockIdx.x - id * a.Hkv;
-  const Rows w = find_rows(a, id, g, threadIdx.x & (kWave - 1));
-  for (int r0 = 0; r0 < w.rows; r0 += 16) dense_rows<BF, D, PARTS>(a, w, r0, sh);
+__device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int split,
+                                          ListLds<BF, D>& lds) {
+  constexpr int TT = kTile<BF>;
+  constexpr int NZ = scores_per_lane<BF>();
+  constexpr int QB = PARTS == 1 ? 2 : 4;
+  constexpr int RT = kListTiles<BF, PARTS>;
+  typedef Stage<BF, D> St;
+  constexpr int ST = St::kTokens;
+  constexpr int kQuarter = ST / kChunkWaves;
+  constexpr int kLoads = St::kBytes / kChunkWaves / 1024;
+  auto& sh = lds.many;
+
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane >> 4, rl = lane & 15;
+  const int nt = ((w.rows + 15) / 16 + kChunkWaves - 1) / kChunkWaves;  // tiles a wave
+  const int wr = wave * nt * 16, wrows = max(min(nt * 16, w.rows - wr), 0);
+  const int top = seen(a, w, w.rows - 1);
+  const Cache x = cache_of<BF, D>(a, w, top);
+  const int stages = (top + ST - 1) / ST, per = (stages + a.splits - 1) / a.splits;
+  const int v0 = min(split * per, stages), v1 = min(v0 + per, stages);
+
+  int hi[RT];
+  QFrag<BF, D, PARTS> q[RT];
+  Track tr[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const bool live = t < nt && t * 16 + rl < wrows;
+    hi[t] = live ? seen(a, w, wr + t * 16 + rl) : 0;
+    q[t].load(live ? static_cast<const char*>(a.q) + row_at(a, w, wr + t * 16 + rl) * (D * QB)
+                   : nullptr, c);
+  }
+  // tokens that some, and that all, of this wave's rows see
+  const int some = wrows ? seen(a, w, wr + wrows - 1) : 0, every = wrows ? seen(a, w, wr) : 0;
+  const bool whole = wrows == nt * 16;  // (rows that are none see nothing)
+  auto list = [&](int t) {
+    return [&, t](int row) {
+      // a row past the last has no entries: any address serves
+      const int r = min(wr + t * 16 + row, w.rows - 1);
+      return a.lists + (row_at(a, w, r) * a.splits + split) * kCap;
+    };
+  };
+
+  int from[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = i * 1024 + lane * 16;
+    const int r = at / St::kRow, slot = at % St::kRow / 16;
+    from[i] = r * St::kRow + ((slot ^ St::swizzle(wave * kQuarter + r)) << 4);
+  }
+  // page of this wave's quarter of each of the next 64 stages, one a lane
+  int base = v0, pg = -1;
+  auto look = [&](int v) {
+    base = v;
+    pg = -1;
+    if (v + lane < v1)
+      pg = page_at(a, x.table, x.npages, ((v + lane) * ST + wave * kQuarter) >> a.ps_bits);
+  };
+  auto stage = [&](int v) {
+    const int p = __builtin_amdgcn_readlane(pg, v - base);
+    const int t = v * ST + wave * kQuarter;
+    const char* src = x.k.base + (size_t)max(p, 0) * x.k.page_bytes +
+                      (size_t)(t & ((1 << a.ps_bits) - 1)) * St::kRow;
+    char* dst = sh.st[v & 1] + wave * (St::kBytes / kChunkWaves);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      __builtin_amdgcn_global_load_lds(src + from[i], dst + i * 1024, 16, 0, 0);
+    if (lane == 0) sh.ok[v & 1][wave] = p >= 0 ? 1 : 0;
+  };
+
+  int limit[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) limit[t] = kCap - TT;
+  if (v0 < v1) {
+    look(v0);
+    stage(v0);
+    wait_vmcnt<0>();
+  }
+  __syncthreads();
+  for (int v = v0; v < v1; ++v) {
+    if (v + 1 < v1) {
+      if (v + 1 - base == kWave) look(v + 1);
+      stage(v + 1);
+    }
+    const int ts = v * ST;
+    if (ts < some) {
+      const int4 ok = *reinterpret_cast<const int4*>(sh.ok[v & 1]);
+      const bool full = whole && ts + ST <= every &&
+                        __builtin_amdgcn_readfirstlane(ok.x & ok.y & ok.z & ok.w);
+      const lds_at kst = lds_addr(sh.st[v & 1]);
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        KTile<BF, D> kt;
+        kt.read(kst, sub, lane);
+        const int t0 = ts + sub * TT;
+        float z[RT][NZ], tmax[RT];
+        bool hit = false;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          if (t >= nt) break;
+          kt.template scores<PARTS>(q[t], z[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          if (t >= nt) break;
+          if (!full) {
+            const bool page_ok = (c < 2 ? (sub ? ok.z : ok.x) : (sub ? ok.w : ok.y)) != 0;
+#pragma unroll
+            for (int i = 0; i < NZ; ++i)
+              z[t][i] = page_ok & (t0 + tile_token<BF>(c, i) < hi[t]) ? z[t][i] : -INFINITY;
+          }
+          tmax[t] = max_of(z[t]);
+          hit |= !(tmax[t] <= tr[t].thr);
+        }
+        if (__any(hit)) {
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            if (t >= nt) break;
+            if (!__any(!(tmax[t] <= tr[t].thr))) continue;
+            collect<BF>(a, tr[t], z[t], tmax[t], t0, lane, list(t));
+            if (__any(tr[t].n > limit[t]))
+              prune<kCap>(a, tr[t], kCap - TT, lane, list(t));
+          }
+        }
+      }
+    }
+    if (v + 1 < v1) wait_vmcnt<0>();
+    __syncthreads();
+  }
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+    if (c == 0 && t < nt && t * 16 + rl < wrows)
+      a.counts[row_at(a, w, wr + t * 16 + rl) * a.splits + split] = length_of(tr[t]);
+}
+
+// At most 16 rows (single tokens): the waves share them and take turns at the
+// tiles, loaded from memory straight into the operands' registers; each keeps
+// lists of its own in LDS, joined at the end.
+template <bool BF, int D, int PARTS>
+__device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int split,
+                                         ListLds<BF, D>& lds) {
+  constexpr int TT = kTile<BF>;
+  constexpr int NZ = scores_per_lane<BF>();
+  constexpr int QB = PARTS == 1 ? 2 : 4;
+  constexpr int NW = kChunkWaves;
+  auto& sh = lds.few;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane >> 4, rl = lane & 15;
+  const int top = seen(a, w, w.rows - 1), every = w.rows == 16 ? seen(a, w, 0) : 0;
+  const int hi = rl < w.rows ? seen(a, w, rl) : 0;
+  const Cache x = cache_of<BF, D>(a, w, top);
+  const int tiles = (top + TT - 1) / TT, per = (tiles + a.splits - 1) / a.splits;
+  const int v0 = min(split * per, tiles), v1 = min(v0 + per, tiles);
+
+  QFrag<BF, D, PARTS> q;
+  q.load(rl < w.rows ? static_cast<const char*>(a.q) + row_at(a, w, rl) * (D * QB) : nullptr, c);
+  Track tr;
+  auto list = [&](int row) { return sh.list[wave][row]; };
+  for (int base = v0 + wave; base < v1; base += NW * kWave) {
+    // pages of this wave's next 64 tiles, one tile a lane
+    const int nt = min(kWave, (v1 - base + NW - 1) / NW);
+    int pg0 = -1, pg1 = -1;
+    if (lane < nt) {
+      const int j = ((base + lane * NW) * TT) >> a.ps_bits;
+      pg0 = pg1 = page_at(a, x.table, x.npages, j);
+      if (BF && a.ps_bits == 4) pg1 = page_at(a, x.table, x.npages, j + 1);
+    }
+    auto pages = [&](int j) {
+      return TilePages{__builtin_amdgcn_readlane(pg0, j), __builtin_amdgcn_readlane(pg1, j)};
+    };
+    KTile<BF, D> kt;
+    TilePages pc = pages(0);
+    kt.load(x.k, pc, base * TT, lane);
+    for (int j = 0; j < nt; ++j) {
+      const int t0 = (base + j * NW) * TT;
+      float z[NZ];
+      kt.template scores<PARTS>(q, z);
+      const TilePages now = pc;
+      if (j + 1 < nt) {
+        pc = pages(j + 1);
+        kt.load(x.k, pc, t0 + NW * TT, lane);
+      }
+      if (now.p0 < 0 || now.p1 < 0 || t0 + TT > every) {
+        const bool page_ok = (!BF || c < 2 ? now.p0 : now.p1) >= 0;
+#pragma unroll
+        for (int i = 0; i < NZ; ++i)
+          z[i] = page_ok & (t0 + tile_token<BF>(c, i) < hi) ? z[i] : -INFINITY;
+      }
+      const float tmax = max_of(z);
+      if (__any(!(tmax <= tr.thr))) {
+        collect<BF>(a, tr, z, tmax, t0, lane, list);
+        if (__any(tr.n > kFewCap - TT)) prune<kFewCap>(a, tr, kFewCap - TT, lane, list);
+      }
+    }
+  }
+  if (c == 0) sh.n[wave][rl] = length_of(tr);
+  __syncthreads();
+
+  // join the waves' lists of a row, 16 lanes a row: what is within the window
+  // of the joint maximum, or above the joint threshold if that is too much
+  const int row = wave * 4 + c, sub = rl;
+  int n[NW], worst = 0;
+#pragma unroll
+  for (int v = 0; v < NW; ++v) {
+    n[v] = sh.n[v][row];
+    worst = min(worst, n[v]);
+  }
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int v = 0; v < NW; ++v)
+      for (int i = sub; i < n[v]; i += 16) f(sh.list[v][row][i]);
+  };
+  float mx = -INFINITY;
+  each([&](uint64_t e) { mx = fmaxf(mx, entry_z(e)); });
+  mx = max16(mx);
+  float thr = mx - a.window;
+  int most = 0;
+  each([&](uint64_t e) { most += entry_z(e) > thr ? 1 : 0; });
+  const bool much = sum16((float)most) > (float)kCap;
+  if (__any(much)) {
+    const float t = solve16(a, mx, much, [&](auto f) { each([&](uint64_t e) { f(entry_z(e)); }); });
+    if (much) thr = fmaxf(thr, bound_of(a, mx, t));
+  }
+  const bool real = row < w.rows;
+  const size_t part = row_at(a, w, min(row, w.rows - 1)) * a.splits + split;
+  int kept = 0;
+#pragma unroll
+  for (int v = 0; v < NW; ++v)
+    for (int i = 0; i < n[v]; i += 16) {
+      const uint64_t e = i + sub < n[v] ? sh.list[v][row][i + sub] : 0;
+      const bool keep = i + sub < n[v] && entry_z(e) > thr;
+      const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
+      const int at = kept + __popc(all & ((1u << sub) - 1));
+      if (keep && real && at < kCap) a.lists[part * kCap + at] = e;
+      kept += __popc(all);
+    }
+  if (sub == 0 && real) a.counts[part] = worst < 0 ? worst : kept > kCap ? kLong : kept;
 }
 
 template <bool BF, int D, int PARTS>
-hipError_t launch(const ChunkArgs& a, long long items, hipStream_t st) {
-  hipLaunchKernelGGL((chunk_kernel<BF, D, PARTS>), dim3((unsigned)items),
-                     dim3(kChunkWaves * kWave), 0, st, a);
+constexpr int kListRows = kChunkWaves * 16 * kListTiles<BF, PARTS>;
+
+template <bool BF, int D, int PARTS>
+__global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs a, int tok_bits) {
+  __shared__ __align__(1024) ListLds<BF, D> lds;
+  // over the KV heads first: with 8 of them, the blocks that read the same
+  // head's tokens share an XCD and its L2; then the parts
+  const int x = blockIdx.x / a.Hkv, g = blockIdx.x - x * a.Hkv;
+  const int id = x / a.splits, split = x - id * a.splits;
+  const Rows w = find_rows(a, tok_bits, id, g, threadIdx.x & (kWave - 1));
+  if (w.rows == 0) return;
+  if (w.rows <= 16)
+    list_few<BF, D, PARTS>(a, w, split, lds);
+  else
+    list_many<BF, D, PARTS>(a, w, split, lds);
+}
+
+// ---------------------------------------------------------------------------
+// tau and the output from the lists
+
+constexpr int kJoinCap = 256;  // joint entries of a row that may have a weight
+
+// 16 lanes a row, 16 rows a workgroup (as dense_kernel takes them). Each lane
+// gathers D / 16 coordinates of the support's V rows.
+template <bool BF, int D, int PARTS>
+__global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a, int tok_bits) {
+  constexpr int kElem = BF ? 2 : 4, kPer = D / 16;
+  typedef uint32_t vec __attribute__((ext_vector_type(kPer * kElem / 4)));
+  __shared__ uint64_t joint[16][kJoinCap];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), sub = tid & 15, row = tid >> 4;
+  const int id = blockIdx.x / a.Hkv, g = blockIdx.x - id * a.Hkv;
+  const Rows w = find_rows(a, tok_bits, id, g, lane);
+  if (w.rows == 0) {
+    if (tid == 0) a.dense[blockIdx.x] = 0;
+    return;
+  }
+  const bool real = row < w.rows;
+  const size_t at = row_at(a, w, min(row, w.rows - 1));
+  const uint64_t* lists = a.lists + at * a.splits * kCap;
+  const int32_t* counts = a.counts + at * a.splits;
+  uint64_t* list = joint[row];
+
+  // f(entry) for this lane's entries
+  auto each = [&](auto f) {
+    for (int s = 0; s < a.splits; ++s) {
+      const int m = counts[s];
+      for (int i = sub; i < m; i += 16) f(lists[s * kCap + i]);
+    }
+  };
+  int worst = 0, total = 0;
+  for (int s = 0; s < a.splits; ++s) {
+    worst = min(worst, counts[s]);
+    total += max(counts[s], 0);
+  }
+  float mx = -INFINITY;
+  each([&](uint64_t e) { mx = fmaxf(mx, entry_z(e)); });
+  mx = max16(mx);
+  float thr = mx - a.window;
+  if (__any(total > kJoinCap)) {
+    // perhaps more than fit within the window: above the joint threshold, then
+    int most = 0;
+    each([&](uint64_t e) { most += entry_z(e) > thr ? 1 : 0; });
+    const bool much = sum16((float)most) > (float)kJoinCap;
+    if (__any(much)) {
+      const float t =
+          solve16(a, mx, much, [&](auto f) { each([&](uint64_t e) { f(entry_z(e)); }); });
+      if (much) thr = fmaxf(thr, bound_of(a, mx, t));
+    }
+  }
+  int n = 0;
+  for (int s = 0; s < a.splits; ++s) {
+    const int m = counts[s];
+    for (int i = 0; i < m; i += 16) {
+      const uint64_t e = i + sub < m ? lists[s * kCap + i + sub] : 0;
+      const bool keep = i + sub < m && entry_z(e) > thr;
+      const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
+      const int to = n + __popc(all & ((1u << sub) - 1));
+      if (keep && to < kJoinCap) list[to] = e;
+      n += __popc(all);
+    }
+  }
+  const bool dense = worst == kLong || (worst == 0 && n > kJoinCap);
+  n = worst < 0 ? 0 : min(n, kJoinCap);
+  const int dense_rows_here = __syncthreads_count(dense && real);  // (and the lists are written)
+  if (tid == 0) a.dense[blockIdx.x] = dense_rows_here > 0;
+  if (dense_rows_here) return;
+
+  const float t = solve16(a, mx, n > 0, [&](auto f) {
+    for (int i = sub; i < n; i += 16) f(entry_z(list[i]));
+  });
+  // the support: its weights and V rows take the places of its scores and tokens
+  float l = 0.0f;
+  int live = 0;
+  const int32_t* table = a.block_table + (size_t)w.b * a.max_pages;
+  for (int i = 0; i < n; i += 16) {
+    const uint64_t e = i + sub < n ? list[i + sub] : entry(-INFINITY, 0);
+    const float u = fmaxf((entry_z(e) - mx) * a.am1 - t, 0.0f);
+    float p, pm1;
+    powers(a, u, p, pm1);
+    l += p;
+    const bool keep = u > 0.0f;
+    const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
+    const int tok = entry_t(e);
+    if (keep) {
+      const int page = table[tok >> a.ps_bits];
+      list[live + __popc(all & ((1u << sub) - 1))] =
+          entry(p, (page << a.ps_bits) + (tok & ((1 << a.ps_bits) - 1)));
+    }
+    live += __popc(all);
+  }
+  l = sum16(l);
+
+  const char* vb = static_cast<const char*>(a.v_pool) +
+                   ((size_t)g << a.ps_bits) * (D * kElem) + sub * (kPer * kElem);
+  const size_t page_bytes = ((size_t)a.Hkv << a.ps_bits) * (D * kElem);
+  float acc[kPer];
+#pragma unroll
+  for (int d = 0; d < kPer; ++d) acc[d] = 0.0f;
+  constexpr int U = 8;  // rows on their way
+  for (int i = 0; i < live; i += U) {
+    float p[U];
+    vec v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const uint64_t e = list[min(i + k, live - 1)];
+      const int r = entry_t(e);
+      p[k] = i + k < live ? entry_z(e) : 0.0f;
+      v[k] = *reinterpret_cast<const vec*>(vb + (size_t)(r >> a.ps_bits) * page_bytes +
+                                           (size_t)(r & ((1 << a.ps_bits) - 1)) * (D * kElem));
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (i + k >= live) break;
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) {
+        const float x = BF ? (d & 1 ? bf16_hi(v[k][d / 2]) : bf16_lo(v[k][d / 2]))
+                           : __uint_as_float(v[k][BF ? 0 : d]);
+        acc[d] = fmaf(p[k], x, acc[d]);
+      }
+    }
+  }
+  if (!real) return;
+  const float inv = worst == kNoNumber ? NAN : total == 0 ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int d = 0; d < kPer; d += 4)
+    store_out<PARTS>(a.out, at * D + sub * kPer + d,
+                     f32x4{acc[d], acc[d + 1], acc[d + 2], acc[d + 3]} * inv);
+  if (sub == 0) {
+    if (a.tau) a.tau[at] = n > 0 ? fmaf(a.am1, mx, t) : NAN;
+    if (a.support) a.support[at] = live;
+  }
+}
+
+template <bool BF, int D, int PARTS>
+__global__ __launch_bounds__(kChunkWaves * kWave, 2) void dense_kernel(ChunkArgs a, int tok_bits) {
+  __shared__ DenseLds<D> sh;
+  if (a.dense[blockIdx.x] == 0) return;
+  const int id = blockIdx.x / a.Hkv, g = blockIdx.x - id * a.Hkv;
+  const Rows w = find_rows(a, tok_bits, id, g, threadIdx.x & (kWave - 1));
+  dense_rows<BF, D, PARTS>(a, w, 0, sh);
+}
+
+template <bool BF, int D, int PARTS>
+hipError_t launch(const ChunkArgs& a, const ChunkPlan& p, int kernel, hipStream_t st) {
+  const dim3 threads(kChunkWaves * kWave);
+  if (kernel == 0)
+    hipLaunchKernelGGL((list_kernel<BF, D, PARTS>), dim3((unsigned)p.items), threads, 0, st, a,
+                       p.tok_bits);
+  else if (kernel == 1)
+    hipLaunchKernelGGL((finish_kernel<BF, D, PARTS>), dim3((unsigned)p.tiles), threads, 0, st, a,
+                       p.tile_bits);
+  else
+    hipLaunchKernelGGL((dense_kernel<BF, D, PARTS>), dim3((unsigned)p.tiles), threads, 0, st, a,
+                       p.tile_bits);
   return hipGetLastError();
 }
 
 }  // namespace
 
-ChunkPlan plan_chunk(const LaunchShape& s, int num_tokens) {
+ChunkPlan plan_chunk(const LaunchShape& s, bool q_bf16, int num_tokens) {
   ChunkPlan p;
-  p.tok_bits = 4 - __builtin_ctz(s.group);  // 16 rows
+  const int g_bits = __builtin_ctz(s.group);
+  const int rows = s.bf16 && q_bf16 ? kListRows<true, 128, 1> : kListRows<true, 128, 3>;
+  p.tok_bits = __builtin_ctz(rows) - g_bits;
+  p.tile_bits = 4 - g_bits;
   p.threads = kChunkWaves * kWave;
-  p.items = ((long long)(num_tokens >> p.tok_bits) + s.batch) * s.num_kv_heads;
+  p.tiles = ((long long)(num_tokens >> p.tile_bits) + s.batch) * s.num_kv_heads;
+  const long long blocks = ((long long)(num_tokens >> p.tok_bits) + s.batch) * s.num_kv_heads;
+  // four workgroups a CU, parts of at least 256 tokens
+  long long splits = 4 * kNumCUs / blocks;
+  const long long most = ((long long)s.max_pages * s.page_size + 255) / 256;
+  if (splits > most) splits = most;
+  if (splits > kChunkMaxSplits) splits = kChunkMaxSplits;
+  if (splits < 1) splits = 1;
+  p.splits = (int)splits;
+  p.items = blocks * splits;
+  const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const size_t parts = (size_t)num_tokens * s.num_q_heads * splits;
+  p.counts_off = parts * kCap * 8;
+  p.dense_off = p.counts_off + up(parts * 4);
+  p.ws_bytes = p.dense_off + up((size_t)p.tiles * 4);
   return p;
 }
 
-hipError_t launch_chunk(const LaunchShape& s, const ChunkPlan& p, const void* q, bool q_bf16,
-                        int num_tokens, const int32_t* token_starts, const void* k_pool,
-                        const void* v_pool, const int32_t* block_table, const int32_t* seq_lens,
-                        float alpha, void* out, float* tau, int32_t* support, void* ws,
-                        hipStream_t st) {
+hipError_t launch_chunk(const LaunchShape& s, const ChunkPlan& p, int kernel, const void* q,
+                        bool q_bf16, int num_tokens, const int32_t* token_starts,
+                        const void* k_pool, const void* v_pool, const int32_t* block_table,
+                        const int32_t* seq_lens, float alpha, void* out, float* tau,
+                        int32_t* support, void* ws, hipStream_t st) {
   ChunkArgs a;
   a.q = q;
   a.k_pool = k_pool;
@@ -373,16 +1003,20 @@ hipError_t launch_chunk(const LaunchShape& s, const ChunkPlan& p, const void* q,
   a.ps_bits = __builtin_ctz(s.page_size);
   a.max_pages = s.max_pages;
   a.num_phys = s.num_phys;
-  a.tok_bits = p.tok_bits;
   a.am1 = (float)((double)alpha - 1.0);
   a.m = (float)(1.0 / ((double)alpha - 1.0));
+  a.window = a.m * (1.0f + 4.0e-6f);
   a.whole = a.m == 1.0f || a.m == 2.0f || a.m == 3.0f || a.m == 4.0f ? (int)a.m : 0;
-  if (!s.bf16) return s.head_dim == 64 ? launch<false, 64, 3>(a, p.items, st)
-                                       : launch<false, 128, 3>(a, p.items, st);
-  if (q_bf16) return s.head_dim == 64 ? launch<true, 64, 1>(a, p.items, st)
-                                      : launch<true, 128, 1>(a, p.items, st);
-  return s.head_dim == 64 ? launch<true, 64, 3>(a, p.items, st)
-                          : launch<true, 128, 3>(a, p.items, st);
+  a.splits = p.splits;
+  a.lists = static_cast<uint64_t*>(ws);
+  a.counts = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + p.counts_off);
+  a.dense = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + p.dense_off);
+  if (!s.bf16) return s.head_dim == 64 ? launch<false, 64, 3>(a, p, kernel, st)
+                                       : launch<false, 128, 3>(a, p, kernel, st);
+  if (q_bf16) return s.head_dim == 64 ? launch<true, 64, 1>(a, p, kernel, st)
+                                      : launch<true, 128, 1>(a, p, kernel, st);
+  return s.head_dim == 64 ? launch<true, 64, 3>(a, p, kernel, st)
+                          : launch<true, 128, 3>(a, p, kernel, st);
 }
 
 }  // namespace ekv

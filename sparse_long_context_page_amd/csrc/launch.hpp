@@ -343,19 +343,23 @@ struct AppendParams {
 };
 hipError_t launch_append_kv(const LaunchShape& s, const AppendParams& p, hipStream_t st);
 
-// alpha-entmax attention of a ragged chunk (chunk.hip).
+// alpha-entmax attention of a ragged chunk (chunk.hip): lists, finish, dense.
+constexpr int kChunkMaxSplits = 64;
+constexpr int kChunkKernels = 3;
 struct ChunkPlan {
-  int tok_bits = 0;      // 2^tok_bits tokens a block of rows
-  long long items = 0;   // workgroups
-  int threads = 0;       // of a workgroup
-  size_t ws_bytes = 0;
+  int tok_bits = 0, tile_bits = 0;   // log2 of the tokens of a list and of a 16-row block
+  long long items = 0, tiles = 0;    // workgroups of the list kernel, of the others
+  int splits = 1;                    // parts of a row's tokens
+  int threads = 0;                   // of a workgroup
+  size_t counts_off = 0, dense_off = 0, ws_bytes = 0;
 };
-ChunkPlan plan_chunk(const LaunchShape& s, int num_tokens);
-hipError_t launch_chunk(const LaunchShape& s, const ChunkPlan& p, const void* q, bool q_bf16,
-                        int num_tokens, const int32_t* token_starts, const void* k_pool,
-                        const void* v_pool, const int32_t* block_table, const int32_t* seq_lens,
-                        float alpha, void* out, float* tau, int32_t* support, void* ws,
-                        hipStream_t st);
+ChunkPlan plan_chunk(const LaunchShape& s, bool q_bf16, int num_tokens);
+// kernel: 0 .. kChunkKernels - 1, launched in this order
+hipError_t launch_chunk(const LaunchShape& s, const ChunkPlan& p, int kernel, const void* q,
+                        bool q_bf16, int num_tokens, const int32_t* token_starts,
+                        const void* k_pool, const void* v_pool, const int32_t* block_table,
+                        const int32_t* seq_lens, float alpha, void* out, float* tau,
+                        int32_t* support, void* ws, hipStream_t st);
 
 // Attention weights and eviction (evict.hip).
 constexpr int kWeightWaves = 4;

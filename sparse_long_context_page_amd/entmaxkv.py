@@ -46,7 +46,7 @@ KERNELS = {"build_page_meta": 1, "append_page_meta": 1, "score_select": 2,
            "score_select_noalloc": 2, "decode_sparse": 2, "decode_topk": 4,
            "decode_full": 2, "build_page_moments": 1, "append_page_moments": 1,
            "gauss_select": 2, "softmax_window": 2, "softmax_prefix": 2, "accumulate_weights": 1,
-           "evict": 1, "plan_tokens": 1, "append_kv": 1, "entmax_chunk": 1}
+           "evict": 1, "plan_tokens": 1, "append_kv": 1, "entmax_chunk": 3}
 
 FULL_WINDOW = 2**31 - 1  # a window that hides no token
 
