@@ -44,9 +44,8 @@ struct ChunkArgs {
   int32_t* dense;
 };
 
-// Entries of a list. 32 are more than twice what most rows hold with weights of
-// a few tokens; a tile can add 32, so a list above kCap - 32 is pruned.
-constexpr int kCap = 128;
+// Entries of a list, and from how many it is pruned for the first time.
+constexpr int kCap = 128, kPruneAt = 96;
 // Lengths that say why there is no list.
 constexpr int kLong = -1;    // the support does not fit
 constexpr int kNoNumber = -2;  // a score is NaN or +inf
@@ -415,36 +414,43 @@ struct Track {
   int n = 0;
 };
 
-// Prunes the lists of the 16 rows of a tile to the tokens above the threshold
-// of what they hold: 4 rows at a time, 16 lanes a row, CAP / 16 entries a lane
-// in registers. at(row): its list.
+// Prunes one row's list to the tokens above the threshold of what it holds: 16
+// lanes a row, CAP / 16 entries a lane in registers. Returns that threshold;
+// n: its length, before and after.
+template <int CAP>
+__device__ __forceinline__ float prune16(const ChunkArgs& a, uint64_t* list, int lane, float mx,
+                                         int& n) {
+  const int sub = lane & 15;
+  uint64_t e[CAP / 16];
+#pragma unroll
+  for (int i = 0; i < CAP / 16; ++i)
+    e[i] = i * 16 + sub < n ? list[i * 16 + sub] : entry(-INFINITY, 0);
+  const float t = solve16(a, mx, n > 0, [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < CAP / 16; ++i) f(entry_z(e[i]));
+  });
+  const float thr = bound_of(a, mx, t);
+  int kept = 0;
+#pragma unroll
+  for (int i = 0; i < CAP / 16; ++i) {
+    const bool keep = i * 16 + sub < n && !(entry_z(e[i]) <= thr);
+    const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
+    if (keep) list[kept + __popc(all & ((1u << sub) - 1))] = e[i];
+    kept += __popc(all);
+  }
+  n = kept;
+  return thr;
+}
+
+// The lists of the 16 rows of a tile, 4 rows at a time. at(row): its list.
 template <int CAP, typename At>
 __device__ __forceinline__ void prune(const ChunkArgs& a, Track& tr, int room, int lane, At at) {
-  const int sub = lane & 15;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     const int row = k * 4 + (lane >> 4);
-    const int n = max(__shfl(tr.n, row, kWave), 0);
-    const float mx = __shfl(tr.mx, row, kWave);
-    uint64_t* list = at(row);
-    uint64_t e[CAP / 16];
-#pragma unroll
-    for (int i = 0; i < CAP / 16; ++i)
-      e[i] = i * 16 + sub < n ? list[i * 16 + sub] : entry(-INFINITY, 0);
-    const float t = solve16(a, mx, n > 0, [&](auto f) {
-#pragma unroll
-      for (int i = 0; i < CAP / 16; ++i) f(entry_z(e[i]));
-    });
-    const float thr = bound_of(a, mx, t);
-    int kept = 0;
-#pragma unroll
-    for (int i = 0; i < CAP / 16; ++i) {
-      const bool keep = i * 16 + sub < n && !(entry_z(e[i]) <= thr);
-      const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
-      if (keep) list[kept + __popc(all & ((1u << sub) - 1))] = e[i];
-      kept += __popc(all);
-    }
+    int kept = max(__shfl(tr.n, row, kWave), 0);
+    const float thr = prune16<CAP>(a, at(row), lane, __shfl(tr.mx, row, kWave), kept);
     // back to the lanes that hold these rows' scores
     const int from = ((lane & 3) << 4), mine = (lane & 15) >> 2;
     const int kn = __shfl(kept, from, kWave);
@@ -512,19 +518,64 @@ __device__ __forceinline__ Cache cache_of(const ChunkArgs& a, const Rows& w, int
   return x;
 }
 
+constexpr int kYoung = 4;  // stages
+
 // Row tiles a wave holds. bf16 queries: 64 rows share each K operand read from
 // LDS. Three parts of a float32 query, and float32 rows, take the registers of
 // more.
 template <bool BF, int PARTS>
 constexpr int kListTiles = BF && PARTS == 1 ? 4 : 2;
 
+// Scores of a K tile and NT row tiles: all of them take a step before any
+// takes the next, so that no matrix instruction waits for the one before it.
+template <bool BF, int D, int PARTS, int NT>
+__device__ __forceinline__ void tile_scores(const KTile<BF, D>& kt, const QFrag<BF, D, PARTS> (&q)[NT],
+                                            float (&z)[NT][scores_per_lane<BF>()]) {
+  if constexpr (BF) {
+    f32x4 acc[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = PARTS - 1; k >= 0; --k)
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                as_bf(kt.f[u][s]), as_bf(q[t].f[k][s]), acc[t][u], 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[t][i] = acc[t][i / 4][i % 4];
+  } else {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) kt.template scores<PARTS>(q[t], z[t]);
+  }
+}
+
 constexpr int kFewCap = 96;  // of a wave's list in LDS
+
+// A wave's hits wait in a queue until they fill a batch: a record is one lane's
+// scores of a tile (NZ of one row), some above the row's bound. It takes a few
+// instructions to queue one, and the work on rows and lists is done for 64 at
+// once.
+constexpr int kBatch = 64, kQueue = 4 * kBatch;  // (a tile brings 4 batches at most)
+
+template <int NZ>
+struct WaveRows {
+  f32x4 z[NZ / 4][kQueue];
+  int code[kQueue];       // row << 24 | the lane's first token
+  float mx[64], thr[64];  // thr: what a score has to pass
+  int n[64], limit[64];   // limit: entries from which a list is pruned
+};
 
 template <bool BF, int D>
 union ListLds {
   struct {
     char st[2][Stage<BF, D>::kBytes];
-    __align__(16) int ok[2][kChunkWaves];
+    WaveRows<scores_per_lane<BF>()> rows[kChunkWaves];
   } many;
   struct {
     uint64_t list[kChunkWaves][16][kFewCap];
@@ -532,15 +583,96 @@ union ListLds {
   } few;
 };
 
-// More than 16 rows: every wave has row tiles of its own, K staged in LDS for
-// all of them by direct loads, one stage ahead.
-template <bool BF, int D, int PARTS>
+// Takes the queue's hits to the rows' lists, 64 records at a time, a lane each,
+// in the order of the queue. at(row): a row's list.
+template <int NZ, typename At>
+__device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int count, int lane,
+                                      At at) {
+  const uint64_t below = lanemask_below(lane);
+#pragma unroll 1
+  for (int b = 0; b < count; b += kBatch) {
+    const bool real = b + lane < count;
+    const int code = real ? w.code[b + lane] : 0;
+    const int row = code >> 24, tok = code & 0xffffff;
+    float z[NZ];
+#pragma unroll
+    for (int i = 0; i < NZ / 4; ++i) {
+      const f32x4 x = w.z[i][b + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[4 * i + e] = x[e];
+    }
+    // the new maxima first: they bound these very hits
+    const float top = max_of(z);
+    if (real && top < INFINITY)
+      __hip_atomic_fetch_max(&w.mx[row], top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+    if (real && !(top < INFINITY)) w.n[row] = kNoNumber;
+    // lanes of the same row
+    uint64_t same = ~0ull;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const bool bit = row >> i & 1;
+      const uint64_t set = __ballot(bit);
+      same &= bit ? set : ~set;
+    }
+    bool pending = real, grown = false;
+    for (;;) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const int n = w.n[row];
+      const float thr = fmaxf(w.thr[row], w.mx[row] - a.window);
+      unsigned bits = 0;
+#pragma unroll
+      for (int i = 0; i < NZ; ++i) bits |= (z[i] > thr ? 1u : 0u) << i;
+      pending = pending && bits != 0 && n >= 0;
+      const int c = pending ? __popc(bits) : 0;
+      // hits of the same row in the lanes before this one
+      int to = n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        to += __popcll(__ballot(c >> i & 1) & same & below) << i;
+      const bool fits = pending && to + c <= kCap;
+      if (fits) {
+        uint64_t* list = at(row) + to;
+#pragma unroll
+        for (int i = 0; i < NZ; ++i)
+          if (bits >> i & 1) *list++ = entry(z[i], tok + i);
+      }
+      const uint64_t done = __ballot(fits) & same;
+      if (fits && done >> lane == 1) w.n[row] = to + c;  // the last of the row
+      pending = pending && !fits;
+      grown = grown || fits;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const uint64_t long_ones = __ballot(pending || (grown && w.n[row] > w.limit[row]));
+      if (long_ones == 0) break;
+      // prune that row's list and its neighbours', 4 rows at a time
+      const int r = __builtin_amdgcn_readlane(row, __builtin_ctzll(long_ones));
+      const int row4 = (r & ~3) + (lane >> 4);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
+      int kept = max(w.n[row4], 0);
+      const bool any = kept > 0;
+      const float bound = prune16<kCap>(a, at(row4), lane, w.mx[row4], kept);
+      if ((lane & 15) == 0 && any) {
+        const bool no_room = kept > kCap - NZ;
+        w.n[row4] = no_room ? kLong : kept;
+        w.thr[row4] = fmaxf(w.thr[row4], bound);
+        w.limit[row4] = min(kCap, max(kPruneAt, kept + 32));
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  // (a row without a list takes no more hits)
+  w.thr[lane] = w.n[lane] < 0 ? INFINITY : fmaxf(w.thr[lane], w.mx[lane] - a.window);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// More than 16 rows: every wave has NT row tiles of its own, K staged in LDS for
+// all of them.
+template <bool BF, int D, int PARTS, int NT>
 __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int split,
                                           ListLds<BF, D>& lds) {
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
   constexpr int QB = PARTS == 1 ? 2 : 4;
-  constexpr int RT = kListTiles<BF, PARTS>;
   typedef Stage<BF, D> St;
   constexpr int ST = St::kTokens;
   constexpr int kQuarter = ST / kChunkWaves;
@@ -550,124 +682,175 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane >> 4, rl = lane & 15;
-  const int nt = ((w.rows + 15) / 16 + kChunkWaves - 1) / kChunkWaves;  // tiles a wave
-  const int wr = wave * nt * 16, wrows = max(min(nt * 16, w.rows - wr), 0);
+  const int wr = wave * NT * 16, wrows = max(min(NT * 16, w.rows - wr), 0);
   const int top = seen(a, w, w.rows - 1);
   const Cache x = cache_of<BF, D>(a, w, top);
   const int stages = (top + ST - 1) / ST, per = (stages + a.splits - 1) / a.splits;
   const int v0 = min(split * per, stages), v1 = min(v0 + per, stages);
 
-  int hi[RT];
-  QFrag<BF, D, PARTS> q[RT];
-  Track tr[RT];
+  auto& mine = sh.rows[wave];
+  mine.n[lane] = 0;
+  mine.limit[lane] = kPruneAt;
+  mine.mx[lane] = mine.thr[lane] = -INFINITY;
+  int hi[NT], queued = 0;
+  QFrag<BF, D, PARTS> q[NT];
+  float thr[NT];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const bool live = t < nt && t * 16 + rl < wrows;
+  for (int t = 0; t < NT; ++t) {
+    thr[t] = -INFINITY;
+    const bool live = t * 16 + rl < wrows;
     hi[t] = live ? seen(a, w, wr + t * 16 + rl) : 0;
     q[t].load(live ? static_cast<const char*>(a.q) + row_at(a, w, wr + t * 16 + rl) * (D * QB)
                    : nullptr, c);
   }
-  // tokens that some, and that all, of this wave's rows see
-  const int some = wrows ? seen(a, w, wr + wrows - 1) : 0, every = wrows ? seen(a, w, wr) : 0;
-  const bool whole = wrows == nt * 16;  // (rows that are none see nothing)
-  auto list = [&](int t) {
-    return [&, t](int row) {
-      // a row past the last has no entries: any address serves
-      const int r = min(wr + t * 16 + row, w.rows - 1);
-      return a.lists + (row_at(a, w, r) * a.splits + split) * kCap;
-    };
+  // tokens below `some` are seen by a row of this wave, below `every` by all
+  const int some = wrows ? seen(a, w, wr + wrows - 1) : 0;
+  const int every = wrows == NT * 16 ? seen(a, w, wr) : 0;
+  auto list = [&](int row) {  // (a row past the last has no hits: any address serves)
+    return a.lists + (row_at(a, w, min(wr + row, w.rows - 1)) * a.splits + split) * kCap;
   };
 
-  int from[kLoads];
+  int to[kLoads];  // where this lane's 16 bytes go
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int at = i * 1024 + lane * 16;
-    const int r = at / St::kRow, slot = at % St::kRow / 16;
-    from[i] = r * St::kRow + ((slot ^ St::swizzle(wave * kQuarter + r)) << 4);
+    const int r = at / St::kRow, ch = at % St::kRow / 16;
+    to[i] = (wave * kQuarter + r) * St::kRow + ((ch ^ St::swizzle(wave * kQuarter + r)) << 4);
   }
-  // page of this wave's quarter of each of the next 64 stages, one a lane
+  // the next 64 stages, one a lane: the page of this wave's quarter, and which
+  // quarters lie in pages of the pool
   int base = v0, pg = -1;
+  uint64_t ok[kChunkWaves];
   auto look = [&](int v) {
     base = v;
-    pg = -1;
-    if (v + lane < v1)
-      pg = page_at(a, x.table, x.npages, ((v + lane) * ST + wave * kQuarter) >> a.ps_bits);
+#pragma unroll
+    for (int k = 0; k < kChunkWaves; ++k) {
+      int p = -1;
+      if (v + lane < v1)
+        p = page_at(a, x.table, x.npages, ((v + lane) * ST + k * kQuarter) >> a.ps_bits);
+      ok[k] = __ballot(p >= 0);
+      if (k == wave) pg = p;
+    }
   };
-  auto stage = [&](int v) {
+  // A stage goes through registers: asked for a stage ahead, put into LDS half
+  // a stage later. (Direct loads into LDS have the compiler wait for all of them
+  // at the next LDS read.)
+  u32x4 raw[kLoads];
+  auto ask = [&](int v) {
     const int p = __builtin_amdgcn_readlane(pg, v - base);
     const int t = v * ST + wave * kQuarter;
     const char* src = x.k.base + (size_t)max(p, 0) * x.k.page_bytes +
                       (size_t)(t & ((1 << a.ps_bits) - 1)) * St::kRow;
-    char* dst = sh.st[v & 1] + wave * (St::kBytes / kChunkWaves);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_global_load_lds(src + from[i], dst + i * 1024, 16, 0, 0);
-    if (lane == 0) sh.ok[v & 1][wave] = p >= 0 ? 1 : 0;
+      raw[i] = *reinterpret_cast<const u32x4*>(src + (i * 1024 + lane * 16));
+  };
+  auto put = [&](int v) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(sh.st[v & 1] + to[i]) = raw[i];
   };
 
-  int limit[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) limit[t] = kCap - TT;
   if (v0 < v1) {
     look(v0);
-    stage(v0);
-    wait_vmcnt<0>();
+    ask(v0);
+    put(v0);
   }
+  wait_vmcnt<0>();  // (the queries too: or the compiler waits for them in the loop)
   __syncthreads();
-  for (int v = v0; v < v1; ++v) {
-    if (v + 1 < v1) {
-      if (v + 1 - base == kWave) look(v + 1);
-      stage(v + 1);
-    }
-    const int ts = v * ST;
-    if (ts < some) {
-      const int4 ok = *reinterpret_cast<const int4*>(sh.ok[v & 1]);
-      const bool full = whole && ts + ST <= every &&
-                        __builtin_amdgcn_readfirstlane(ok.x & ok.y & ok.z & ok.w);
-      const lds_at kst = lds_addr(sh.st[v & 1]);
+  // Tiles in turn, two a stage. A tile's keys are read from LDS while the one
+  // before it is looked through; so the barrier that a stage's keys wait for
+  // lies in the middle of the stage before.
+  int when = v0;  // the stage after which the queues are emptied next
+  KTile<BF, D> kt;
+  if (v0 < v1) kt.read(lds_addr(sh.st[v0 & 1]), 0, lane);
+  unsigned valid = 0;
+  for (int u = 2 * v0; u < 2 * v1; ++u) {
+    const int v = u >> 1, sub = u & 1, t0 = u * TT;
+    if (sub == 0) {
+      valid = 0;  // quarters of this stage (the next may be looked up below)
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        KTile<BF, D> kt;
-        kt.read(kst, sub, lane);
-        const int t0 = ts + sub * TT;
-        float z[RT][NZ], tmax[RT];
-        bool hit = false;
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          if (t >= nt) break;
-          kt.template scores<PARTS>(q[t], z[t]);
-        }
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          if (t >= nt) break;
-          if (!full) {
-            const bool page_ok = (c < 2 ? (sub ? ok.z : ok.x) : (sub ? ok.w : ok.y)) != 0;
-#pragma unroll
-            for (int i = 0; i < NZ; ++i)
-              z[t][i] = page_ok & (t0 + tile_token<BF>(c, i) < hi[t]) ? z[t][i] : -INFINITY;
-          }
-          tmax[t] = max_of(z[t]);
-          hit |= !(tmax[t] <= tr[t].thr);
-        }
-        if (__any(hit)) {
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            if (t >= nt) break;
-            if (!__any(!(tmax[t] <= tr[t].thr))) continue;
-            collect<BF>(a, tr[t], z[t], tmax[t], t0, lane, list(t));
-            if (__any(tr[t].n > limit[t]))
-              prune<kCap>(a, tr[t], kCap - TT, lane, list(t));
-          }
-        }
+      for (int k = 0; k < kChunkWaves; ++k) valid |= (unsigned)(ok[k] >> (v - base) & 1) << k;
+      if (v + 1 < v1) {
+        if (v + 1 - base == kWave) look(v + 1);
+        ask(v + 1);
       }
     }
-    if (v + 1 < v1) wait_vmcnt<0>();
-    __syncthreads();
-  }
+    float z[NT][NZ];
+    __builtin_amdgcn_s_setprio(1);
+    tile_scores<BF, D, PARTS, NT>(kt, q, z);
+    __builtin_amdgcn_s_setprio(0);
+    if (sub == 0) {
+      kt.read(lds_addr(sh.st[v & 1]), 1, lane);
+      if (v + 1 < v1) put(v + 1);
+      __syncthreads();
+    } else {
+      kt.read(lds_addr(sh.st[(v + 1) & 1]), 0, lane);  // (past the last: not used)
+    }
+    uint64_t lanes[NT], any = 0;  // lanes that have hits
+    if (t0 < some) {
+      if (__builtin_expect(valid != (1u << kChunkWaves) - 1 || t0 + TT > every, 0)) {
+        const bool page_ok = valid >> (2 * sub + (c >> 1)) & 1;
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
-    if (c == 0 && t < nt && t * 16 + rl < wrows)
-      a.counts[row_at(a, w, wr + t * 16 + rl) * a.splits + split] = length_of(tr[t]);
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < NZ; ++i)
+            z[t][i] = page_ok & (t0 + tile_token<BF>(c, i) < hi[t]) ? z[t][i] : -INFINITY;
+      }
+      float tmax[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) tmax[t] = max_of(z[t]);
+      // until the bounds have settled, a tile's own maximum goes first
+      if (__builtin_expect(v < v0 + kYoung, 0)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) thr[t] = fmaxf(thr[t], max_across(tmax[t]) - a.window);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        lanes[t] = __ballot(!(tmax[t] <= thr[t]));
+        any |= lanes[t];
+      }
+    }
+    // The queues are emptied by all waves together, about when they hold a batch
+    // (a row's hits become rarer as 1 / tokens): a wave that does so by itself
+    // has the others wait at the next barrier.
+    const bool due = sub == 1 && (v >= when || v + 1 == v1);
+    if (any == 0 && !due) continue;
+    int total = 0;
+    if (any) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) total += __popcll(lanes[t]);
+    }
+    for (;;) {
+      const bool room = queued + total <= kQueue;
+      if (room && any) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (lanes[t] == 0) continue;
+          const int at = __builtin_amdgcn_mbcnt_hi(
+              (unsigned)(lanes[t] >> 32),
+              __builtin_amdgcn_mbcnt_lo((unsigned)lanes[t], (unsigned)queued));
+          if (__builtin_amdgcn_inverse_ballot_w64(lanes[t])) {
+#pragma unroll
+            for (int i = 0; i < NZ / 4; ++i)
+              mine.z[i][at] = f32x4{z[t][4 * i], z[t][4 * i + 1], z[t][4 * i + 2],
+                                    z[t][4 * i + 3]};
+            mine.code[at] = ((t * 16 + rl) << 24) + t0 + tile_token<BF>(c, 0);
+          }
+          queued += __popcll(lanes[t]);
+        }
+      }
+      if (room && !due) break;
+      flush<NZ>(a, mine, queued, lane, list);
+      queued = 0;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) thr[t] = mine.thr[t * 16 + rl];
+      if (room) {
+        when = v + 1 + ((v - v0) >> 3);
+        break;
+      }
+    }
+  }
+  if (lane < wrows) a.counts[row_at(a, w, wr + lane) * a.splits + split] = mine.n[lane];
 }
 
 // At most 16 rows (single tokens): the waves share them and take turns at the
@@ -789,8 +972,12 @@ __global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs 
   if (w.rows == 0) return;
   if (w.rows <= 16)
     list_few<BF, D, PARTS>(a, w, split, lds);
+  else if (w.rows <= 64)
+    list_many<BF, D, PARTS, 1>(a, w, split, lds);
+  else if (kListTiles<BF, PARTS> == 2 || w.rows <= 128)
+    list_many<BF, D, PARTS, 2>(a, w, split, lds);
   else
-    list_many<BF, D, PARTS>(a, w, split, lds);
+    list_many<BF, D, PARTS, kListTiles<BF, PARTS>>(a, w, split, lds);
 }
 
 // ---------------------------------------------------------------------------
