@@ -595,8 +595,7 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
  * entmaxkv_softmax_window; weights are used in float32 or to 2^-17 of
  * themselves (bf16 queries). Results do not depend on what else runs (no
  * atomics on results).
- * Workspace: entmaxkv_entmax_chunk_ws bytes, for either query type and any
- * alpha. Kernels launched: 3 (lists of the tokens that may have a weight; tau
+ * Workspace: entmaxkv_entmax_chunk_ws bytes. Kernels launched: 3 (lists of the tokens that may have a weight; tau
  * and the output; rows whose support is too long for a list).
  */
 int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
@@ -605,7 +604,8 @@ int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_
                           const int32_t* seq_lens, float alpha, void* out, float* tau,
                           int32_t* support, void* ws, size_t ws_bytes, hipStream_t stream,
                           hipEvent_t* events);
-int entmaxkv_entmax_chunk_ws(const entmaxkv_shape* shape, int32_t num_tokens, size_t* bytes);
+int entmaxkv_entmax_chunk_ws(const entmaxkv_shape* shape, int32_t num_tokens, float alpha,
+                             size_t* bytes);
 
 /*
  * Workspace size in bytes for `which` (ENTMAXKV_WS_*) at this shape and

@@ -366,17 +366,13 @@ int prefix_plan(const entmaxkv_shape* shape, int32_t q_dtype, int32_t prefix_pag
   return check_plan(*p);
 }
 
-// q_dtype < 0: of whichever query type needs the larger workspace
-int chunk_plan(const entmaxkv_shape* shape, int32_t q_dtype, int32_t num_tokens, LaunchShape* s,
+int chunk_plan(const entmaxkv_shape* shape, int32_t num_tokens, float alpha, LaunchShape* s,
                ChunkPlan* p) {
   int rc = check_shape(shape, s);
   if (rc) return rc;
   if ((rc = check_num_tokens(num_tokens))) return rc;
-  *p = plan_chunk(*s, q_dtype == ENTMAXKV_BF16, num_tokens);
-  if (q_dtype < 0 && s->bf16) {
-    const ChunkPlan b = plan_chunk(*s, true, num_tokens);
-    if (b.ws_bytes > p->ws_bytes) *p = b;
-  }
+  if ((rc = check_alpha(alpha))) return rc;
+  *p = plan_chunk(*s, num_tokens, alpha);
   return check_grid(p->items > p->tiles ? p->items : p->tiles, p->threads);
 }
 
@@ -873,10 +869,11 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
   return ENTMAXKV_OK;
 }
 
-int entmaxkv_entmax_chunk_ws(const entmaxkv_shape* shape, int32_t num_tokens, size_t* bytes) {
+int entmaxkv_entmax_chunk_ws(const entmaxkv_shape* shape, int32_t num_tokens, float alpha,
+                             size_t* bytes) {
   LaunchShape s;
   ChunkPlan p;
-  if (int rc = chunk_plan(shape, -1, num_tokens, &s, &p)) return rc;
+  if (int rc = chunk_plan(shape, num_tokens, alpha, &s, &p)) return rc;
   if (!bytes) return ENTMAXKV_ERR_INVALID;
   *bytes = p.ws_bytes;
   return ENTMAXKV_OK;
@@ -890,9 +887,8 @@ int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_
                           hipEvent_t* events) {
   LaunchShape s;
   ChunkPlan p;
-  int rc = chunk_plan(shape, q_dtype == ENTMAXKV_BF16 ? q_dtype : ENTMAXKV_F32, num_tokens, &s, &p);
+  int rc = chunk_plan(shape, num_tokens, alpha, &s, &p);
   if (rc) return rc;
-  if ((rc = check_alpha(alpha))) return rc;
   if ((rc = check_q_dtype(s, q_dtype))) return rc;
   if (!q || !token_starts || !k_pool || !v_pool || !block_table || !seq_lens || !out)
     return ENTMAXKV_ERR_INVALID;

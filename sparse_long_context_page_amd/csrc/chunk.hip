@@ -22,6 +22,12 @@ namespace {
 
 constexpr int kChunkWaves = 4;
 
+struct __align__(16) Part {
+  int32_t n;        // entries, or why there are none
+  float mx, slack;  // the largest score; how far two scores may be off together
+  int32_t unused;
+};
+
 struct ChunkArgs {
   const void* q;
   const void* k_pool;
@@ -36,16 +42,23 @@ struct ChunkArgs {
   float am1, m;  // alpha - 1 and 1 / (alpha - 1)
   float window;  // of a score below the row's maximum that may have a weight
   int whole;     // m if it is 1, 2, 3 or 4, else 0
-  int splits;    // parts of a row's tokens
-  // workspace: per (row, part) the list and its length, and per 16 rows whether
-  // they need the dense kernel
+  int tok_bits;  // 2^tok_bits tokens a list block
+  int splits, few_splits;  // parts of a row's tokens; of blocks of at most 16 rows
+  int cap;                 // entries of a list
+  size_t few_parts;        // the first of the few-row blocks' parts
+  unsigned few_items;      // their workgroups
+  // workspace: per (row, part) the list, its length and how far its scores may
+  // be off together, and per 16 rows whether they need the dense kernel
   uint64_t* lists;
-  int32_t* counts;
+  Part* parts;
   int32_t* dense;
 };
 
-// Entries of a list, and from how many it is pruned for the first time.
-constexpr int kCap = 128, kPruneAt = 96;
+// Entries of a list by alpha: support sizes grow as alpha falls (scores of
+// spread 2.5, 32K tokens: 8 tokens on average and 20 at most at alpha 1.5, 67 and
+// 140 at 1.25, 200 rows each). Fewer entries are a smaller workspace and, in the
+// finish kernel, more workgroups a CU.
+constexpr int cap_of(float alpha) { return alpha >= 1.5f ? 128 : 256; }
 // Lengths that say why there is no list.
 constexpr int kLong = -1;    // the support does not fit
 constexpr int kNoNumber = -2;  // a score is NaN or +inf
@@ -89,6 +102,35 @@ __device__ __forceinline__ int seen(const ChunkArgs& a, const Rows& w, int r) {
 __device__ __forceinline__ size_t row_at(const ChunkArgs& a, const Rows& w, int r) {
   const int i = r >> a.g_bits;
   return (size_t)(w.tok0 + i) * a.H + (w.g << a.g_bits) + (r - (i << a.g_bits));
+}
+
+// The block of a sequence's last tokens (of several, the only one that may have
+// few rows).
+__device__ __forceinline__ Rows last_rows(const ChunkArgs& a, int b, int g) {
+  Rows r;
+  const int s = clamp_len(a.starts[b], a.N);
+  r.b = b;
+  r.g = g;
+  r.n = clamp_len(a.starts[b + 1], a.N) - s;
+  r.i0 = max(r.n - 1, 0) & ~((1 << a.tok_bits) - 1);
+  r.tok0 = s + r.i0;
+  r.rows = max(r.n - r.i0, 0) << a.g_bits;
+  r.L = clamp_len(a.seq_lens[b], a.max_pages << a.ps_bits);
+  return r;
+}
+
+// The first of the parts of row r of a list block, and how many. The parts of a
+// block of few rows are more, for single tokens over long caches, and lie by
+// sequence.
+struct Parts {
+  size_t first;
+  int count;
+};
+__device__ __forceinline__ Parts parts_of(const ChunkArgs& a, const Rows& w, int r) {
+  if (w.rows <= 16)
+    return Parts{a.few_parts + (((size_t)w.b * a.Hkv + w.g) * 16 + r) * a.few_splits,
+                 a.few_splits};
+  return Parts{row_at(a, w, r) * a.splits, a.splits};
 }
 
 __device__ __forceinline__ int page_at(const ChunkArgs& a, const int32_t* table, int npages,
@@ -363,6 +405,13 @@ __device__ __forceinline__ float max16(float x) {
   x = fmaxf(x, partner<4>(x));
   return fmaxf(x, partner<8>(x));
 }
+template <typename T, typename Op>
+__device__ __forceinline__ T reduce16(T x, Op op) {
+  x = op(x, partner<1>(x));
+  x = op(x, partner<2>(x));
+  x = op(x, partner<4>(x));
+  return op(x, partner<8>(x));
+}
 // NaN if one is among them; no LDS traffic
 __device__ __forceinline__ float max_across(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -415,42 +464,47 @@ struct Track {
 };
 
 // Prunes one row's list to the tokens above the threshold of what it holds: 16
-// lanes a row, CAP / 16 entries a lane in registers. Returns that threshold;
-// n: its length, before and after.
-template <int CAP>
+// lanes a row, up to 128 entries in their registers, more read again for every
+// step. Returns that threshold (entries are kept from `slack` below it); n: its
+// length, before and after.
 __device__ __forceinline__ float prune16(const ChunkArgs& a, uint64_t* list, int lane, float mx,
-                                         int& n) {
+                                         float slack, int& n) {
+  constexpr int kRegs = 8;
   const int sub = lane & 15;
-  uint64_t e[CAP / 16];
+  uint64_t e[kRegs];
 #pragma unroll
-  for (int i = 0; i < CAP / 16; ++i)
+  for (int i = 0; i < kRegs; ++i)
     e[i] = i * 16 + sub < n ? list[i * 16 + sub] : entry(-INFINITY, 0);
   const float t = solve16(a, mx, n > 0, [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < CAP / 16; ++i) f(entry_z(e[i]));
+    for (int i = 0; i < kRegs; ++i) f(entry_z(e[i]));
+    for (int i = kRegs * 16 + sub; i < n; i += 16) f(entry_z(list[i]));
   });
   const float thr = bound_of(a, mx, t);
   int kept = 0;
-#pragma unroll
-  for (int i = 0; i < CAP / 16; ++i) {
-    const bool keep = i * 16 + sub < n && !(entry_z(e[i]) <= thr);
+  auto keep_of = [&](uint64_t x, bool real) {
+    const bool keep = real && !(entry_z(x) <= thr - slack);
     const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
-    if (keep) list[kept + __popc(all & ((1u << sub) - 1))] = e[i];
+    if (keep) list[kept + __popc(all & ((1u << sub) - 1))] = x;
     kept += __popc(all);
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) keep_of(e[i], i * 16 + sub < n);
+  for (int i = kRegs * 16; i < n; i += 16)  // (entries move forward only)
+    keep_of(i + sub < n ? list[i + sub] : 0, i + sub < n);
   n = kept;
   return thr;
 }
 
 // The lists of the 16 rows of a tile, 4 rows at a time. at(row): its list.
-template <int CAP, typename At>
+template <typename At>
 __device__ __forceinline__ void prune(const ChunkArgs& a, Track& tr, int room, int lane, At at) {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {
     const int row = k * 4 + (lane >> 4);
     int kept = max(__shfl(tr.n, row, kWave), 0);
-    const float thr = prune16<CAP>(a, at(row), lane, __shfl(tr.mx, row, kWave), kept);
+    const float thr = prune16(a, at(row), lane, __shfl(tr.mx, row, kWave), 0.0f, kept);
     // back to the lanes that hold these rows' scores
     const int from = ((lane & 3) << 4), mine = (lane & 15) >> 2;
     const int kn = __shfl(kept, from, kWave);
@@ -520,11 +574,39 @@ __device__ __forceinline__ Cache cache_of(const ChunkArgs& a, const Rows& w, int
 
 constexpr int kYoung = 4;  // stages
 
-// Row tiles a wave holds. bf16 queries: 64 rows share each K operand read from
-// LDS. Three parts of a float32 query, and float32 rows, take the registers of
-// more.
-template <bool BF, int PARTS>
-constexpr int kListTiles = BF && PARTS == 1 ? 4 : 2;
+// Row tiles a wave holds: with a bf16 cache 64 rows share each K operand read from
+// LDS; float32 rows take the registers of more.
+template <bool BF>
+constexpr int kListTiles = BF ? 4 : 2;
+
+// A float32 query over bf16 keys takes three bf16 parts to be exact. To look for
+// the few tokens that matter its nearest bf16 does: a score of it is off by at
+// most e = sum |q - q'| * max |k| (both known), so that no token within 2 e of a
+// bound is dropped; the finish kernel takes those that are left once more, in
+// float32. (Three parts in this kernel: 1.20 ms for the mixed batch of 32, one:
+// see below.)
+template <int D>
+__device__ __forceinline__ void load_nearest(QFrag<true, D, 1>& q, const char* row, int c,
+                                             float& off) {
+  off = 0.0f;
+#pragma unroll
+  for (int s = 0; s < D / 32; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 x = row ? *reinterpret_cast<const f32x4*>(row + 4 * (s * 32 + c * 8 + 4 * h))
+                          : f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t b = nearest2(x[2 * e], x[2 * e + 1]);
+        q.f[0][s][2 * h + e] = b;
+        // (2^-18: the sum of products of that part, in float32)
+        off += fabsf(x[2 * e] - __uint_as_float(b << 16)) +
+               fabsf(x[2 * e + 1] - __uint_as_float(b & 0xffff0000u)) +
+               (fabsf(x[2 * e]) + fabsf(x[2 * e + 1])) * 0x1p-18f;
+      }
+    }
+  off = group_sum(off);
+}
 
 // Scores of a K tile and NT row tiles: all of them take a step before any
 // takes the next, so that no matrix instruction waits for the one before it.
@@ -567,8 +649,9 @@ template <int NZ>
 struct WaveRows {
   f32x4 z[NZ / 4][kQueue];
   int code[kQueue];       // row << 24 | the lane's first token
-  float mx[64], thr[64];  // thr: what a score has to pass
+  float mx[64], thr[64];  // thr: what a score has to pass, but for `off`
   int n[64], limit[64];   // limit: entries from which a list is pruned
+  float off[64];          // of the row's scores, by the largest |key|
 };
 
 template <bool BF, int D>
@@ -576,6 +659,7 @@ union ListLds {
   struct {
     char st[2][Stage<BF, D>::kBytes];
     WaveRows<scores_per_lane<BF>()> rows[kChunkWaves];
+    __align__(16) float kmax[2][kChunkWaves];
   } many;
   struct {
     uint64_t list[kChunkWaves][16][kFewCap];
@@ -587,7 +671,7 @@ union ListLds {
 // in the order of the queue. at(row): a row's list.
 template <int NZ, typename At>
 __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int count, int lane,
-                                      At at) {
+                                      float kmax, At at) {
   const uint64_t below = lanemask_below(lane);
 #pragma unroll 1
   for (int b = 0; b < count; b += kBatch) {
@@ -618,7 +702,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
     for (;;) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       const int n = w.n[row];
-      const float thr = fmaxf(w.thr[row], w.mx[row] - a.window);
+      const float thr = fmaxf(w.thr[row], w.mx[row] - a.window) - 2.0f * kmax * w.off[row];
       unsigned bits = 0;
 #pragma unroll
       for (int i = 0; i < NZ; ++i) bits |= (z[i] > thr ? 1u : 0u) << i;
@@ -629,7 +713,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         to += __popcll(__ballot(c >> i & 1) & same & below) << i;
-      const bool fits = pending && to + c <= kCap;
+      const bool fits = pending && to + c <= a.cap;
       if (fits) {
         uint64_t* list = at(row) + to;
 #pragma unroll
@@ -649,12 +733,13 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
       int kept = max(w.n[row4], 0);
       const bool any = kept > 0;
-      const float bound = prune16<kCap>(a, at(row4), lane, w.mx[row4], kept);
+      const float bound = prune16(a, at(row4), lane, w.mx[row4],
+                                  2.0f * kmax * w.off[row4], kept);
       if ((lane & 15) == 0 && any) {
-        const bool no_room = kept > kCap - NZ;
+        const bool no_room = kept > a.cap - NZ;
         w.n[row4] = no_room ? kLong : kept;
         w.thr[row4] = fmaxf(w.thr[row4], bound);
-        w.limit[row4] = min(kCap, max(kPruneAt, kept + 32));
+        w.limit[row4] = min(a.cap, max(a.cap * 3 / 4, kept + a.cap / 4));
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     }
@@ -673,6 +758,8 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
   constexpr int QB = PARTS == 1 ? 2 : 4;
+  constexpr bool kNear = BF && PARTS > 1;  // scores of the queries' nearest bf16
+  constexpr int QP = kNear ? 1 : PARTS;
   typedef Stage<BF, D> St;
   constexpr int ST = St::kTokens;
   constexpr int kQuarter = ST / kChunkWaves;
@@ -690,24 +777,32 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
 
   auto& mine = sh.rows[wave];
   mine.n[lane] = 0;
-  mine.limit[lane] = kPruneAt;
+  mine.limit[lane] = a.cap * 3 / 4;
   mine.mx[lane] = mine.thr[lane] = -INFINITY;
   int hi[NT], queued = 0;
-  QFrag<BF, D, PARTS> q[NT];
-  float thr[NT];
+  QFrag<BF, D, QP> q[NT];
+  float thr[NT], off[NT], kmax = 0.0f;
+  mine.off[lane] = 0.0f;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     thr[t] = -INFINITY;
+    off[t] = 0.0f;
     const bool live = t * 16 + rl < wrows;
     hi[t] = live ? seen(a, w, wr + t * 16 + rl) : 0;
-    q[t].load(live ? static_cast<const char*>(a.q) + row_at(a, w, wr + t * 16 + rl) * (D * QB)
-                   : nullptr, c);
+    const char* row =
+        live ? static_cast<const char*>(a.q) + row_at(a, w, wr + t * 16 + rl) * (D * QB) : nullptr;
+    if constexpr (kNear) {
+      load_nearest<D>(q[t], row, c, off[t]);
+      if (c == 0) mine.off[t * 16 + rl] = off[t];
+    } else {
+      q[t].load(row, c);
+    }
   }
   // tokens below `some` are seen by a row of this wave, below `every` by all
   const int some = wrows ? seen(a, w, wr + wrows - 1) : 0;
   const int every = wrows == NT * 16 ? seen(a, w, wr) : 0;
   auto list = [&](int row) {  // (a row past the last has no hits: any address serves)
-    return a.lists + (row_at(a, w, min(wr + row, w.rows - 1)) * a.splits + split) * kCap;
+    return a.lists + (row_at(a, w, min(wr + row, w.rows - 1)) * a.splits + split) * a.cap;
   };
 
   int to[kLoads];  // where this lane's 16 bytes go
@@ -748,6 +843,39 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
   auto put = [&](int v) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(sh.st[v & 1] + to[i]) = raw[i];
+    if constexpr (kNear) {
+      // the largest |key| of this quarter's tokens that some row sees; one that is
+      // no finite number gives scores that are none, and needs no room
+      const bool valid_page = ok[wave] >> (v - base) & 1;
+      const int left = valid_page ? top - v * ST - wave * kQuarter : 0;  // tokens seen
+      u16x2 big = {0, 0};
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          big = __builtin_elementwise_max(big,
+                                          __builtin_bit_cast(u16x2, raw[i][e] & 0x7fff7fffu));
+      int m = wave_max((int)max(big[0], big[1]));
+      if (__builtin_expect(left < kQuarter || m >= 0x7f80, 0)) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int lo = raw[i][e] & 0x7fff, hi = raw[i][e] >> 16 & 0x7fff;
+            const bool use = (i * 1024 + lane * 16) / St::kRow < left;
+            m = max(m, use && lo < 0x7f80 ? lo : 0);
+            m = max(m, use && hi < 0x7f80 ? hi : 0);
+          }
+        m = wave_max(m);
+      }
+      if (lane == 0) sh.kmax[v & 1][wave] = __uint_as_float((uint32_t)m << 16);
+    }
+  };
+  // thr: the rows' bounds less what the scores may be off
+  auto refresh = [&] {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) thr[t] = mine.thr[t * 16 + rl] - 2.0f * kmax * off[t];
   };
 
   if (v0 < v1) {
@@ -774,10 +902,18 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
         if (v + 1 - base == kWave) look(v + 1);
         ask(v + 1);
       }
+      if constexpr (kNear) {
+        const f32x4 k = *reinterpret_cast<const f32x4*>(sh.kmax[v & 1]);
+        const float m = fmaxf(fmaxf(k[0], k[1]), fmaxf(k[2], k[3]));
+        if (m > kmax) {
+          kmax = m;
+          refresh();
+        }
+      }
     }
     float z[NT][NZ];
     __builtin_amdgcn_s_setprio(1);
-    tile_scores<BF, D, PARTS, NT>(kt, q, z);
+    tile_scores<BF, D, QP, NT>(kt, q, z);
     __builtin_amdgcn_s_setprio(0);
     if (sub == 0) {
       kt.read(lds_addr(sh.st[v & 1]), 1, lane);
@@ -802,7 +938,8 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
       // until the bounds have settled, a tile's own maximum goes first
       if (__builtin_expect(v < v0 + kYoung, 0)) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) thr[t] = fmaxf(thr[t], max_across(tmax[t]) - a.window);
+        for (int t = 0; t < NT; ++t)
+          thr[t] = fmaxf(thr[t], max_across(tmax[t]) - a.window - 2.0f * kmax * off[t]);
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -840,17 +977,18 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
         }
       }
       if (room && !due) break;
-      flush<NZ>(a, mine, queued, lane, list);
+      flush<NZ>(a, mine, queued, lane, kmax, list);
       queued = 0;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) thr[t] = mine.thr[t * 16 + rl];
+      refresh();
       if (room) {
         when = v + 1 + ((v - v0) >> 3);
         break;
       }
     }
   }
-  if (lane < wrows) a.counts[row_at(a, w, wr + lane) * a.splits + split] = mine.n[lane];
+  if (lane < wrows)
+    a.parts[row_at(a, w, wr + lane) * a.splits + split] =
+        Part{mine.n[lane], mine.mx[lane], 2.0f * kmax * mine.off[lane], 0};
 }
 
 // At most 16 rows (single tokens): the waves share them and take turns at the
@@ -870,7 +1008,7 @@ __device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int 
   const int top = seen(a, w, w.rows - 1), every = w.rows == 16 ? seen(a, w, 0) : 0;
   const int hi = rl < w.rows ? seen(a, w, rl) : 0;
   const Cache x = cache_of<BF, D>(a, w, top);
-  const int tiles = (top + TT - 1) / TT, per = (tiles + a.splits - 1) / a.splits;
+  const int tiles = (top + TT - 1) / TT, per = (tiles + a.few_splits - 1) / a.few_splits;
   const int v0 = min(split * per, tiles), v1 = min(v0 + per, tiles);
 
   QFrag<BF, D, PARTS> q;
@@ -910,7 +1048,7 @@ __device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int 
       const float tmax = max_of(z);
       if (__any(!(tmax <= tr.thr))) {
         collect<BF>(a, tr, z, tmax, t0, lane, list);
-        if (__any(tr.n > kFewCap - TT)) prune<kFewCap>(a, tr, kFewCap - TT, lane, list);
+        if (__any(tr.n > kFewCap - TT)) prune(a, tr, kFewCap - TT, lane, list);
       }
     }
   }
@@ -937,13 +1075,13 @@ __device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int 
   float thr = mx - a.window;
   int most = 0;
   each([&](uint64_t e) { most += entry_z(e) > thr ? 1 : 0; });
-  const bool much = sum16((float)most) > (float)kCap;
+  const bool much = sum16((float)most) > (float)a.cap;
   if (__any(much)) {
     const float t = solve16(a, mx, much, [&](auto f) { each([&](uint64_t e) { f(entry_z(e)); }); });
     if (much) thr = fmaxf(thr, bound_of(a, mx, t));
   }
   const bool real = row < w.rows;
-  const size_t part = row_at(a, w, min(row, w.rows - 1)) * a.splits + split;
+  const size_t part = parts_of(a, w, row).first + split;
   int kept = 0;
 #pragma unroll
   for (int v = 0; v < NW; ++v)
@@ -952,46 +1090,55 @@ __device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int 
       const bool keep = i + sub < n[v] && entry_z(e) > thr;
       const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
       const int at = kept + __popc(all & ((1u << sub) - 1));
-      if (keep && real && at < kCap) a.lists[part * kCap + at] = e;
+      if (keep && real && at < a.cap) a.lists[part * a.cap + at] = e;
       kept += __popc(all);
     }
-  if (sub == 0 && real) a.counts[part] = worst < 0 ? worst : kept > kCap ? kLong : kept;
+  if (sub == 0 && real)
+    a.parts[part] = Part{worst < 0 ? worst : kept > a.cap ? kLong : kept, mx, 0.0f, 0};
 }
 
-template <bool BF, int D, int PARTS>
-constexpr int kListRows = kChunkWaves * 16 * kListTiles<BF, PARTS>;
+template <bool BF>
+constexpr int kListRows = kChunkWaves * 16 * kListTiles<BF>;
 
 template <bool BF, int D, int PARTS>
-__global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs a, int tok_bits) {
+__global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs a) {
   __shared__ __align__(1024) ListLds<BF, D> lds;
   // over the KV heads first: with 8 of them, the blocks that read the same
-  // head's tokens share an XCD and its L2; then the parts
-  const int x = blockIdx.x / a.Hkv, g = blockIdx.x - x * a.Hkv;
-  const int id = x / a.splits, split = x - id * a.splits;
-  const Rows w = find_rows(a, tok_bits, id, g, threadIdx.x & (kWave - 1));
-  if (w.rows == 0) return;
-  if (w.rows <= 16)
+  // head's tokens share an XCD and its L2; then the parts. The blocks of few rows
+  // come first: they are bound by memory, those that start beside them are not.
+  const bool few = blockIdx.x < a.few_items;
+  const int item = few ? blockIdx.x : blockIdx.x - a.few_items;
+  const int splits = few ? a.few_splits : a.splits;
+  const int x = item / a.Hkv, g = item - x * a.Hkv;
+  const int id = x / splits, split = x - id * splits;
+  const Rows w = few ? last_rows(a, id, g)
+                     : find_rows(a, a.tok_bits, id, g, threadIdx.x & (kWave - 1));
+  if (w.rows == 0 || few != w.rows <= 16) return;
+  if (few)
     list_few<BF, D, PARTS>(a, w, split, lds);
   else if (w.rows <= 64)
     list_many<BF, D, PARTS, 1>(a, w, split, lds);
-  else if (kListTiles<BF, PARTS> == 2 || w.rows <= 128)
+  else if (kListTiles<BF> == 2 || w.rows <= 128)
     list_many<BF, D, PARTS, 2>(a, w, split, lds);
   else
-    list_many<BF, D, PARTS, kListTiles<BF, PARTS>>(a, w, split, lds);
+    list_many<BF, D, PARTS, kListTiles<BF>>(a, w, split, lds);
 }
 
 // ---------------------------------------------------------------------------
 // tau and the output from the lists
 
-constexpr int kJoinCap = 256;  // joint entries of a row that may have a weight
-
-// 16 lanes a row, 16 rows a workgroup (as dense_kernel takes them). Each lane
-// gathers D / 16 coordinates of the support's V rows.
-template <bool BF, int D, int PARTS>
+// 16 lanes a row, 16 rows a workgroup (as dense_kernel takes them). A row's
+// entries go straight to the lanes' registers, LE a lane, where there are few
+// enough of them, else through LDS, pruned. Each lane gathers D / 16 coordinates
+// of the support's V rows. Bound by latency: lengths, entries, pages and V rows wait for
+// each other, so a workgroup is small and many share a CU.
+template <bool BF, int D, int PARTS, int LE>
 __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a, int tok_bits) {
+  constexpr int kJoinCap = 16 * LE;
   constexpr int kElem = BF ? 2 : 4, kPer = D / 16;
   typedef uint32_t vec __attribute__((ext_vector_type(kPer * kElem / 4)));
   __shared__ uint64_t joint[16][kJoinCap];
+  __shared__ int length[16][kChunkMaxSplits];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), sub = tid & 15, row = tid >> 4;
   const int id = blockIdx.x / a.Hkv, g = blockIdx.x - id * a.Hkv;
   const Rows w = find_rows(a, tok_bits, id, g, lane);
@@ -1001,83 +1148,193 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
   }
   const bool real = row < w.rows;
   const size_t at = row_at(a, w, min(row, w.rows - 1));
-  const uint64_t* lists = a.lists + at * a.splits * kCap;
-  const int32_t* counts = a.counts + at * a.splits;
+  // the list block that the row is in, and its parts
+  const int past = w.i0 & ((1 << a.tok_bits) - 1);  // tokens of that block before this tile
+  Rows lw = w;
+  lw.i0 -= past;
+  lw.tok0 -= past;
+  lw.rows = min(1 << a.tok_bits, w.n - lw.i0) << a.g_bits;
+  const Parts pt = parts_of(a, lw, min(row, w.rows - 1) + (past << a.g_bits));
+  const uint64_t* lists = a.lists + pt.first * a.cap;
+  const Part* parts = a.parts + pt.first;
   uint64_t* list = joint[row];
 
-  // f(entry) for this lane's entries
-  auto each = [&](auto f) {
-    for (int s = 0; s < a.splits; ++s) {
-      const int m = counts[s];
-      for (int i = sub; i < m; i += 16) f(lists[s * kCap + i]);
-    }
-  };
   int worst = 0, total = 0;
-  for (int s = 0; s < a.splits; ++s) {
-    worst = min(worst, counts[s]);
-    total += max(counts[s], 0);
+  float mx = -INFINITY, slack = 0.0f;
+  for (int i = sub; i < pt.count; i += 16) {
+    const Part part = parts[i];
+    length[row][i] = max(part.n, 0);
+    worst = min(worst, part.n);
+    total += max(part.n, 0);
+    slack = fmaxf(slack, part.slack);
+    if (part.n > 0) mx = fmaxf(mx, part.mx);
   }
-  float mx = -INFINITY;
-  each([&](uint64_t e) { mx = fmaxf(mx, entry_z(e)); });
+  worst = reduce16(worst, [](int x, int y) { return min(x, y); });
+  total = reduce16(total, [](int x, int y) { return x + y; });
+  slack = max16(slack);
   mx = max16(mx);
-  float thr = mx - a.window;
-  if (__any(total > kJoinCap)) {
-    // perhaps more than fit within the window: above the joint threshold, then
-    int most = 0;
-    each([&](uint64_t e) { most += entry_z(e) > thr ? 1 : 0; });
-    const bool much = sum16((float)most) > (float)kJoinCap;
-    if (__any(much)) {
-      const float t =
-          solve16(a, mx, much, [&](auto f) { each([&](uint64_t e) { f(entry_z(e)); }); });
-      if (much) thr = fmaxf(thr, bound_of(a, mx, t));
+  if (worst < 0) total = 0;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+
+  // this lane's entries sub, sub + 16, ... of the row's n
+  uint64_t e[LE];
+#pragma unroll
+  for (int i = 0; i < LE; ++i) e[i] = entry(-INFINITY, 0);
+  int n = total;
+  if (!__any(total > kJoinCap || pt.count > 4)) {
+    int before = 0;
+    for (int s = 0; s < pt.count; ++s) {
+      const int m = total > 0 ? length[row][s] : 0;
+#pragma unroll
+      for (int i = 0; i < LE; ++i) {
+        const int j = i * 16 + sub - before;
+        if (j >= 0 && j < m) e[i] = lists[s * a.cap + j];
+      }
+      before += m;
     }
-  }
-  int n = 0;
-  for (int s = 0; s < a.splits; ++s) {
-    const int m = counts[s];
-    for (int i = 0; i < m; i += 16) {
-      const uint64_t e = i + sub < m ? lists[s * kCap + i + sub] : 0;
-      const bool keep = i + sub < m && entry_z(e) > thr;
-      const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
-      const int to = n + __popc(all & ((1u << sub) - 1));
-      if (keep && to < kJoinCap) list[to] = e;
-      n += __popc(all);
+  } else {
+    // many: through LDS those that may have a weight, by the joint maximum, or by
+    // the joint threshold if that is too much
+    auto gather = [&](float thr) {
+      int k = 0;
+      auto take = [&](uint64_t x, bool mine) {
+        const bool keep = mine && !(entry_z(x) <= thr);
+        const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
+        const int to = k + __popc(all & ((1u << sub) - 1));
+        if (keep && to < kJoinCap) list[to] = x;
+        k += __popc(all);
+      };
+      constexpr int U = 4;  // parts on their way
+      for (int s = 0; s < pt.count; s += U) {
+        uint64_t x[U];
+        int m[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          m[u] = s + u < pt.count && total > 0 ? length[row][s + u] : 0;
+          x[u] = sub < m[u] ? lists[(s + u) * a.cap + sub] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          take(x[u], sub < m[u]);
+          for (int i = 16; i < m[u]; i += 16)
+            take(i + sub < m[u] ? lists[(s + u) * a.cap + i + sub] : 0, i + sub < m[u]);
+        }
+      }
+      return k;
+    };
+    n = gather(mx - a.window - slack);
+    if (__any(n > kJoinCap)) {
+      const float t = solve16(a, mx, n > kJoinCap, [&](auto f) {
+        if (n <= kJoinCap) return;
+        for (int s = 0; s < pt.count; ++s)
+          for (int i = sub; i < length[row][s]; i += 16) f(entry_z(lists[s * a.cap + i]));
+      });
+      n = gather((n > kJoinCap ? bound_of(a, mx, t) : mx - a.window) - slack);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < LE; ++i)
+      if (i * 16 + sub < n) e[i] = list[i * 16 + sub];
   }
-  const bool dense = worst == kLong || (worst == 0 && n > kJoinCap);
-  n = worst < 0 ? 0 : min(n, kJoinCap);
-  const int dense_rows_here = __syncthreads_count(dense && real);  // (and the lists are written)
+  const bool dense = worst == kLong || n > kJoinCap;
+  const int dense_rows_here = __syncthreads_count(dense && real);
   if (tid == 0) a.dense[blockIdx.x] = dense_rows_here > 0;
   if (dense_rows_here) return;
 
-  const float t = solve16(a, mx, n > 0, [&](auto f) {
-    for (int i = sub; i < n; i += 16) f(entry_z(list[i]));
-  });
-  // the support: its weights and V rows take the places of its scores and tokens
+  const char* kb = static_cast<const char*>(a.k_pool) + ((size_t)g << a.ps_bits) * (D * kElem) +
+                   sub * (kPer * kElem);
+  const char* vb = static_cast<const char*>(a.v_pool) + ((size_t)g << a.ps_bits) * (D * kElem) +
+                   sub * (kPer * kElem);
+  const size_t page_bytes = ((size_t)a.Hkv << a.ps_bits) * (D * kElem);
+  // this lane's coordinates of K or V row `slot` (page * page_size + row)
+  auto row_of = [&](const char* base, int slot) {
+    return *reinterpret_cast<const vec*>(base + (size_t)(slot >> a.ps_bits) * page_bytes +
+                                         (size_t)(slot & ((1 << a.ps_bits) - 1)) * (D * kElem));
+  };
+  auto coord = [](const vec& v, int d) {
+    return BF ? (d & 1 ? bf16_hi(v[d / 2]) : bf16_lo(v[d / 2])) : __uint_as_float(v[BF ? 0 : d]);
+  };
+  const int32_t* table = a.block_table + (size_t)w.b * a.max_pages;
+  auto slot_of = [&](int tok) {
+    return (table[tok >> a.ps_bits] << a.ps_bits) + (tok & ((1 << a.ps_bits) - 1));
+  };
+  auto solve = [&] {
+    mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < LE; ++i) mx = fmaxf(mx, entry_z(e[i]));
+    mx = max16(mx);
+    return solve16(a, mx, n > 0, [&](auto f) {
+#pragma unroll
+      for (int i = 0; i < LE; ++i)
+        if (i == 0 || __any(i * 16 < n)) f(entry_z(e[i]));
+    });
+  };
+  float t = solve();
+  // scores of rounded queries: those that may be in the support again, in float32
+  const bool again = BF && PARTS > 1 && __any(slack > 0.0f);
+  if (again) {
+    const float thr = bound_of(a, mx, t) - slack;
+    int kept = 0;
+#pragma unroll
+    for (int i = 0; i < LE; ++i) {
+      if (!__any(i * 16 < n)) break;
+      const bool keep = i * 16 + sub < n && !(entry_z(e[i]) <= thr);
+      const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
+      if (keep)
+        list[kept + __popc(all & ((1u << sub) - 1))] = entry(0.0f, slot_of(entry_t(e[i])));
+      kept += __popc(all);
+    }
+    n = kept;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float q[kPer];
+#pragma unroll
+    for (int d = 0; d < kPer; ++d)
+      q[d] = static_cast<const float*>(a.q)[at * D + sub * kPer + d];
+    constexpr int U = 8;  // rows on their way
+    for (int i = 0; i < n; i += U) {
+      vec k[U];
+      int slot[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        slot[j] = entry_t(list[min(i + j, n - 1)]);
+        k[j] = row_of(kb, slot[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        float z = 0.0f;
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) z = fmaf(q[d], coord(k[j], d), z);
+        z = sum16(z);
+        if (sub == 0 && i + j < n) list[i + j] = entry(z, slot[j]);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < LE; ++i)
+      e[i] = i * 16 + sub < n ? list[i * 16 + sub] : entry(-INFINITY, 0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    t = solve();
+  }
+  // the support: its weights and V rows, to LDS in order
   float l = 0.0f;
   int live = 0;
-  const int32_t* table = a.block_table + (size_t)w.b * a.max_pages;
-  for (int i = 0; i < n; i += 16) {
-    const uint64_t e = i + sub < n ? list[i + sub] : entry(-INFINITY, 0);
-    const float u = fmaxf((entry_z(e) - mx) * a.am1 - t, 0.0f);
+#pragma unroll
+  for (int i = 0; i < LE; ++i) {
+    if (!__any(i * 16 < n)) break;
+    const float u = n > 0 ? fmaxf((entry_z(e[i]) - mx) * a.am1 - t, 0.0f) : 0.0f;
     float p, pm1;
     powers(a, u, p, pm1);
     l += p;
     const bool keep = u > 0.0f;
     const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
-    const int tok = entry_t(e);
-    if (keep) {
-      const int page = table[tok >> a.ps_bits];
+    if (keep)
       list[live + __popc(all & ((1u << sub) - 1))] =
-          entry(p, (page << a.ps_bits) + (tok & ((1 << a.ps_bits) - 1)));
-    }
+          entry(p, again ? entry_t(e[i]) : slot_of(entry_t(e[i])));
     live += __popc(all);
   }
   l = sum16(l);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
-  const char* vb = static_cast<const char*>(a.v_pool) +
-                   ((size_t)g << a.ps_bits) * (D * kElem) + sub * (kPer * kElem);
-  const size_t page_bytes = ((size_t)a.Hkv << a.ps_bits) * (D * kElem);
   float acc[kPer];
 #pragma unroll
   for (int d = 0; d < kPer; ++d) acc[d] = 0.0f;
@@ -1087,21 +1344,15 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
     vec v[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const uint64_t e = list[min(i + k, live - 1)];
-      const int r = entry_t(e);
-      p[k] = i + k < live ? entry_z(e) : 0.0f;
-      v[k] = *reinterpret_cast<const vec*>(vb + (size_t)(r >> a.ps_bits) * page_bytes +
-                                           (size_t)(r & ((1 << a.ps_bits) - 1)) * (D * kElem));
+      const uint64_t x = list[min(i + k, live - 1)];
+      p[k] = entry_z(x);
+      v[k] = row_of(vb, entry_t(x));
     }
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       if (i + k >= live) break;
 #pragma unroll
-      for (int d = 0; d < kPer; ++d) {
-        const float x = BF ? (d & 1 ? bf16_hi(v[k][d / 2]) : bf16_lo(v[k][d / 2]))
-                           : __uint_as_float(v[k][BF ? 0 : d]);
-        acc[d] = fmaf(p[k], x, acc[d]);
-      }
+      for (int d = 0; d < kPer; ++d) acc[d] = fmaf(p[k], coord(v[k], d), acc[d]);
     }
   }
   if (!real) return;
@@ -1129,11 +1380,13 @@ template <bool BF, int D, int PARTS>
 hipError_t launch(const ChunkArgs& a, const ChunkPlan& p, int kernel, hipStream_t st) {
   const dim3 threads(kChunkWaves * kWave);
   if (kernel == 0)
-    hipLaunchKernelGGL((list_kernel<BF, D, PARTS>), dim3((unsigned)p.items), threads, 0, st, a,
-                       p.tok_bits);
-  else if (kernel == 1)
-    hipLaunchKernelGGL((finish_kernel<BF, D, PARTS>), dim3((unsigned)p.tiles), threads, 0, st, a,
+    hipLaunchKernelGGL((list_kernel<BF, D, PARTS>), dim3((unsigned)p.items), threads, 0, st, a);
+  else if (kernel == 1 && a.cap == 128)
+    hipLaunchKernelGGL((finish_kernel<BF, D, PARTS, 8>), dim3((unsigned)p.tiles), threads, 0, st, a,
                        p.tile_bits);
+  else if (kernel == 1)
+    hipLaunchKernelGGL((finish_kernel<BF, D, PARTS, 16>), dim3((unsigned)p.tiles), threads, 0, st,
+                       a, p.tile_bits);
   else
     hipLaunchKernelGGL((dense_kernel<BF, D, PARTS>), dim3((unsigned)p.tiles), threads, 0, st, a,
                        p.tile_bits);
@@ -1142,27 +1395,35 @@ hipError_t launch(const ChunkArgs& a, const ChunkPlan& p, int kernel, hipStream_
 
 }  // namespace
 
-ChunkPlan plan_chunk(const LaunchShape& s, bool q_bf16, int num_tokens) {
+ChunkPlan plan_chunk(const LaunchShape& s, int num_tokens, float alpha) {
   ChunkPlan p;
   const int g_bits = __builtin_ctz(s.group);
-  const int rows = s.bf16 && q_bf16 ? kListRows<true, 128, 1> : kListRows<true, 128, 3>;
+  const int rows = s.bf16 ? kListRows<true> : kListRows<false>;
   p.tok_bits = __builtin_ctz(rows) - g_bits;
   p.tile_bits = 4 - g_bits;
   p.threads = kChunkWaves * kWave;
   p.tiles = ((long long)(num_tokens >> p.tile_bits) + s.batch) * s.num_kv_heads;
-  const long long blocks = ((long long)(num_tokens >> p.tok_bits) + s.batch) * s.num_kv_heads;
-  // four workgroups a CU, parts of at least 256 tokens
-  long long splits = 4 * kNumCUs / blocks;
-  const long long most = ((long long)s.max_pages * s.page_size + 255) / 256;
-  if (splits > most) splits = most;
-  if (splits > kChunkMaxSplits) splits = kChunkMaxSplits;
-  if (splits < 1) splits = 1;
-  p.splits = (int)splits;
-  p.items = blocks * splits;
+  const long long ids = (long long)(num_tokens >> p.tok_bits) + s.batch;
+  const long long total = (long long)s.max_pages * s.page_size;
+  // parts of a row's tokens: about two workgroups a CU where there are fewer
+  // blocks; more parts bring more hits, as each begins without a bound
+  const auto parts_for = [&](long long want, long long blocks, long long least) {
+    const long long n = want / (blocks > 0 ? blocks : 1), most = (total + least - 1) / least;
+    const long long k = n < most ? n : most;
+    return (int)(k < 1 ? 1 : k > kChunkMaxSplits ? kChunkMaxSplits : k);
+  };
+  const long long full = num_tokens >> p.tok_bits;
+  p.splits = parts_for(2 * kNumCUs, (full > 0 ? full : 1) * s.num_kv_heads, 256);
+  // single tokens: eight, and never a long cache by one workgroup
+  p.few_splits = parts_for(8 * kNumCUs, (long long)s.batch * s.num_kv_heads, 512);
+  p.few_items = (long long)s.batch * s.num_kv_heads * p.few_splits;
+  p.items = p.few_items + ids * s.num_kv_heads * p.splits;
   const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  const size_t parts = (size_t)num_tokens * s.num_q_heads * splits;
-  p.counts_off = parts * kCap * 8;
-  p.dense_off = p.counts_off + up(parts * 4);
+  p.few_parts = (size_t)num_tokens * s.num_q_heads * p.splits;
+  const size_t parts = p.few_parts + (size_t)p.few_items * 16;
+  p.cap = cap_of(alpha);
+  p.parts_off = parts * p.cap * 8;
+  p.dense_off = p.parts_off + up(parts * sizeof(Part));
   p.ws_bytes = p.dense_off + up((size_t)p.tiles * 4);
   return p;
 }
@@ -1194,9 +1455,14 @@ hipError_t launch_chunk(const LaunchShape& s, const ChunkPlan& p, int kernel, co
   a.m = (float)(1.0 / ((double)alpha - 1.0));
   a.window = a.m * (1.0f + 4.0e-6f);
   a.whole = a.m == 1.0f || a.m == 2.0f || a.m == 3.0f || a.m == 4.0f ? (int)a.m : 0;
+  a.tok_bits = p.tok_bits;
   a.splits = p.splits;
+  a.few_splits = p.few_splits;
+  a.few_parts = p.few_parts;
+  a.few_items = (unsigned)p.few_items;
+  a.cap = p.cap;
   a.lists = static_cast<uint64_t*>(ws);
-  a.counts = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + p.counts_off);
+  a.parts = reinterpret_cast<Part*>(static_cast<char*>(ws) + p.parts_off);
   a.dense = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + p.dense_off);
   if (!s.bf16) return s.head_dim == 64 ? launch<false, 64, 3>(a, p, kernel, st)
                                        : launch<false, 128, 3>(a, p, kernel, st);

@@ -117,7 +117,7 @@ def _load() -> ctypes.CDLL:
     lib.entmaxkv_append_kv.argtypes = [SP, ctypes.POINTER(Append), *[P] * 14]
     lib.entmaxkv_entmax_chunk.argtypes = [SP, P, I32, I32, P, P, P, P, P, F32, P, P, P, P, SZ, P,
                                           P]
-    lib.entmaxkv_entmax_chunk_ws.argtypes = [SP, I32, ctypes.POINTER(SZ)]
+    lib.entmaxkv_entmax_chunk_ws.argtypes = [SP, I32, F32, ctypes.POINTER(SZ)]
     lib.entmaxkv_workspace_bytes.argtypes = [SP, I32, I32, ctypes.POINTER(SZ)]
     lib.entmaxkv_topk_kernels.argtypes = [SP, I32, ctypes.POINTER(I32)]
     lib.entmaxkv_strerror.argtypes = [ctypes.c_int]
@@ -651,9 +651,9 @@ def _args_append_kv(shape: Shape, q, k, v, positions, slots, q_out, k_pool, v_po
                                     _stream(stream, q.device), None]
 
 
-def entmaxkv_entmax_chunk_ws(shape: Shape, num_tokens: int) -> int:
+def entmaxkv_entmax_chunk_ws(shape: Shape, num_tokens: int, alpha: float) -> int:
     out = ctypes.c_size_t(0)
-    _check(lib.entmaxkv_entmax_chunk_ws(ctypes.byref(shape), _int32(num_tokens),
+    _check(lib.entmaxkv_entmax_chunk_ws(ctypes.byref(shape), _int32(num_tokens), float(alpha),
                                         ctypes.byref(out)), "entmaxkv_entmax_chunk_ws")
     return int(out.value)
 
@@ -677,7 +677,7 @@ def _args_entmax_chunk(shape: Shape, q, token_starts, k_pool, v_pool, block_tabl
     pq = _ptr(q, "q")
     _one_device(q=q, token_starts=token_starts, k_pool=k_pool, v_pool=v_pool,
                 block_table=block_table, seq_lens=seq_lens, out=out, tau=tau, support=support)
-    need = 0 if ws is not None else entmaxkv_entmax_chunk_ws(shape, tokens)
+    need = 0 if ws is not None else entmaxkv_entmax_chunk_ws(shape, tokens, alpha)
     pw, nw, ws = _given_or_new(ws, need, q, stream)
     return lib.entmaxkv_entmax_chunk, [
         ctypes.byref(shape), pq, qd, _int32(tokens), *ptrs, float(alpha), *outs, pw, nw,
