@@ -40,6 +40,7 @@ struct ChunkArgs {
   int32_t* support;  // nullable
   int N, B, H, Hkv, g_bits, ps_bits, max_pages, num_phys;
   float am1, m;  // alpha - 1 and 1 / (alpha - 1)
+  float rooted;  // 2 - alpha = 1 - 1/m
   float window;  // of a score below the row's maximum that may have a weight
   int whole;     // m if it is 1, 2, 3 or 4, else 0
   int tok_bits;  // 2^tok_bits tokens a list block
@@ -153,6 +154,13 @@ __device__ __forceinline__ void powers(const ChunkArgs& a, float u, float& pm, f
   }
 }
 
+// s^(1 - 1/m), of m >= 1
+__device__ __forceinline__ float root_of(const ChunkArgs& a, float s) {
+  return a.whole == 1   ? 1.0f
+         : a.whole == 2 ? __builtin_amdgcn_sqrtf(s)
+                        : __builtin_amdgcn_exp2f(a.rooted * __builtin_amdgcn_logf(s));
+}
+
 // The threshold of one row, by steps from tau = -1 (max x = 0), where the sum
 // s = sum u^m is at least 1. For m >= 1 Newton's steps are those of the convex
 // norm (sum u^m)^(1/m) = 1, nearly straight where the support stays the same:
@@ -169,11 +177,7 @@ struct Threshold {
     const float eps = 6.0e-8f * fmaxf(-t, 1e-3f);
     float next;
     if (a.m >= 1.0f) {
-      const float r = a.whole == 1 ? 1.0f
-                      : a.whole == 2
-                          ? __builtin_sqrtf(s)
-                          : __builtin_amdgcn_exp2f((1.0f - 1.0f / a.m) * __builtin_amdgcn_logf(s));
-      const float d = (s - r) / s1;
+      const float d = (s - root_of(a, s)) * __builtin_amdgcn_rcpf(s1);
       next = t + d;
       done = !(d > eps);  // from below; at or past the root only by rounding
       if (!(next < 0.0f)) next = 0.5f * (t + hi);
@@ -237,7 +241,7 @@ __device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, in
       const bool page_ok = (!BF || c < 2 ? pg.p0 : pg.p1) >= 0;
 #pragma unroll
       for (int i = 0; i < NZ; ++i)
-        z[i] = page_ok & (t0 + tile_token<BF>(c, i) < hi) ? z[i] : -INFINITY;
+        z[i] = (page_ok & (t0 + tile_token<BF>(c, i) < hi)) ? z[i] : -INFINITY;
       f(t0, pg, z);
     }
   };
@@ -464,12 +468,12 @@ struct Track {
 };
 
 // Prunes one row's list to the tokens above the threshold of what it holds: 16
-// lanes a row, up to 128 entries in their registers, more read again for every
+// lanes a row, up to 64 entries in their registers, more read again for every
 // step. Returns that threshold (entries are kept from `slack` below it); n: its
 // length, before and after.
 __device__ __forceinline__ float prune16(const ChunkArgs& a, uint64_t* list, int lane, float mx,
                                          float slack, int& n) {
-  constexpr int kRegs = 8;
+  constexpr int kRegs = 4;
   const int sub = lane & 15;
   uint64_t e[kRegs];
 #pragma unroll
@@ -551,6 +555,10 @@ __device__ __forceinline__ float max_of(const float (&z)[N]) {
   return m;
 }
 
+__device__ __forceinline__ float max_of4(const f32x4& x) {
+  return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+}
+
 // The length to hand on.
 __device__ __forceinline__ int length_of(const Track& tr) {
   return tr.mx < INFINITY ? tr.n : kNoNumber;  // (NaN too)
@@ -608,34 +616,83 @@ __device__ __forceinline__ void load_nearest(QFrag<true, D, 1>& q, const char* r
   off = group_sum(off);
 }
 
-// Scores of a K tile and NT row tiles: all of them take a step before any
-// takes the next, so that no matrix instruction waits for the one before it.
-template <bool BF, int D, int PARTS, int NT>
-__device__ __forceinline__ void tile_scores(const KTile<BF, D>& kt, const QFrag<BF, D, PARTS> (&q)[NT],
-                                            float (&z)[NT][scores_per_lane<BF>()]) {
-  if constexpr (BF) {
-    f32x4 acc[NT][2];
+// Half the dimensions of a staged K tile (the operands of KTile), and their part
+// of the scores of NT row tiles: all of them take a step before any takes the
+// next, so that no matrix instruction waits for the one before it. Halves, as one
+// is read while the other is used, and only one is held from tile to tile: with
+// whole tiles the registers overflowed.
+template <bool BF, int D, int NT>
+struct KHalf;
+
+template <int D, int NT>
+struct KHalf<true, D, NT> {
+  static constexpr int kSteps = D / 64;
+  typedef f32x4 Acc[NT][2];
+  u32x4 f[2][kSteps];
+  __device__ __forceinline__ void read(lds_at st, int tile, int lane, int h) {
+    typedef Stage<true, D> St;
+    const int m = lane & 15, c = lane >> 4;
+    const lds_at r = st + St::at(((m >> 2) << 3) + (m & 3), c);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = f32x4{0, 0, 0, 0};
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        f[u][s] = lds_read<u32x4>(St::on(r, 4 * (s + h * kSteps)) + tile * (St::kBytes / 2) +
+                                  u * 4 * St::kRow);
+  }
+  template <int PARTS>
+  __device__ __forceinline__ void add(const QFrag<true, D, PARTS> (&q)[NT], int h, Acc& acc) const {
 #pragma unroll
     for (int k = PARTS - 1; k >= 0; --k)
 #pragma unroll
-      for (int s = 0; s < D / 32; ++s)
+      for (int s = 0; s < kSteps; ++s)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                as_bf(kt.f[u][s]), as_bf(q[t].f[k][s]), acc[t][u], 0, 0, 0);
+                as_bf(f[u][s]), as_bf(q[t].f[k][s + h * kSteps]), acc[t][u], 0, 0, 0);
+  }
+  __device__ __forceinline__ static void scores(const Acc& acc, float (&z)[NT][8]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[t][i] = acc[t][i / 4][i % 4];
-  } else {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) kt.template scores<PARTS>(q[t], z[t]);
   }
-}
+};
+
+template <int D, int NT>
+struct KHalf<false, D, NT> {
+  static constexpr int kSteps = D / 32;
+  typedef f32x4 Acc[NT][4];  // four sums each, as KTile's
+  f32x4 f[kSteps];
+  __device__ __forceinline__ void read(lds_at st, int tile, int lane, int h) {
+    typedef Stage<false, D> St;
+    const lds_at r = st + St::at(lane & 15, lane >> 4);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      f[s] = lds_read<f32x4>(St::on(r, 4 * (s + h * kSteps)) + tile * (St::kBytes / 2));
+  }
+  template <int PARTS>
+  __device__ __forceinline__ void add(const QFrag<false, D, PARTS> (&q)[NT], int h,
+                                      Acc& acc) const {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[t][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[s][e], q[t].f[s + h * kSteps][e],
+                                                           acc[t][e], 0, 0, 0);
+  }
+  __device__ __forceinline__ static void scores(const Acc& acc, float (&z)[NT][4]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        z[t][i] = (acc[t][0][i] + acc[t][1][i]) + (acc[t][2][i] + acc[t][3][i]);
+  }
+};
 
 constexpr int kFewCap = 96;  // of a wave's list in LDS
 
@@ -649,7 +706,8 @@ template <int NZ>
 struct WaveRows {
   f32x4 z[NZ / 4][kQueue];
   int code[kQueue];       // row << 24 | the lane's first token
-  float mx[64], thr[64];  // thr: what a score has to pass, but for `off`
+  f32x4 top[64];          // the largest scores of four classes of a row's tokens
+  float thr[64];          // what a score has to pass, but for `off`
   int n[64], limit[64];   // limit: entries from which a list is pruned
   float off[64];          // of the row's scores, by the largest |key|
 };
@@ -688,7 +746,8 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
     // the new maxima first: they bound these very hits
     const float top = max_of(z);
     if (real && top < INFINITY)
-      __hip_atomic_fetch_max(&w.mx[row], top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+      __hip_atomic_fetch_max(reinterpret_cast<float*>(&w.top[row]) + (tok / NZ & 3), top,
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
     if (real && !(top < INFINITY)) w.n[row] = kNoNumber;
     // lanes of the same row
     uint64_t same = ~0ull;
@@ -702,7 +761,8 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
     for (;;) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       const int n = w.n[row];
-      const float thr = fmaxf(w.thr[row], w.mx[row] - a.window) - 2.0f * kmax * w.off[row];
+      const float thr =
+          fmaxf(w.thr[row], max_of4(w.top[row]) - a.window) - 2.0f * kmax * w.off[row];
       unsigned bits = 0;
 #pragma unroll
       for (int i = 0; i < NZ; ++i) bits |= (z[i] > thr ? 1u : 0u) << i;
@@ -733,7 +793,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
       int kept = max(w.n[row4], 0);
       const bool any = kept > 0;
-      const float bound = prune16(a, at(row4), lane, w.mx[row4],
+      const float bound = prune16(a, at(row4), lane, max_of4(w.top[row4]),
                                   2.0f * kmax * w.off[row4], kept);
       if ((lane & 15) == 0 && any) {
         const bool no_room = kept > a.cap - NZ;
@@ -745,8 +805,30 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
     }
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  // (a row without a list takes no more hits)
-  w.thr[lane] = w.n[lane] < 0 ? INFINITY : fmaxf(w.thr[lane], w.mx[lane] - a.window);
+  // A row's new bound, a row a lane: the threshold of the classes' four largest
+  // scores alone, tokens like any others. It is nearly that of all tokens (the
+  // largest ones lie apart; 32K tokens of spread 2.5 at alpha 1.5: 50 hits a row,
+  // 43 by the exact threshold, 82 by the maximum alone). A few Newton steps from
+  // below: stopped early, it bounds less.
+  const f32x4 x = w.top[lane];
+  const float mx = max_of4(x);
+  float t = -1.0f;
+  if (a.m >= 1.0f) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      float sum = 0.0f, sum1 = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float pm, pm1;
+        powers(a, fmaxf((x[e] - mx) * a.am1 - t, 0.0f), pm, pm1);
+        sum += pm;
+        sum1 += pm1;
+      }
+      t += fmaxf((sum - root_of(a, sum)) * __builtin_amdgcn_rcpf(sum1), 0.0f);
+    }
+  }
+  // (a row without a list takes no more hits; one without a score keeps its bound)
+  w.thr[lane] = w.n[lane] < 0 ? INFINITY : fmaxf(w.thr[lane], bound_of(a, mx, t));
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
@@ -778,22 +860,22 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
   auto& mine = sh.rows[wave];
   mine.n[lane] = 0;
   mine.limit[lane] = a.cap * 3 / 4;
-  mine.mx[lane] = mine.thr[lane] = -INFINITY;
-  int hi[NT], queued = 0;
-  QFrag<BF, D, QP> q[NT];
-  float thr[NT], off[NT], kmax = 0.0f;
+  mine.thr[lane] = -INFINITY;
+  mine.top[lane] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   mine.off[lane] = 0.0f;
+  int queued = 0;
+  QFrag<BF, D, QP> q[NT];
+  float thr[NT], kmax = 0.0f;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     thr[t] = -INFINITY;
-    off[t] = 0.0f;
     const bool live = t * 16 + rl < wrows;
-    hi[t] = live ? seen(a, w, wr + t * 16 + rl) : 0;
     const char* row =
         live ? static_cast<const char*>(a.q) + row_at(a, w, wr + t * 16 + rl) * (D * QB) : nullptr;
     if constexpr (kNear) {
-      load_nearest<D>(q[t], row, c, off[t]);
-      if (c == 0) mine.off[t * 16 + rl] = off[t];
+      float off;
+      load_nearest<D>(q[t], row, c, off);
+      if (c == 0) mine.off[t * 16 + rl] = off;
     } else {
       q[t].load(row, c);
     }
@@ -801,9 +883,6 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
   // tokens below `some` are seen by a row of this wave, below `every` by all
   const int some = wrows ? seen(a, w, wr + wrows - 1) : 0;
   const int every = wrows == NT * 16 ? seen(a, w, wr) : 0;
-  auto list = [&](int row) {  // (a row past the last has no hits: any address serves)
-    return a.lists + (row_at(a, w, min(wr + row, w.rows - 1)) * a.splits + split) * a.cap;
-  };
 
   int to[kLoads];  // where this lane's 16 bytes go
 #pragma unroll
@@ -812,24 +891,25 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
     const int r = at / St::kRow, ch = at % St::kRow / 16;
     to[i] = (wave * kQuarter + r) * St::kRow + ((ch ^ St::swizzle(wave * kQuarter + r)) << 4);
   }
-  // the next 64 stages, one a lane: the page of this wave's quarter, and which
-  // quarters lie in pages of the pool
+  // the next 64 stages, one a lane: the page of this wave's quarter, and whether
+  // all quarters lie in pages of the pool
   int base = v0, pg = -1;
-  uint64_t ok[kChunkWaves];
+  uint64_t valid = 0;
   auto look = [&](int v) {
     base = v;
+    valid = ~0ull;
 #pragma unroll
     for (int k = 0; k < kChunkWaves; ++k) {
       int p = -1;
       if (v + lane < v1)
         p = page_at(a, x.table, x.npages, ((v + lane) * ST + k * kQuarter) >> a.ps_bits);
-      ok[k] = __ballot(p >= 0);
+      valid &= __ballot(p >= 0);
       if (k == wave) pg = p;
     }
   };
-  // A stage goes through registers: asked for a stage ahead, put into LDS half
-  // a stage later. (Direct loads into LDS have the compiler wait for all of them
-  // at the next LDS read.)
+  // A stage goes through registers: asked for at the end of the stage two before
+  // it, put into LDS at the end of the one before. (Direct loads into LDS have the
+  // compiler wait for all of them at the next LDS read.)
   u32x4 raw[kLoads];
   auto ask = [&](int v) {
     const int p = __builtin_amdgcn_readlane(pg, v - base);
@@ -846,8 +926,8 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
     if constexpr (kNear) {
       // the largest |key| of this quarter's tokens that some row sees; one that is
       // no finite number gives scores that are none, and needs no room
-      const bool valid_page = ok[wave] >> (v - base) & 1;
-      const int left = valid_page ? top - v * ST - wave * kQuarter : 0;  // tokens seen
+      const int p = __builtin_amdgcn_readlane(pg, v - base);
+      const int left = p >= 0 ? top - v * ST - wave * kQuarter : 0;  // tokens seen
       u16x2 big = {0, 0};
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
@@ -875,120 +955,141 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
   // thr: the rows' bounds less what the scores may be off
   auto refresh = [&] {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) thr[t] = mine.thr[t * 16 + rl] - 2.0f * kmax * off[t];
+    for (int t = 0; t < NT; ++t) {
+      thr[t] = mine.thr[t * 16 + rl];
+      if constexpr (kNear) thr[t] -= 2.0f * kmax * mine.off[t * 16 + rl];
+    }
   };
 
   if (v0 < v1) {
     look(v0);
     ask(v0);
     put(v0);
+    if (v0 + 1 < v1) ask(v0 + 1);
   }
   wait_vmcnt<0>();  // (the queries too: or the compiler waits for them in the loop)
   __syncthreads();
-  // Tiles in turn, two a stage. A tile's keys are read from LDS while the one
-  // before it is looked through; so the barrier that a stage's keys wait for
-  // lies in the middle of the stage before.
-  int when = v0;  // the stage after which the queues are emptied next
-  KTile<BF, D> kt;
-  if (v0 < v1) kt.read(lds_addr(sh.st[v0 & 1]), 0, lane);
-  unsigned valid = 0;
-  for (int u = 2 * v0; u < 2 * v1; ++u) {
-    const int v = u >> 1, sub = u & 1, t0 = u * TT;
-    if (sub == 0) {
-      valid = 0;  // quarters of this stage (the next may be looked up below)
-#pragma unroll
-      for (int k = 0; k < kChunkWaves; ++k) valid |= (unsigned)(ok[k] >> (v - base) & 1) << k;
-      if (v + 1 < v1) {
-        if (v + 1 - base == kWave) look(v + 1);
-        ask(v + 1);
-      }
-      if constexpr (kNear) {
-        const f32x4 k = *reinterpret_cast<const f32x4*>(sh.kmax[v & 1]);
-        const float m = fmaxf(fmaxf(k[0], k[1]), fmaxf(k[2], k[3]));
-        if (m > kmax) {
-          kmax = m;
-          refresh();
+  // Tiles in turn, two a stage. The first half of a tile's keys is read from LDS
+  // while the tile before it is looked through, the second half while the first
+  // is used. One turn more empties the queue.
+  int when = v0 + 1;  // the stage at which the queues are emptied next
+  bool pages = true, pages_next = valid & 1;  // the stage lies in pages of the pool
+  typedef KHalf<BF, D, NT> Half;
+  Half k0;
+  if (v0 < v1) k0.read(lds_addr(sh.st[0]), 2 * v0 & 3, lane, 0);
+  for (int u = 2 * v0; u <= 2 * v1; ++u) {
+    const int v = u >> 1, t0 = u * TT;
+    const bool first = (u & 1) == 0;
+    float z[NT][NZ];
+    uint64_t lanes[NT], any = 0;  // lanes that have hits
+    if (u < 2 * v1) {
+      if (first) {
+        pages = pages_next;
+        if constexpr (kNear) {
+          const f32x4 k = *reinterpret_cast<const f32x4*>(sh.kmax[v & 1]);
+          const float m = max_of4(k);
+          if (m > kmax) {
+            kmax = m;
+            refresh();
+          }
         }
       }
-    }
-    float z[NT][NZ];
-    __builtin_amdgcn_s_setprio(1);
-    tile_scores<BF, D, QP, NT>(kt, q, z);
-    __builtin_amdgcn_s_setprio(0);
-    if (sub == 0) {
-      kt.read(lds_addr(sh.st[v & 1]), 1, lane);
-      if (v + 1 < v1) put(v + 1);
-      __syncthreads();
-    } else {
-      kt.read(lds_addr(sh.st[(v + 1) & 1]), 0, lane);  // (past the last: not used)
-    }
-    uint64_t lanes[NT], any = 0;  // lanes that have hits
-    if (t0 < some) {
-      if (__builtin_expect(valid != (1u << kChunkWaves) - 1 || t0 + TT > every, 0)) {
-        const bool page_ok = valid >> (2 * sub + (c >> 1)) & 1;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < NZ; ++i)
-            z[t][i] = page_ok & (t0 + tile_token<BF>(c, i) < hi[t]) ? z[t][i] : -INFINITY;
+      {
+        Half k1;
+        k1.read(lds_addr(sh.st[0]), u & 3, lane, 1);
+        typename Half::Acc acc = {};
+        __builtin_amdgcn_s_setprio(1);
+        k0.template add<QP>(q, 0, acc);
+        k1.template add<QP>(q, 1, acc);
+        __builtin_amdgcn_s_setprio(0);
+        Half::scores(acc, z);
       }
-      float tmax[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) tmax[t] = max_of(z[t]);
-      // until the bounds have settled, a tile's own maximum goes first
-      if (__builtin_expect(v < v0 + kYoung, 0)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          thr[t] = fmaxf(thr[t], max_across(tmax[t]) - a.window - 2.0f * kmax * off[t]);
+      if (!first) {
+        // the other stage's keys, in place of those that every wave has read
+        // before the last barrier
+        if (v + 1 < v1) put(v + 1);
+        pages_next = valid >> (v + 1 - base & 63) & 1;
+        if (v + 2 < v1) {
+          if (v + 2 - base == kWave) look(v + 2);
+          ask(v + 2);
+        }
+        __syncthreads();
       }
+      k0.read(lds_addr(sh.st[0]), (u + 1) & 3, lane, 0);  // (past the last: not used)
+      if (t0 < some) {
+        if (__builtin_expect(!pages || t0 + TT > every, 0)) {
+          bool page_ok = true;
+          if (!pages)
+            page_ok = page_at(a, x.table, x.npages,
+                              (t0 + tile_token<BF>(c, 0)) >> a.ps_bits) >= 0;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        lanes[t] = __ballot(!(tmax[t] <= thr[t]));
-        any |= lanes[t];
+          for (int t = 0; t < NT; ++t) {
+            const int r = t * 16 + rl, hi = r < wrows && page_ok ? seen(a, w, wr + r) : 0;
+#pragma unroll
+            for (int i = 0; i < NZ; ++i)
+              z[t][i] = t0 + tile_token<BF>(c, i) < hi ? z[t][i] : -INFINITY;
+          }
+        }
+        float tmax[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) tmax[t] = max_of(z[t]);
+        // until the bounds have settled, a tile's own maximum goes first
+        if (__builtin_expect(v < v0 + kYoung, 0)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float m = max_across(tmax[t]) - a.window;
+            if constexpr (kNear) m -= 2.0f * kmax * mine.off[t * 16 + rl];
+            thr[t] = fmaxf(thr[t], m);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          lanes[t] = __ballot(!(tmax[t] <= thr[t]));
+          any |= lanes[t];
+        }
       }
     }
     // The queues are emptied by all waves together, about when they hold a batch
     // (a row's hits become rarer as 1 / tokens): a wave that does so by itself
-    // has the others wait at the next barrier.
-    const bool due = sub == 1 && (v >= when || v + 1 == v1);
-    if (any == 0 && !due) continue;
+    // has the others wait at the next barrier. Before this tile's hits go in.
     int total = 0;
     if (any) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) total += __popcll(lanes[t]);
     }
-    for (;;) {
-      const bool room = queued + total <= kQueue;
-      if (room && any) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (lanes[t] == 0) continue;
-          const int at = __builtin_amdgcn_mbcnt_hi(
-              (unsigned)(lanes[t] >> 32),
-              __builtin_amdgcn_mbcnt_lo((unsigned)lanes[t], (unsigned)queued));
-          if (__builtin_amdgcn_inverse_ballot_w64(lanes[t])) {
-#pragma unroll
-            for (int i = 0; i < NZ / 4; ++i)
-              mine.z[i][at] = f32x4{z[t][4 * i], z[t][4 * i + 1], z[t][4 * i + 2],
-                                    z[t][4 * i + 3]};
-            mine.code[at] = ((t * 16 + rl) << 24) + t0 + tile_token<BF>(c, 0);
-          }
-          queued += __popcll(lanes[t]);
-        }
-      }
-      if (room && !due) break;
-      flush<NZ>(a, mine, queued, lane, kmax, list);
+    const bool due = first && v >= when;
+    if (due) when = v + 1 + ((v - v0) >> 3);
+    if (queued > 0 && (due || u == 2 * v1 || queued + total > kQueue)) {
+      // (the arguments once more: they would fill the loop's scalar registers)
+      auto kernarg = __builtin_amdgcn_kernarg_segment_ptr();
+      asm volatile("" : "+s"(kernarg));
+      const ChunkArgs b = *(const ChunkArgs*)kernarg;
+      flush<NZ>(b, mine, queued, lane, kmax, [&](int row) {
+        // (a row past the last has no hits: any address serves)
+        return b.lists + (row_at(b, w, min(wr + row, w.rows - 1)) * b.splits + split) * b.cap;
+      });
       queued = 0;
       refresh();
-      if (room) {
-        when = v + 1 + ((v - v0) >> 3);
-        break;
+    }
+    if (any == 0) continue;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (lanes[t] == 0) continue;
+      const int at = __builtin_amdgcn_mbcnt_hi(
+          (unsigned)(lanes[t] >> 32),
+          __builtin_amdgcn_mbcnt_lo((unsigned)lanes[t], (unsigned)queued));
+      if (__builtin_amdgcn_inverse_ballot_w64(lanes[t])) {
+#pragma unroll
+        for (int i = 0; i < NZ / 4; ++i)
+          mine.z[i][at] = f32x4{z[t][4 * i], z[t][4 * i + 1], z[t][4 * i + 2], z[t][4 * i + 3]};
+        mine.code[at] = ((t * 16 + rl) << 24) + t0 + tile_token<BF>(c, 0);
       }
+      queued += __popcll(lanes[t]);
     }
   }
   if (lane < wrows)
     a.parts[row_at(a, w, wr + lane) * a.splits + split] =
-        Part{mine.n[lane], mine.mx[lane], 2.0f * kmax * mine.off[lane], 0};
+        Part{mine.n[lane], max_of4(mine.top[lane]), 2.0f * kmax * mine.off[lane], 0};
 }
 
 // At most 16 rows (single tokens): the waves share them and take turns at the
@@ -1043,7 +1144,7 @@ __device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int 
         const bool page_ok = (!BF || c < 2 ? now.p0 : now.p1) >= 0;
 #pragma unroll
         for (int i = 0; i < NZ; ++i)
-          z[i] = page_ok & (t0 + tile_token<BF>(c, i) < hi) ? z[i] : -INFINITY;
+          z[i] = (page_ok & (t0 + tile_token<BF>(c, i) < hi)) ? z[i] : -INFINITY;
       }
       const float tmax = max_of(z);
       if (__any(!(tmax <= tr.thr))) {
@@ -1453,6 +1554,7 @@ hipError_t launch_chunk(const LaunchShape& s, const ChunkPlan& p, int kernel, co
   a.num_phys = s.num_phys;
   a.am1 = (float)((double)alpha - 1.0);
   a.m = (float)(1.0 / ((double)alpha - 1.0));
+  a.rooted = (float)(2.0 - (double)alpha);
   a.window = a.m * (1.0f + 4.0e-6f);
   a.whole = a.m == 1.0f || a.m == 2.0f || a.m == 3.0f || a.m == 4.0f ? (int)a.m : 0;
   a.tok_bits = p.tok_bits;
