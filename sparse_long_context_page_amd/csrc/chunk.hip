@@ -467,37 +467,43 @@ struct Track {
   int n = 0;
 };
 
-// Prunes one row's list to the tokens above the threshold of what it holds: 16
-// lanes a row, up to 64 entries in their registers, more read again for every
-// step. Returns that threshold (entries are kept from `slack` below it); n: its
-// length, before and after.
-__device__ __forceinline__ float prune16(const ChunkArgs& a, uint64_t* list, int lane, float mx,
-                                         float slack, int& n) {
-  constexpr int kRegs = 4;
+// Keeps the entries of one row's list above thr, in order: 16 lanes a row, four
+// groups of 16 entries on their way.
+__device__ __forceinline__ int filter16(uint64_t* list, int lane, int n, float thr) {
+  constexpr int U = 4;
   const int sub = lane & 15;
-  uint64_t e[kRegs];
-#pragma unroll
-  for (int i = 0; i < kRegs; ++i)
-    e[i] = i * 16 + sub < n ? list[i * 16 + sub] : entry(-INFINITY, 0);
-  const float t = solve16(a, mx, n > 0, [&](auto f) {
-#pragma unroll
-    for (int i = 0; i < kRegs; ++i) f(entry_z(e[i]));
-    for (int i = kRegs * 16 + sub; i < n; i += 16) f(entry_z(list[i]));
-  });
-  const float thr = bound_of(a, mx, t);
   int kept = 0;
-  auto keep_of = [&](uint64_t x, bool real) {
-    const bool keep = real && !(entry_z(x) <= thr - slack);
-    const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
-    if (keep) list[kept + __popc(all & ((1u << sub) - 1))] = x;
-    kept += __popc(all);
-  };
+  for (int i = 0; i < n; i += U * 16) {
+    uint64_t e[U];
 #pragma unroll
-  for (int i = 0; i < kRegs; ++i) keep_of(e[i], i * 16 + sub < n);
-  for (int i = kRegs * 16; i < n; i += 16)  // (entries move forward only)
-    keep_of(i + sub < n ? list[i + sub] : 0, i + sub < n);
-  n = kept;
-  return thr;
+    for (int u = 0; u < U; ++u) e[u] = i + u * 16 + sub < n ? list[i + u * 16 + sub] : 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {  // (entries move forward only)
+      const bool keep = i + u * 16 + sub < n && !(entry_z(e[u]) <= thr);
+      const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
+      if (keep) list[kept + __popc(all & ((1u << sub) - 1))] = e[u];
+      kept += __popc(all);
+    }
+  }
+  return kept;
+}
+
+// Prunes one row's list to the tokens above `bound`, or, where more than `few`
+// are left, above the threshold of what it holds, which is the next bound; from
+// `slack` below it. n: its length, before and after.
+__device__ __forceinline__ float prune16(const ChunkArgs& a, uint64_t* list, int lane, float mx,
+                                         float bound, float slack, int few, int& n) {
+  const int sub = lane & 15;
+  n = filter16(list, lane, n, bound - slack);
+  if (!__any(n > few)) return bound;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+  const float t = solve16(a, mx, n > few, [&](auto f) {
+    if (n <= few) return;
+    for (int i = sub; i < n; i += 16) f(entry_z(list[i]));
+  });
+  if (n > few) bound = fmaxf(bound, bound_of(a, mx, t));
+  n = filter16(list, lane, n, bound - slack);
+  return bound;
 }
 
 // The lists of the 16 rows of a tile, 4 rows at a time. at(row): its list.
@@ -508,7 +514,8 @@ __device__ __forceinline__ void prune(const ChunkArgs& a, Track& tr, int room, i
   for (int k = 0; k < 4; ++k) {
     const int row = k * 4 + (lane >> 4);
     int kept = max(__shfl(tr.n, row, kWave), 0);
-    const float thr = prune16(a, at(row), lane, __shfl(tr.mx, row, kWave), 0.0f, kept);
+    const float thr = prune16(a, at(row), lane, __shfl(tr.mx, row, kWave),
+                              __shfl(tr.thr, row, kWave), 0.0f, room / 2, kept);
     // back to the lanes that hold these rows' scores
     const int from = ((lane & 3) << 4), mine = (lane & 15) >> 2;
     const int kn = __shfl(kept, from, kWave);
@@ -580,7 +587,7 @@ __device__ __forceinline__ Cache cache_of(const ChunkArgs& a, const Rows& w, int
   return x;
 }
 
-constexpr int kYoung = 4;  // stages
+constexpr int kYoung = 2;  // stages
 
 // Row tiles a wave holds: with a bf16 cache 64 rows share each K operand read from
 // LDS; float32 rows take the registers of more.
@@ -708,7 +715,7 @@ struct WaveRows {
   int code[kQueue];       // row << 24 | the lane's first token
   f32x4 top[64];          // the largest scores of four classes of a row's tokens
   float thr[64];          // what a score has to pass, but for `off`
-  int n[64], limit[64];   // limit: entries from which a list is pruned
+  int n[64];
   float off[64];          // of the row's scores, by the largest |key|
 };
 
@@ -757,7 +764,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       const uint64_t set = __ballot(bit);
       same &= bit ? set : ~set;
     }
-    bool pending = real, grown = false;
+    bool pending = real;
     for (;;) {
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       const int n = w.n[row];
@@ -783,9 +790,8 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       const uint64_t done = __ballot(fits) & same;
       if (fits && done >> lane == 1) w.n[row] = to + c;  // the last of the row
       pending = pending && !fits;
-      grown = grown || fits;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      const uint64_t long_ones = __ballot(pending || (grown && w.n[row] > w.limit[row]));
+      const uint64_t long_ones = __ballot(pending);
       if (long_ones == 0) break;
       // prune that row's list and its neighbours', 4 rows at a time
       const int r = __builtin_amdgcn_readlane(row, __builtin_ctzll(long_ones));
@@ -793,13 +799,14 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
       int kept = max(w.n[row4], 0);
       const bool any = kept > 0;
-      const float bound = prune16(a, at(row4), lane, max_of4(w.top[row4]),
-                                  2.0f * kmax * w.off[row4], kept);
+      const f32x4 tops = w.top[row4];
+      const float bound =
+          prune16(a, at(row4), lane, max_of4(tops), fmaxf(w.thr[row4], max_of4(tops) - a.window),
+                  2.0f * kmax * w.off[row4], a.cap / 2, kept);
       if ((lane & 15) == 0 && any) {
         const bool no_room = kept > a.cap - NZ;
         w.n[row4] = no_room ? kLong : kept;
         w.thr[row4] = fmaxf(w.thr[row4], bound);
-        w.limit[row4] = min(a.cap, max(a.cap * 3 / 4, kept + a.cap / 4));
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     }
@@ -815,7 +822,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
   float t = -1.0f;
   if (a.m >= 1.0f) {
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float sum = 0.0f, sum1 = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -859,7 +866,6 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
 
   auto& mine = sh.rows[wave];
   mine.n[lane] = 0;
-  mine.limit[lane] = a.cap * 3 / 4;
   mine.thr[lane] = -INFINITY;
   mine.top[lane] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   mine.off[lane] = 0.0f;
