@@ -313,11 +313,20 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
   }
 }
 
+// Tokens of a workgroup: one, so that few tokens still fill the chip, up to
+// kAppendFew; four beyond, which share the angles' work (32/8 heads of 128 dims,
+// one against four, us: 64 tokens 4.5 : 8.8, 1024 7.5 : 11.6, 4096 23.3 : 24.7,
+// 8192 40.4 : 36.8).
+constexpr int kAppendFew = 4096;
+
 template <bool XBF, bool QBF, bool KVBF, int D>
 hipError_t launch_append_t(const AppendArgs& a, hipStream_t st) {
-  constexpr int TW = 4;
-  hipLaunchKernelGGL((append_kernel<XBF, QBF, KVBF, D, TW>), dim3((unsigned)((a.n + TW - 1) / TW)),
-                     dim3(kAppendThreads), 0, st, a);
+  if (a.n <= kAppendFew)
+    hipLaunchKernelGGL((append_kernel<XBF, QBF, KVBF, D, 1>), dim3((unsigned)a.n),
+                       dim3(kAppendThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((append_kernel<XBF, QBF, KVBF, D, 4>), dim3((unsigned)((a.n + 3) / 4)),
+                       dim3(kAppendThreads), 0, st, a);
   return hipGetLastError();
 }
 

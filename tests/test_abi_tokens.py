@@ -118,3 +118,59 @@ def test_plan_binding_refusals(ek):
                   (dict(seq_lens=z((2, 2))[:, 0]), ValueError), (dict(), ValueError)]:
         with pytest.raises(e):
             ek.entmaxkv_plan_tokens(small(ek), **{**good, **kw})
+
+
+def chunk(ek, s, q=D, qd=1, n=64, starts=D, k=D, v=D, bt=D, lens=D, alpha=1.5, out=E, ws=D,
+          nws=1 << 40):
+    return ek.lib.entmaxkv_entmax_chunk(ctypes.byref(s), q, qd, n, starts, k, v, bt, lens, alpha,
+                                        out, None, None, ws, nws, None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=0), INVALID), (dict(n=-3), INVALID), (dict(n=1 << 24), UNSUPPORTED),
+    (dict(alpha=1.0), INVALID), (dict(alpha=0.5), INVALID), (dict(alpha=float("nan")), INVALID),
+    (dict(alpha=float("inf")), INVALID), (dict(qd=2), UNSUPPORTED), (dict(q=None), INVALID),
+    (dict(starts=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
+    (dict(bt=None), INVALID), (dict(lens=None), INVALID), (dict(out=None), INVALID),
+    (dict(q=BAD), INVALID), (dict(k=BAD), INVALID), (dict(v=BAD), INVALID), (dict(out=BAD), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(nws=256), WORKSPACE), (dict(ws=ctypes.c_void_p(16)), INVALID),
+])
+def test_chunk_refusals(ek, kw, code):
+    assert chunk(ek, shape(ek), **kw) == code
+
+
+def test_chunk_types_and_sizes(ek):
+    assert chunk(ek, shape(ek, kv_dtype="f32")) == UNSUPPORTED  # bf16 queries, float32 cache
+    assert chunk(ek, shape(ek, head_dim=96)) == UNSUPPORTED
+    # more workgroups than a launch holds
+    one = dict(num_q_heads=1, num_kv_heads=1, batch=1 << 24)
+    assert chunk(ek, shape(ek, **one), n=(1 << 24) - 1) == UNSUPPORTED
+    out = ctypes.c_size_t(0)
+    ws = ek.lib.entmaxkv_entmax_chunk_ws
+    assert ws(ctypes.byref(shape(ek)), 64, 1.5, None) == INVALID
+    assert ws(ctypes.byref(shape(ek)), 0, 1.5, ctypes.byref(out)) == INVALID
+    assert ws(ctypes.byref(shape(ek)), 64, 1.0, ctypes.byref(out)) == INVALID
+    # flat weights take longer lists
+    assert ek.entmaxkv_entmax_chunk_ws(shape(ek), 64, 1.25) > ek.entmaxkv_entmax_chunk_ws(
+        shape(ek), 64, 1.5) > 0
+
+
+def test_chunk_binding_refusals(ek):
+    bf, i32 = torch.bfloat16, torch.int32
+    good = dict(q=torch.zeros(5, 4, 64, dtype=bf), token_starts=torch.zeros(3, dtype=i32),
+                k_pool=torch.zeros(9, 2, 16, 64, dtype=bf),
+                v_pool=torch.zeros(9, 2, 16, 64, dtype=bf), block_table=torch.zeros(2, 3, dtype=i32),
+                seq_lens=torch.zeros(2, dtype=i32), alpha=1.5, out=torch.zeros(5, 4, 64, dtype=bf))
+    for kw, e in [(dict(q=torch.zeros(5, 2, 64, dtype=bf)), ValueError),
+                  (dict(q=torch.zeros(5, 4 * 64, dtype=bf)), ValueError),
+                  (dict(q=torch.zeros(5, 4, 128, dtype=bf)[..., :64]), ValueError),
+                  (dict(q=torch.zeros(5, 4, 64, dtype=torch.float16)), TypeError),
+                  (dict(token_starts=torch.zeros(2, dtype=i32)), ValueError),
+                  (dict(out=torch.zeros(5, 4, 64)), TypeError),
+                  (dict(out=torch.zeros(4, 4, 64, dtype=bf)), ValueError),
+                  (dict(tau=torch.zeros(5, 3)), ValueError),
+                  (dict(support=torch.zeros(5, 4)), TypeError),
+                  (dict(k_pool=torch.zeros(8, 2, 16, 64, dtype=bf)), ValueError),
+                  (dict(seq_lens=torch.zeros(1, dtype=i32)), ValueError), (dict(), ValueError)]:
+        with pytest.raises(e):
+            ek.entmaxkv_entmax_chunk(small(ek), **{**good, **kw})
