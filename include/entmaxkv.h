@@ -595,8 +595,10 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
  * entmaxkv_softmax_window; weights are used in float32 or to 2^-17 of
  * themselves (bf16 queries). Results do not depend on what else runs (no
  * atomics on results).
- * Workspace: entmaxkv_entmax_chunk_ws bytes. Kernels launched: 3 (lists of the tokens that may have a weight; tau
- * and the output; rows whose support is too long for a list).
+ * Workspace: entmaxkv_entmax_chunk_ws bytes. Kernels launched: 3 (lists of the
+ * tokens that may have a weight; tau and the output; rows whose support is too
+ * long for a list), or 2 for few tokens, the last within the second (events'
+ * pair 2 then encloses nothing).
  */
 int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
                           int32_t num_tokens, const int32_t* token_starts, const void* k_pool,

@@ -897,9 +897,10 @@ int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_
   if (!ws || ws_bytes < p.ws_bytes) return ENTMAXKV_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return ENTMAXKV_ERR_INVALID;
   const Events ev{events, stream};
-  for (int i = 0; i < kChunkKernels; ++i) {
+  for (int i = 0; i < 3; ++i) {
     if (!ev.before(i)) return ENTMAXKV_ERR_HIP;
-    if (launch_chunk(s, p, i, q, q_dtype == ENTMAXKV_BF16, num_tokens, token_starts, k_pool, v_pool,
+    if (i < p.kernels &&
+        launch_chunk(s, p, i, q, q_dtype == ENTMAXKV_BF16, num_tokens, token_starts, k_pool, v_pool,
                      block_table, seq_lens, alpha, out, tau, support, ws, stream) != hipSuccess)
       return ENTMAXKV_ERR_HIP;
     if (!ev.after(i)) return ENTMAXKV_ERR_HIP;

@@ -1239,7 +1239,9 @@ __global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs 
 // enough of them, else through LDS, pruned. Each lane gathers D / 16 coordinates
 // of the support's V rows. Bound by latency: lengths, entries, pages and V rows wait for
 // each other, so a workgroup is small and many share a CU.
-template <bool BF, int D, int PARTS, int LE>
+// kDense: rows for the dense kernel are done here (few workgroups, which need not
+// share a CU: a launch less, 5.8 us by themselves).
+template <bool BF, int D, int PARTS, int LE, bool kDense>
 __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a, int tok_bits) {
   constexpr int kJoinCap = 16 * LE;
   constexpr int kElem = BF ? 2 : 4, kPer = D / 16;
@@ -1250,7 +1252,7 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
   const int id = blockIdx.x / a.Hkv, g = blockIdx.x - id * a.Hkv;
   const Rows w = find_rows(a, tok_bits, id, g, lane);
   if (w.rows == 0) {
-    if (tid == 0) a.dense[blockIdx.x] = 0;
+    if (!kDense && tid == 0) a.dense[blockIdx.x] = 0;
     return;
   }
   const bool real = row < w.rows;
@@ -1269,10 +1271,13 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
   int worst = 0, total = 0;
   float mx = -INFINITY, slack = 0.0f;
   for (int i = sub; i < pt.count; i += 16) {
+    // (clamped, as tokens and pages are below: starts that do not ascend leave
+    // parts that no block has written)
     const Part part = parts[i];
-    length[row][i] = max(part.n, 0);
+    const int m = min(max(part.n, 0), a.cap);
+    length[row][i] = m;
     worst = min(worst, part.n);
-    total += max(part.n, 0);
+    total += m;
     slack = fmaxf(slack, part.slack);
     if (part.n > 0) mx = fmaxf(mx, part.mx);
   }
@@ -1345,8 +1350,14 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
   }
   const bool dense = worst == kLong || n > kJoinCap;
   const int dense_rows_here = __syncthreads_count(dense && real);
-  if (tid == 0) a.dense[blockIdx.x] = dense_rows_here > 0;
-  if (dense_rows_here) return;
+  if (!kDense && tid == 0) a.dense[blockIdx.x] = dense_rows_here > 0;
+  if (dense_rows_here) {
+    if constexpr (kDense) {
+      __shared__ DenseLds<D> sh;
+      dense_rows<BF, D, PARTS>(a, w, 0, sh);
+    }
+    return;
+  }
 
   const char* kb = static_cast<const char*>(a.k_pool) + ((size_t)g << a.ps_bits) * (D * kElem) +
                    sub * (kPer * kElem);
@@ -1362,8 +1373,11 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
     return BF ? (d & 1 ? bf16_hi(v[d / 2]) : bf16_lo(v[d / 2])) : __uint_as_float(v[BF ? 0 : d]);
   };
   const int32_t* table = a.block_table + (size_t)w.b * a.max_pages;
+  const int last = (a.max_pages << a.ps_bits) - 1;
   auto slot_of = [&](int tok) {
-    return (table[tok >> a.ps_bits] << a.ps_bits) + (tok & ((1 << a.ps_bits) - 1));
+    tok = min(max(tok, 0), last);
+    const int page = min(max(table[tok >> a.ps_bits], 0), a.num_phys - 1);
+    return (page << a.ps_bits) + (tok & ((1 << a.ps_bits) - 1));
   };
   auto solve = [&] {
     mx = -INFINITY;
@@ -1376,6 +1390,11 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
         if (i == 0 || __any(i * 16 < n)) f(entry_z(e[i]));
     });
   };
+  // (asked for before the threshold is solved: the pages of a few tokens too many)
+  int slot[LE];
+#pragma unroll
+  for (int i = 0; i < LE; ++i)
+    slot[i] = i * 16 + sub < n ? slot_of(entry_t(e[i])) : 0;
   float t = solve();
   // scores of rounded queries: those that may be in the support again, in float32
   const bool again = BF && PARTS > 1 && __any(slack > 0.0f);
@@ -1388,7 +1407,7 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
       const bool keep = i * 16 + sub < n && !(entry_z(e[i]) <= thr);
       const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
       if (keep)
-        list[kept + __popc(all & ((1u << sub) - 1))] = entry(0.0f, slot_of(entry_t(e[i])));
+        list[kept + __popc(all & ((1u << sub) - 1))] = entry(0.0f, slot[i]);
       kept += __popc(all);
     }
     n = kept;
@@ -1400,11 +1419,11 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
     constexpr int U = 8;  // rows on their way
     for (int i = 0; i < n; i += U) {
       vec k[U];
-      int slot[U];
+      int at[U];
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        slot[j] = entry_t(list[min(i + j, n - 1)]);
-        k[j] = row_of(kb, slot[j]);
+        at[j] = entry_t(list[min(i + j, n - 1)]);
+        k[j] = row_of(kb, at[j]);
       }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
@@ -1412,13 +1431,15 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
 #pragma unroll
         for (int d = 0; d < kPer; ++d) z = fmaf(q[d], coord(k[j], d), z);
         z = sum16(z);
-        if (sub == 0 && i + j < n) list[i + j] = entry(z, slot[j]);
+        if (sub == 0 && i + j < n) list[i + j] = entry(z, at[j]);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < LE; ++i)
       e[i] = i * 16 + sub < n ? list[i * 16 + sub] : entry(-INFINITY, 0);
+#pragma unroll
+    for (int i = 0; i < LE; ++i) slot[i] = entry_t(e[i]);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     t = solve();
   }
@@ -1436,7 +1457,7 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
     const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
     if (keep)
       list[live + __popc(all & ((1u << sub) - 1))] =
-          entry(p, again ? entry_t(e[i]) : slot_of(entry_t(e[i])));
+          entry(p, slot[i]);
     live += __popc(all);
   }
   l = sum16(l);
@@ -1483,22 +1504,34 @@ __global__ __launch_bounds__(kChunkWaves * kWave, 2) void dense_kernel(ChunkArgs
   dense_rows<BF, D, PARTS>(a, w, 0, sh);
 }
 
+template <bool BF, int D, int PARTS, int LE>
+void launch_finish(const ChunkArgs& a, const ChunkPlan& p, hipStream_t st) {
+  const dim3 grid((unsigned)p.tiles), threads(kChunkWaves * kWave);
+  if (p.kernels == 2)
+    hipLaunchKernelGGL((finish_kernel<BF, D, PARTS, LE, true>), grid, threads, 0, st, a,
+                       p.tile_bits);
+  else
+    hipLaunchKernelGGL((finish_kernel<BF, D, PARTS, LE, false>), grid, threads, 0, st, a,
+                       p.tile_bits);
+}
+
 template <bool BF, int D, int PARTS>
 hipError_t launch(const ChunkArgs& a, const ChunkPlan& p, int kernel, hipStream_t st) {
   const dim3 threads(kChunkWaves * kWave);
   if (kernel == 0)
     hipLaunchKernelGGL((list_kernel<BF, D, PARTS>), dim3((unsigned)p.items), threads, 0, st, a);
   else if (kernel == 1 && a.cap == 128)
-    hipLaunchKernelGGL((finish_kernel<BF, D, PARTS, 8>), dim3((unsigned)p.tiles), threads, 0, st, a,
-                       p.tile_bits);
+    launch_finish<BF, D, PARTS, 8>(a, p, st);
   else if (kernel == 1)
-    hipLaunchKernelGGL((finish_kernel<BF, D, PARTS, 16>), dim3((unsigned)p.tiles), threads, 0, st,
-                       a, p.tile_bits);
+    launch_finish<BF, D, PARTS, 16>(a, p, st);
   else
     hipLaunchKernelGGL((dense_kernel<BF, D, PARTS>), dim3((unsigned)p.tiles), threads, 0, st, a,
                        p.tile_bits);
   return hipGetLastError();
 }
+
+// Workgroups of the finish kernel up to which the dense rows are done there.
+constexpr long long kFewTiles = 2 * kNumCUs;
 
 }  // namespace
 
@@ -1510,6 +1543,7 @@ ChunkPlan plan_chunk(const LaunchShape& s, int num_tokens, float alpha) {
   p.tile_bits = 4 - g_bits;
   p.threads = kChunkWaves * kWave;
   p.tiles = ((long long)(num_tokens >> p.tile_bits) + s.batch) * s.num_kv_heads;
+  p.kernels = p.tiles <= kFewTiles ? 2 : 3;
   const long long ids = (long long)(num_tokens >> p.tok_bits) + s.batch;
   const long long total = (long long)s.max_pages * s.page_size;
   // parts of a row's tokens: about two workgroups a CU where there are fewer

@@ -345,7 +345,6 @@ hipError_t launch_append_kv(const LaunchShape& s, const AppendParams& p, hipStre
 
 // alpha-entmax attention of a ragged chunk (chunk.hip): lists, finish, dense.
 constexpr int kChunkMaxSplits = 64;
-constexpr int kChunkKernels = 3;
 struct ChunkPlan {
   int tok_bits = 0, tile_bits = 0;   // log2 of the tokens of a list and of a 16-row block
   long long items = 0, few_items = 0, tiles = 0;  // workgroups of the list kernel, those of few
@@ -353,10 +352,11 @@ struct ChunkPlan {
   int splits = 1, few_splits = 1;    // parts of a row's tokens; in blocks of at most 16 rows
   int cap = 0;                       // entries of a part's list
   int threads = 0;                   // of a workgroup
+  int kernels = 3;                   // 2: the finish kernel does the dense rows
   size_t few_parts = 0, parts_off = 0, dense_off = 0, ws_bytes = 0;
 };
 ChunkPlan plan_chunk(const LaunchShape& s, int num_tokens, float alpha);
-// kernel: 0 .. kChunkKernels - 1, launched in this order
+// kernel: 0 .. p.kernels - 1, launched in this order
 hipError_t launch_chunk(const LaunchShape& s, const ChunkPlan& p, int kernel, const void* q,
                         bool q_bf16, int num_tokens, const int32_t* token_starts,
                         const void* k_pool, const void* v_pool, const int32_t* block_table,
