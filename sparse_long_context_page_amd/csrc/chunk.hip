@@ -25,7 +25,7 @@ constexpr int kChunkWaves = 4;
 struct __align__(16) Part {
   int32_t n;        // entries, or why there are none
   float mx, slack;  // the largest score; how far two scores may be off together
-  int32_t unused;
+  float thr;        // a bound of the row's threshold from below, but for `slack`
 };
 
 struct ChunkArgs {
@@ -1095,7 +1095,7 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
   }
   if (lane < wrows)
     a.parts[row_at(a, w, wr + lane) * a.splits + split] =
-        Part{mine.n[lane], max_of4(mine.top[lane]), 2.0f * kmax * mine.off[lane], 0};
+        Part{mine.n[lane], max_of4(mine.top[lane]), 2.0f * kmax * mine.off[lane], mine.thr[lane]};
 }
 
 // At most 16 rows (single tokens): the waves share them and take turns at the
@@ -1201,7 +1201,7 @@ __device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int 
       kept += __popc(all);
     }
   if (sub == 0 && real)
-    a.parts[part] = Part{worst < 0 ? worst : kept > a.cap ? kLong : kept, mx, 0.0f, 0};
+    a.parts[part] = Part{worst < 0 ? worst : kept > a.cap ? kLong : kept, mx, 0.0f, thr};
 }
 
 template <bool BF>
@@ -1234,6 +1234,30 @@ __global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs 
 // ---------------------------------------------------------------------------
 // tau and the output from the lists
 
+constexpr int kJoins = 3;  // times a bound is taken for lists too long for LDS
+
+// The lists of P parts as one: entry j of them lies at place(j).
+template <int P>
+struct Run {
+  int before[P - 1], shift[P - 1], total = 0;
+  __device__ __forceinline__ Run(const int* length, int first, int count, int cap) {
+#pragma unroll
+    for (int s = 0; s < P; ++s) {
+      const int m = first + s < count ? length[first + s] : 0;
+      total += m;
+      if (s == P - 1) break;
+      before[s] = total;
+      shift[s] = cap - m;
+    }
+  }
+  __device__ __forceinline__ int place(int j) const {
+    int to = j;
+#pragma unroll
+    for (int s = 0; s < P - 1; ++s) to += j >= before[s] ? shift[s] : 0;
+    return to;
+  }
+};
+
 // 16 lanes a row, 16 rows a workgroup (as dense_kernel takes them). A row's
 // entries go straight to the lanes' registers, LE a lane, where there are few
 // enough of them, else through LDS, pruned. Each lane gathers D / 16 coordinates
@@ -1242,7 +1266,7 @@ __global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs 
 // kDense: rows for the dense kernel are done here (few workgroups, which need not
 // share a CU: a launch less, 5.8 us by themselves).
 template <bool BF, int D, int PARTS, int LE, bool kDense>
-__global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a, int tok_bits) {
+__global__ __launch_bounds__(kChunkWaves * kWave, kDense ? 1 : 5) void finish_kernel(ChunkArgs a, int tok_bits) {
   constexpr int kJoinCap = 16 * LE;
   constexpr int kElem = BF ? 2 : 4, kPer = D / 16;
   typedef uint32_t vec __attribute__((ext_vector_type(kPer * kElem / 4)));
@@ -1269,7 +1293,7 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
   uint64_t* list = joint[row];
 
   int worst = 0, total = 0;
-  float mx = -INFINITY, slack = 0.0f;
+  float mx = -INFINITY, low = -INFINITY, slack = 0.0f;
   for (int i = sub; i < pt.count; i += 16) {
     // (clamped, as tokens and pages are below: starts that do not ascend leave
     // parts that no block has written)
@@ -1280,33 +1304,31 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
     total += m;
     slack = fmaxf(slack, part.slack);
     if (part.n > 0) mx = fmaxf(mx, part.mx);
+    if (part.n > 0) low = fmaxf(low, part.thr);
   }
   worst = reduce16(worst, [](int x, int y) { return min(x, y); });
   total = reduce16(total, [](int x, int y) { return x + y; });
   slack = max16(slack);
   mx = max16(mx);
+  low = max16(low);
   if (worst < 0) total = 0;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 
+  const int count = worst < 0 ? 0 : pt.count;
+
   // this lane's entries sub, sub + 16, ... of the row's n
   uint64_t e[LE];
-#pragma unroll
-  for (int i = 0; i < LE; ++i) e[i] = entry(-INFINITY, 0);
   int n = total;
   if (!__any(total > kJoinCap || pt.count > 4)) {
-    int before = 0;
-    for (int s = 0; s < pt.count; ++s) {
-      const int m = total > 0 ? length[row][s] : 0;
+    const Run<4> run(length[row], 0, count, a.cap);
 #pragma unroll
-      for (int i = 0; i < LE; ++i) {
-        const int j = i * 16 + sub - before;
-        if (j >= 0 && j < m) e[i] = lists[s * a.cap + j];
-      }
-      before += m;
+    for (int i = 0; i < LE; ++i) {
+      const int j = i * 16 + sub;
+      e[i] = j < total ? lists[run.place(j)] : entry(-INFINITY, 0);
     }
   } else {
-    // many: through LDS those that may have a weight, by the joint maximum, or by
-    // the joint threshold if that is too much
+    // many: through LDS those that may have a weight, by the joint maximum and the
+    // parts' bounds
     auto gather = [&](float thr) {
       int k = 0;
       auto take = [&](uint64_t x, bool mine) {
@@ -1316,37 +1338,44 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
         if (keep && to < kJoinCap) list[to] = x;
         k += __popc(all);
       };
-      constexpr int U = 4;  // parts on their way
-      for (int s = 0; s < pt.count; s += U) {
-        uint64_t x[U];
-        int m[U];
+      for (int s = 0; s < count; s += 8) {
+        const Run<8> run(length[row], s, count, a.cap);
+        for (int i = 0; i < run.total; i += LE * 16) {  // LE loads on their way
+          uint64_t x[LE];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          m[u] = s + u < pt.count && total > 0 ? length[row][s + u] : 0;
-          x[u] = sub < m[u] ? lists[(s + u) * a.cap + sub] : 0;
-        }
+          for (int u = 0; u < LE; ++u) {
+            const int j = i + u * 16 + sub;
+            x[u] = j < run.total ? lists[s * a.cap + run.place(j)] : 0;
+          }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          take(x[u], sub < m[u]);
-          for (int i = 16; i < m[u]; i += 16)
-            take(i + sub < m[u] ? lists[(s + u) * a.cap + i + sub] : 0, i + sub < m[u]);
+          for (int u = 0; u < LE; ++u)
+            if (i + u * 16 < run.total) take(x[u], i + u * 16 + sub < run.total);
         }
       }
       return k;
     };
-    n = gather(mx - a.window - slack);
-    if (__any(n > kJoinCap)) {
-      const float t = solve16(a, mx, n > kJoinCap, [&](auto f) {
-        if (n <= kJoinCap) return;
-        for (int s = 0; s < pt.count; ++s)
-          for (int i = sub; i < length[row][s]; i += 16) f(entry_z(lists[s * a.cap + i]));
+    low = fmaxf(low, mx - a.window);
+    n = gather(low - slack);
+    // the first that fit bound the threshold of all
+    for (int i = 0; i < kJoins && __any(n > kJoinCap); ++i) {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      const bool much = n > kJoinCap;
+      float big = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < LE; ++k) big = fmaxf(big, much ? entry_z(list[k * 16 + sub]) : 0.0f);
+      big = max16(big);
+      const float t = solve16(a, big, much, [&](auto f) {
+        for (int k = 0; k < LE; ++k)
+          if (much) f(entry_z(list[k * 16 + sub]));
       });
-      n = gather((n > kJoinCap ? bound_of(a, mx, t) : mx - a.window) - slack);
+      if (much) low = fmaxf(low, bound_of(a, big, t));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      n = gather(low - slack);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int i = 0; i < LE; ++i)
-      if (i * 16 + sub < n) e[i] = list[i * 16 + sub];
+      e[i] = i * 16 + sub < n ? list[min(i * 16 + sub, kJoinCap - 1)] : entry(-INFINITY, 0);
   }
   const bool dense = worst == kLong || n > kJoinCap;
   const int dense_rows_here = __syncthreads_count(dense && real);
@@ -1416,7 +1445,7 @@ __global__ __launch_bounds__(kChunkWaves * kWave) void finish_kernel(ChunkArgs a
 #pragma unroll
     for (int d = 0; d < kPer; ++d)
       q[d] = static_cast<const float*>(a.q)[at * D + sub * kPer + d];
-    constexpr int U = 8;  // rows on their way
+    constexpr int U = 4;  // rows on their way
     for (int i = 0; i < n; i += U) {
       vec k[U];
       int at[U];
