@@ -57,9 +57,11 @@ struct ChunkArgs {
 
 // Entries of a list by alpha: support sizes grow as alpha falls (scores of
 // spread 2.5, 32K tokens: 8 tokens on average and 20 at most at alpha 1.5, 67 and
-// 140 at 1.25, 200 rows each). Fewer entries are a smaller workspace and, in the
-// finish kernel, more workgroups a CU.
-constexpr int cap_of(float alpha) { return alpha >= 1.5f ? 128 : 256; }
+// 140 at 1.25, 200 rows each), and with them the hits, so that a short list is
+// pruned more often; a long one is more workspace. Measured, 4096 of 32K tokens at
+// alpha 1.25, list and finish kernel: 256 entries 2.88 + 0.55 ms, 384 2.40 + 0.66,
+// 512 2.32 + 0.67.
+constexpr int cap_of(float alpha) { return alpha >= 1.5f ? 128 : 384; }
 // Lengths that say why there is no list.
 constexpr int kLong = -1;    // the support does not fit
 constexpr int kNoNumber = -2;  // a score is NaN or +inf
@@ -598,8 +600,8 @@ constexpr int kListTiles = BF ? 4 : 2;
 // the few tokens that matter its nearest bf16 does: a score of it is off by at
 // most e = sum |q - q'| * max |k| (both known), so that no token within 2 e of a
 // bound is dropped; the finish kernel takes those that are left once more, in
-// float32. (Three parts in this kernel: 1.20 ms for the mixed batch of 32, one:
-// see below.)
+// float32. (Mixed batch of 32, list kernel: three
+// parts 1.20 ms, one 0.69; 70 us in the finish kernel in place of 40.)
 template <int D>
 __device__ __forceinline__ void load_nearest(QFrag<true, D, 1>& q, const char* row, int c,
                                              float& off) {
@@ -793,7 +795,9 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       const uint64_t long_ones = __ballot(pending);
       if (long_ones == 0) break;
-      // prune that row's list and its neighbours', 4 rows at a time
+  // prune that row's list and its neighbours', 4 rows at a time; thresholds are
+      // solved where three quarters stay (where half do: 3.12 ms in place of 2.88, as
+      // above with 256 entries)
       const int r = __builtin_amdgcn_readlane(row, __builtin_ctzll(long_ones));
       const int row4 = (r & ~3) + (lane >> 4);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
@@ -802,7 +806,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       const f32x4 tops = w.top[row4];
       const float bound =
           prune16(a, at(row4), lane, max_of4(tops), fmaxf(w.thr[row4], max_of4(tops) - a.window),
-                  2.0f * kmax * w.off[row4], a.cap / 2, kept);
+                  2.0f * kmax * w.off[row4], a.cap / 4 * 3, kept);
       if ((lane & 15) == 0 && any) {
         const bool no_room = kept > a.cap - NZ;
         w.n[row4] = no_room ? kLong : kept;
@@ -1234,7 +1238,9 @@ __global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs 
 // ---------------------------------------------------------------------------
 // tau and the output from the lists
 
-constexpr int kJoins = 3;  // times a bound is taken for lists too long for LDS
+// Times a bound is taken for lists too long for LDS, at most: each brings nearer
+// the support of the row, or that it is too long.
+constexpr int kJoins = 16;
 
 // The lists of P parts as one: entry j of them lies at place(j).
 template <int P>
