@@ -592,10 +592,16 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
  * overflow. What lies in hidden tokens' rows and in page tails has no effect,
  * NaN and infinities included, nor do values of zero weight; a seen score that
  * is NaN or +inf makes its row's out and tau NaN. Scores are float32, as in
- * entmaxkv_softmax_window; weights are used in float32 or to 2^-17 of
- * themselves (bf16 queries). Results do not depend on what else runs (no
- * atomics on results).
- * Workspace: entmaxkv_entmax_chunk_ws bytes. Kernels launched: 3 (lists of the
+ * entmaxkv_softmax_window; weights are used in float32 or, in rows whose support
+ * is too long for a list, to 2^-17 of themselves (bf16 queries). Of float32
+ * queries over a BF16 cache hidden rows of the same block may move the last bits
+ * (which tokens are taken again in float32 is decided for a block), and |q| stays
+ * below 2^127. Results do not depend on what else runs (no atomics on results).
+ * Weights on hundreds of tokens (beyond 128 from alpha 1.5, 256 below) are right
+ * but slow: their rows go over all scores once a threshold step.
+ * Workspace: entmaxkv_entmax_chunk_ws bytes, for one call at a time (calls that
+ * may overlap, graphs that replay side by side, need one each); it holds nothing
+ * between calls. Kernels launched: 3 (lists of the
  * tokens that may have a weight; tau and the output; rows whose support is too
  * long for a list), or 2 for few tokens, the last within the second (events'
  * pair 2 then encloses nothing).

@@ -600,8 +600,9 @@ constexpr int kListTiles = BF ? 4 : 2;
 // the few tokens that matter its nearest bf16 does: a score of it is off by at
 // most e = sum |q - q'| * max |k| (both known), so that no token within 2 e of a
 // bound is dropped; the finish kernel takes those that are left once more, in
-// float32. (Mixed batch of 32, list kernel: three
-// parts 1.20 ms, one 0.69; 70 us in the finish kernel in place of 40.)
+// float32. (Two chunks of 512 among 32K tokens, list and finish kernel: float32
+// queries 380 + 69 us, bf16 queries 336 + 40; three parts take three times the
+// matrix instructions.)
 template <int D>
 __device__ __forceinline__ void load_nearest(QFrag<true, D, 1>& q, const char* row, int c,
                                              float& off) {
@@ -844,7 +845,11 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
 }
 
 // More than 16 rows: every wave has NT row tiles of its own, K staged in LDS for
-// all of them.
+// all of them. Bound by the matrix instructions, and beside them by hits (queue
+// and flush): 4096 of 32K tokens, 32/8 heads of 128 dims, 1.15 ms or 900 TFLOP/s
+// of the score product alone; without a hit 0.88 ms. A prompt of 2048, whose rows
+// have nearly all of their hits before the bounds have settled: 86 us, its product
+// 17.
 template <bool BF, int D, int PARTS, int NT>
 __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int split,
                                           ListLds<BF, D>& lds) {
@@ -1062,6 +1067,8 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
     // The queues are emptied by all waves together, about when they hold a batch
     // (a row's hits become rarer as 1 / tokens): a wave that does so by itself
     // has the others wait at the next barrier. Before this tile's hits go in.
+    // (4096 of 32K tokens, after 1/2, 1/4, 1/8, 1/16 of the tokens so far: 1293, 1218,
+    // 1219, 1522 us.)
     int total = 0;
     if (any) {
 #pragma unroll
@@ -1104,7 +1111,8 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
 
 // At most 16 rows (single tokens): the waves share them and take turns at the
 // tiles, loaded from memory straight into the operands' registers; each keeps
-// lists of its own in LDS, joined at the end.
+// lists of its own in LDS, joined at the end. Bound by memory: 30 sequences of 32K
+// tokens (1.75 GB of keys) 320 us, 5.5 TB/s.
 template <bool BF, int D, int PARTS>
 __device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int split,
                                          ListLds<BF, D>& lds) {
@@ -1268,9 +1276,12 @@ struct Run {
 // entries go straight to the lanes' registers, LE a lane, where there are few
 // enough of them, else through LDS, pruned. Each lane gathers D / 16 coordinates
 // of the support's V rows. Bound by latency: lengths, entries, pages and V rows wait for
-// each other, so a workgroup is small and many share a CU.
-// kDense: rows for the dense kernel are done here (few workgroups, which need not
-// share a CU: a launch less, 5.8 us by themselves).
+// each other, so a workgroup is small and many share a CU (the bound of five waves
+// a SIMD: float32 queries, 4096 of 32K tokens, 187 us; without it 209). A prompt of
+// 2048 39 us, of which 34 without the threshold's steps and 38 without the V rows.
+// kDense: rows for the dense kernel are done here, by few workgroups, which need
+// not share a CU: a launch less (four short chats 27.4 us against 29.1; a prompt of
+// 2048, which has 16 workgroups a CU, 163 against 122).
 template <bool BF, int D, int PARTS, int LE, bool kDense>
 __global__ __launch_bounds__(kChunkWaves * kWave, kDense ? 1 : 5) void finish_kernel(ChunkArgs a, int tok_bits) {
   constexpr int kJoinCap = 16 * LE;
@@ -1582,7 +1593,9 @@ ChunkPlan plan_chunk(const LaunchShape& s, int num_tokens, float alpha) {
   const long long ids = (long long)(num_tokens >> p.tok_bits) + s.batch;
   const long long total = (long long)s.max_pages * s.page_size;
   // parts of a row's tokens: about two workgroups a CU where there are fewer
-  // blocks; more parts bring more hits, as each begins without a bound
+  // blocks; more parts bring more hits, as each begins without a bound (four a CU
+  // against two, list and finish kernel, us: 4096 of 32K tokens 1677 + 188 : 1524 +
+  // 76, a prompt of 2048 87 + 63 : 88 + 51, odd float32 chunks 212 + 311 : 296 + 178)
   const auto parts_for = [&](long long want, long long blocks, long long least) {
     const long long n = want / (blocks > 0 ? blocks : 1), most = (total + least - 1) / least;
     const long long k = n < most ? n : most;
@@ -1590,7 +1603,8 @@ ChunkPlan plan_chunk(const LaunchShape& s, int num_tokens, float alpha) {
   };
   const long long full = num_tokens >> p.tok_bits;
   p.splits = parts_for(2 * kNumCUs, (full > 0 ? full : 1) * s.num_kv_heads, 256);
-  // single tokens: eight, and never a long cache by one workgroup
+  // single tokens: eight, and never a long cache by one workgroup (4, 8, 16 of
+  // them: mixed batch of 32 1051, 1028, 1026 us)
   p.few_splits = parts_for(8 * kNumCUs, (long long)s.batch * s.num_kv_heads, 512);
   p.few_items = (long long)s.batch * s.num_kv_heads * p.few_splits;
   p.items = p.few_items + ids * s.num_kv_heads * p.splits;
