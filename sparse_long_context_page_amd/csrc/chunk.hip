@@ -589,10 +589,13 @@ __device__ __forceinline__ Cache cache_of(const ChunkArgs& a, const Rows& w, int
   return x;
 }
 
-constexpr int kYoung = 2;  // stages
+// Stages whose tiles' own maxima go before the bounds (none, 2, 8 of them: a prompt
+// of 2048 88, 85, 86 us; mixed batch of 32 693, 694, 701).
+constexpr int kYoung = 2;
 
 // Row tiles a wave holds: with a bf16 cache 64 rows share each K operand read from
-// LDS; float32 rows take the registers of more.
+// LDS (4096 of 32K tokens 1.15 ms, with 32 rows 1.55); float32 rows take the
+// registers of more.
 template <bool BF>
 constexpr int kListTiles = BF ? 4 : 2;
 
@@ -1224,9 +1227,11 @@ __global__ __launch_bounds__(kChunkWaves * kWave, 2) void list_kernel(ChunkArgs 
   __shared__ __align__(1024) ListLds<BF, D> lds;
   // over the KV heads first: with 8 of them, the blocks that read the same
   // head's tokens share an XCD and its L2; then the parts. The blocks of few rows
-  // come first: they are bound by memory, those that start beside them are not.
-  const bool few = blockIdx.x < a.few_items;
-  const int item = few ? blockIdx.x : blockIdx.x - a.few_items;
+  // come last: they are short and fill in behind the others (first, and last: odd
+  // float32 chunks 283, 249 us, mixed batch of 32 761, 755).
+  const unsigned many_items = gridDim.x - a.few_items;
+  const bool few = blockIdx.x >= many_items;
+  const int item = few ? blockIdx.x - many_items : blockIdx.x;
   const int splits = few ? a.few_splits : a.splits;
   const int x = item / a.Hkv, g = item - x * a.Hkv;
   const int id = x / splits, split = x - id * splits;
@@ -1593,9 +1598,9 @@ ChunkPlan plan_chunk(const LaunchShape& s, int num_tokens, float alpha) {
   const long long ids = (long long)(num_tokens >> p.tok_bits) + s.batch;
   const long long total = (long long)s.max_pages * s.page_size;
   // parts of a row's tokens: about two workgroups a CU where there are fewer
-  // blocks; more parts bring more hits, as each begins without a bound (four a CU
-  // against two, list and finish kernel, us: 4096 of 32K tokens 1677 + 188 : 1524 +
-  // 76, a prompt of 2048 87 + 63 : 88 + 51, odd float32 chunks 212 + 311 : 296 + 178)
+  // blocks; more parts bring more hits, as each begins without a bound (one, two,
+  // four a CU, us: 4096 of 32K tokens 1260, 1261, 1378; mixed batch of 32 1050, 761,
+  // 832; a prompt of 2048 153, 123, 130; odd float32 chunks 322, 283, 279)
   const auto parts_for = [&](long long want, long long blocks, long long least) {
     const long long n = want / (blocks > 0 ? blocks : 1), most = (total + least - 1) / least;
     const long long k = n < most ? n : most;
