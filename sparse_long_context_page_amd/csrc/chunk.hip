@@ -1057,7 +1057,7 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
           for (int t = 0; t < NT; ++t) {
             float m = max_across(tmax[t]) - a.window;
             if constexpr (kNear) m -= 2.0f * kmax * mine.off[t * 16 + rl];
-            thr[t] = fmaxf(thr[t], m);
+            if (m < INFINITY) thr[t] = fmaxf(thr[t], m);  // (+inf has to be a hit)
           }
         }
 #pragma unroll
