@@ -463,6 +463,14 @@ __device__ __forceinline__ float bound_of(const ChunkArgs& a, float mx, float t)
   return mx + (t - 2.0e-6f) / a.am1 - 1.0e-6f * fabsf(mx);
 }
 
+// A score below every one that may have a weight beside the maximum mx. What is
+// relative to mx is for the difference's own rounding: half a unit in the last
+// place of mx, 2^-24 of it, may be more than the window itself. (mx = +inf: NaN,
+// which bounds nothing.)
+__device__ __forceinline__ float window_below(const ChunkArgs& a, float mx) {
+  return mx - a.window - 1.0e-6f * fabsf(mx);
+}
+
 // One row's running state, the same in the four lanes that hold its scores.
 struct Track {
   float mx = -INFINITY, thr = -INFINITY;
@@ -542,7 +550,7 @@ __device__ __forceinline__ void collect(const ChunkArgs& a, Track& tr,
                                         int lane, At at) {
   const int c = lane >> 4;
   tr.mx = __builtin_elementwise_maximum(tr.mx, max_across(tmax));
-  tr.thr = fmaxf(tr.thr, tr.mx - a.window);
+  tr.thr = fmaxf(tr.thr, window_below(a, tr.mx));
   // this row's four lanes, and those of them below this one
   const uint64_t row = 0x0001000100010001ull << (lane & 15), below = row & lanemask_below(lane);
   uint64_t* list = at(lane & 15);
@@ -775,7 +783,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       const int n = w.n[row];
       const float thr =
-          fmaxf(w.thr[row], max_of4(w.top[row]) - a.window) - 2.0f * kmax * w.off[row];
+          fmaxf(w.thr[row], window_below(a, max_of4(w.top[row]))) - 2.0f * kmax * w.off[row];
       unsigned bits = 0;
 #pragma unroll
       for (int i = 0; i < NZ; ++i) bits |= (z[i] > thr ? 1u : 0u) << i;
@@ -807,9 +815,9 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the entries are written
       int kept = max(w.n[row4], 0);
       const bool any = kept > 0;
-      const f32x4 tops = w.top[row4];
+      const float mx4 = max_of4(w.top[row4]);
       const float bound =
-          prune16(a, at(row4), lane, max_of4(tops), fmaxf(w.thr[row4], max_of4(tops) - a.window),
+          prune16(a, at(row4), lane, mx4, fmaxf(w.thr[row4], window_below(a, mx4)),
                   2.0f * kmax * w.off[row4], a.cap / 4 * 3, kept);
       if ((lane & 15) == 0 && any) {
         const bool no_room = kept > a.cap - NZ;
@@ -1055,9 +1063,9 @@ __device__ __forceinline__ void list_many(const ChunkArgs& a, const Rows& w, int
         if (__builtin_expect(v < v0 + kYoung, 0)) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            float m = max_across(tmax[t]) - a.window;
+            float m = window_below(a, max_across(tmax[t]));  // (+inf has to be a hit: NaN here)
             if constexpr (kNear) m -= 2.0f * kmax * mine.off[t * 16 + rl];
-            if (m < INFINITY) thr[t] = fmaxf(thr[t], m);  // (+inf has to be a hit)
+            thr[t] = fmaxf(thr[t], m);
           }
         }
 #pragma unroll
@@ -1194,7 +1202,7 @@ __device__ __forceinline__ void list_few(const ChunkArgs& a, const Rows& w, int 
   float mx = -INFINITY;
   each([&](uint64_t e) { mx = fmaxf(mx, entry_z(e)); });
   mx = max16(mx);
-  float thr = mx - a.window;
+  float thr = window_below(a, mx);
   int most = 0;
   each([&](uint64_t e) { most += entry_z(e) > thr ? 1 : 0; });
   const bool much = sum16((float)most) > (float)a.cap;
@@ -1376,7 +1384,7 @@ __global__ __launch_bounds__(kChunkWaves * kWave, kDense ? 1 : 5) void finish_ke
       }
       return k;
     };
-    low = fmaxf(low, mx - a.window);
+    low = fmaxf(low, window_below(a, mx));
     n = gather(low - slack);
     // the first that fit bound the threshold of all
     for (int i = 0; i < kJoins && __any(n > kJoinCap); ++i) {
