@@ -49,7 +49,7 @@ struct ChunkArgs {
   size_t few_parts;        // the first of the few-row blocks' parts
   unsigned few_items;      // their workgroups
   // workspace: per (row, part) the list, its length and how far its scores may
-  // be off together, and per 16 rows whether they need the dense kernel
+  // be off together, and per 16 rows a bit for each that needs the dense kernel
   uint64_t* lists;
   Part* parts;
   int32_t* dense;
@@ -199,11 +199,13 @@ struct DenseLds {
   float s[2][kChunkWaves][16][2];
 };
 
-// Rows r0 .. r0 + 15 of a block by passes over all of their scores: the
-// maximum, one pass a threshold step, and the weights' product with V. The
-// workgroup's waves share the rows and take turns at the tiles.
+// Those of a block's 16 rows at most that `which` has a bit for, by passes over
+// all of their scores: the maximum, one pass a threshold step, and the weights'
+// product with V. The workgroup's waves share the rows and take turns at the
+// tiles. The other rows keep what their lists gave, in other roundings (with
+// bf16 queries the weights of these are off by 2^-17).
 template <bool BF, int D, int PARTS>
-__device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, int r0,
+__device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, unsigned which,
                                            DenseLds<D>& sh) {
   constexpr int TT = kTile<BF>;
   constexpr int NZ = scores_per_lane<BF>();
@@ -215,10 +217,9 @@ __device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, in
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane >> 4, rl = lane & 15;
-  const int nrows = min(16, w.rows - r0);
-  const bool mine = rl < nrows;
-  const int hi = mine ? seen(a, w, r0 + rl) : 0;
-  const int top = seen(a, w, r0 + nrows - 1);  // the last row sees the most
+  const bool mine = which >> rl & 1;
+  const int hi = mine ? seen(a, w, rl) : 0;
+  const int top = seen(a, w, 31 - __builtin_clz(which));  // the last row sees the most
   const int tiles = (top + TT - 1) / TT, npages = (top + (1 << a.ps_bits) - 1) >> a.ps_bits;
   const size_t head_off = ((size_t)w.g << a.ps_bits) * (D * kElem);
   const size_t page_bytes = ((size_t)a.Hkv << a.ps_bits) * (D * kElem);
@@ -227,7 +228,7 @@ __device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, in
   const int32_t* table = a.block_table + (size_t)w.b * a.max_pages;
 
   QFrag<BF, D, PARTS> q;
-  q.load(mine ? static_cast<const char*>(a.q) + row_at(a, w, r0 + rl) * (D * QB) : nullptr, c);
+  q.load(mine ? static_cast<const char*>(a.q) + row_at(a, w, rl) * (D * QB) : nullptr, c);
 
   // f(tile's first token, its pages, this lane's scores; -inf where hidden)
   auto each_tile = [&](auto f) {
@@ -371,7 +372,8 @@ __device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, in
   }
   __syncthreads();
   constexpr int TPR = D / 4;
-  for (int r = tid / TPR; r < nrows; r += NW * kWave / TPR) {
+  for (int r = tid / TPR; r < 16; r += NW * kWave / TPR) {
+    if (!(which >> r & 1)) continue;
     const int d = (tid % TPR) * 4;
     float ls = 0.0f;
     int lv = 0;
@@ -383,7 +385,7 @@ __device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, in
       o += *reinterpret_cast<const f32x4*>(&sh.o[v][r][d]);
     }
     const float kind = sh.s[1][0][r][1];
-    const size_t at = row_at(a, w, r0 + r);
+    const size_t at = row_at(a, w, r);
     const float inv = kind == 1.0f ? 1.0f / ls : kind;
     f32x4 y = o * inv;
     if (kind != 1.0f) y = f32x4{kind, kind, kind, kind};
@@ -1302,6 +1304,7 @@ __global__ __launch_bounds__(kChunkWaves * kWave, kDense ? 1 : 5) void finish_ke
   typedef uint32_t vec __attribute__((ext_vector_type(kPer * kElem / 4)));
   __shared__ uint64_t joint[16][kJoinCap];
   __shared__ int length[16][kChunkMaxSplits];
+  __shared__ unsigned wave_dense[kChunkWaves];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), sub = tid & 15, row = tid >> 4;
   const int id = blockIdx.x / a.Hkv, g = blockIdx.x - id * a.Hkv;
   const Rows w = find_rows(a, tok_bits, id, g, lane);
@@ -1407,16 +1410,18 @@ __global__ __launch_bounds__(kChunkWaves * kWave, kDense ? 1 : 5) void finish_ke
     for (int i = 0; i < LE; ++i)
       e[i] = i * 16 + sub < n ? list[min(i * 16 + sub, kJoinCap - 1)] : entry(-INFINITY, 0);
   }
-  const bool dense = worst == kLong || n > kJoinCap;
-  const int dense_rows_here = __syncthreads_count(dense && real);
-  if (!kDense && tid == 0) a.dense[blockIdx.x] = dense_rows_here > 0;
-  if (dense_rows_here) {
-    if constexpr (kDense) {
-      __shared__ DenseLds<D> sh;
-      dense_rows<BF, D, PARTS>(a, w, 0, sh);
-    }
-    return;
-  }
+  const bool dense = real && (worst == kLong || n > kJoinCap);
+  // a bit for each of the workgroup's rows that is dense; the others go on
+  const uint64_t lanes = __ballot(dense && sub == 0);
+  if (lane == 0)
+    wave_dense[tid / kWave] =
+        (lanes & 1) | (lanes >> 15 & 2) | (lanes >> 30 & 4) | (lanes >> 45 & 8);
+  __syncthreads();
+  unsigned which = 0;
+#pragma unroll
+  for (int v = 0; v < kChunkWaves; ++v) which |= wave_dense[v] << (4 * v);
+  if (!kDense && tid == 0) a.dense[blockIdx.x] = which;
+  if (dense) n = total = 0;
 
   const char* kb = static_cast<const char*>(a.k_pool) + ((size_t)g << a.ps_bits) * (D * kElem) +
                    sub * (kPer * kElem);
@@ -1542,25 +1547,31 @@ __global__ __launch_bounds__(kChunkWaves * kWave, kDense ? 1 : 5) void finish_ke
       for (int d = 0; d < kPer; ++d) acc[d] = fmaf(p[k], coord(v[k], d), acc[d]);
     }
   }
-  if (!real) return;
-  const float inv = worst == kNoNumber ? NAN : total == 0 ? 0.0f : 1.0f / l;
+  if (real && !dense) {
+    const float inv = worst == kNoNumber ? NAN : total == 0 ? 0.0f : 1.0f / l;
 #pragma unroll
-  for (int d = 0; d < kPer; d += 4)
-    store_out<PARTS>(a.out, at * D + sub * kPer + d,
-                     f32x4{acc[d], acc[d + 1], acc[d + 2], acc[d + 3]} * inv);
-  if (sub == 0) {
-    if (a.tau) a.tau[at] = n > 0 ? fmaf(a.am1, mx, t) : NAN;
-    if (a.support) a.support[at] = live;
+    for (int d = 0; d < kPer; d += 4)
+      store_out<PARTS>(a.out, at * D + sub * kPer + d,
+                       f32x4{acc[d], acc[d + 1], acc[d + 2], acc[d + 3]} * inv);
+    if (sub == 0) {
+      if (a.tau) a.tau[at] = n > 0 ? fmaf(a.am1, mx, t) : NAN;
+      if (a.support) a.support[at] = live;
+    }
+  }
+  if constexpr (kDense) {
+    __shared__ DenseLds<D> sh;
+    if (which) dense_rows<BF, D, PARTS>(a, w, which, sh);
   }
 }
 
 template <bool BF, int D, int PARTS>
 __global__ __launch_bounds__(kChunkWaves * kWave, 2) void dense_kernel(ChunkArgs a, int tok_bits) {
   __shared__ DenseLds<D> sh;
-  if (a.dense[blockIdx.x] == 0) return;
+  const unsigned which = a.dense[blockIdx.x];
+  if (which == 0) return;
   const int id = blockIdx.x / a.Hkv, g = blockIdx.x - id * a.Hkv;
   const Rows w = find_rows(a, tok_bits, id, g, threadIdx.x & (kWave - 1));
-  dense_rows<BF, D, PARTS>(a, w, 0, sh);
+  dense_rows<BF, D, PARTS>(a, w, which, sh);
 }
 
 template <bool BF, int D, int PARTS, int LE>
