@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 
 import torch
 
@@ -472,19 +473,26 @@ def entmaxkv_softmax_form(shape: Shape, q_dtype: int, q_tokens: int = 1,
     return int(out.value)
 
 
+def _torch_stream(stream, device):
+    """The torch stream of a call's `stream` argument, a stream or a handle."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    # (ExternalStream(0) is a new stream, not the null one)
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+
+
 def _given_or_new(ws, nbytes, q, stream):
     """(pointer, bytes, tensor) of a workspace of `nbytes`. One allocated here
-    is the allocator's again when the call returns, so it is marked as in use
-    by the stream that the kernels run on."""
+    is the allocator's again when the call returns. It is taken on the stream
+    that the kernels run on: what that memory held before, and what it holds
+    next, follows on the same stream."""
     if ws is None:
         if nbytes == 0:
             return None, 0, None
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-                stream = torch.cuda.ExternalStream(raw, device=q.device)
-            ws.record_stream(stream)
+        on = nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream, q.device))
+        with on:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     else:
         _ptr(ws, "ws")
         _one_device(q=q, ws=ws)
