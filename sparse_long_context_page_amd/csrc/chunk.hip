@@ -156,6 +156,24 @@ __device__ __forceinline__ void powers(const ChunkArgs& a, float u, float& pm, f
   }
 }
 
+// A token's weight in the output, up to a factor that all tokens of its row share:
+// u^m of u = y - t > 0 where m is whole, else (u / s)^m = (1 + y / s)^m, s = -t.
+// Near alpha = 1, u is nearly 1, and u^m would be off by m times u's rounding; the
+// logarithm of 1 + y / s is taken with what the sum's rounding lost put back.
+__device__ __forceinline__ float weight_of(const ChunkArgs& a, float y, float t, float u) {
+  if (a.whole) {
+    float pm, pm1;
+    powers(a, u, pm, pm1);
+    return pm;
+  }
+  const float rs = __builtin_amdgcn_rcpf(-t), x = y * rs;
+  const float w = 1.0f + x, e = w - 1.0f;
+  const float near = e != 0.0f ? __builtin_amdgcn_logf(w) * (x * __builtin_amdgcn_rcpf(e))
+                               : x * kLog2e;
+  const float lg = x > -0.5f ? near : __builtin_amdgcn_logf(u * rs);
+  return u > 0.0f ? __builtin_amdgcn_exp2f(a.m * lg) : 0.0f;
+}
+
 // s^(1 - 1/m), of m >= 1
 __device__ __forceinline__ float root_of(const ChunkArgs& a, float s) {
   return a.whole == 1   ? 1.0f
@@ -316,9 +334,9 @@ __device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, un
     float b = 0.0f;
 #pragma unroll
     for (int i = 0; i < NZ; ++i) {
-      float pm1;
-      const float u = finite ? fmaxf((z[i] - ref) * a.am1 - th.t, 0.0f) : 0.0f;
-      powers(a, u, p[i], pm1);
+      const float y = (z[i] - ref) * a.am1;
+      const float u = finite ? fmaxf(y - th.t, 0.0f) : 0.0f;
+      p[i] = weight_of(a, y, th.t, u);
       b += p[i];
       see |= (u > 0.0f ? 1u : 0u) << i;  // (a high power may be below float32)
     }
@@ -1513,9 +1531,9 @@ __global__ __launch_bounds__(kChunkWaves * kWave, kDense ? 1 : 5) void finish_ke
 #pragma unroll
   for (int i = 0; i < LE; ++i) {
     if (!__any(i * 16 < n)) break;
-    const float u = n > 0 ? fmaxf((entry_z(e[i]) - mx) * a.am1 - t, 0.0f) : 0.0f;
-    float p, pm1;
-    powers(a, u, p, pm1);
+    const float y = (entry_z(e[i]) - mx) * a.am1;
+    const float u = n > 0 ? fmaxf(y - t, 0.0f) : 0.0f;
+    const float p = weight_of(a, y, t, u);
     l += p;
     const bool keep = u > 0.0f;
     const unsigned all = (unsigned)(__ballot(keep) >> (lane & 48)) & 0xffffu;
