@@ -489,7 +489,9 @@ int entmaxkv_evict(const entmaxkv_shape* shape, void* k_pool, void* v_pool,
  * The free pages are a stack: page i (from 0) needed by all fitting sequences
  * together, in their order, is free_pages[free_count - 1 - i]; it is written to
  * block_table at the first column behind the sequence's pages. A sequence that
- * is not granted keeps its length and table; its rows have no slots.
+ * is not granted keeps its length and table; its rows have no slots. They are
+ * still rows of the step: entmaxkv_entmax_chunk takes them for the last n of the
+ * sequence's L tokens, and their output has no meaning.
  *   num_tokens    rows of the per-token arrays, 1 .. 2^24 - 1
  *   free_pages    int32 [free_capacity] (nullable if 0); free_count int32 [1],
  *                 clamped to [0, free_capacity]
@@ -587,24 +589,40 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
  *   alpha         > 1, finite (else ENTMAXKV_ERR_INVALID)
  *   tau           float32 [num_tokens, num_q_heads] (nullable)
  *   support       int32 [num_tokens, num_q_heads] (nullable)
+ * out may be q itself (of q_dtype); any other overlap of outputs and inputs is
+ * undefined. A long prompt may come in several calls, each with seq_lens up to
+ * its last token.
  * A row that sees no token (n_b > seq_lens[b]; every page invalid) gets out = 0,
  * tau = NaN, support = 0, and so does one whose scores are all -inf, by
  * overflow. What lies in hidden tokens' rows and in page tails has no effect,
  * NaN and infinities included, nor do values of zero weight; a seen score that
  * is NaN or +inf makes its row's out and tau NaN. Scores are float32, as in
  * entmaxkv_softmax_window; weights are used in float32 or, in rows whose support
- * is too long for a list, to 2^-17 of themselves (bf16 queries). Of float32
- * queries over a BF16 cache hidden rows of the same block may move the last bits
- * (which tokens are taken again in float32 is decided for a block), and |q| stays
+ * is too long for a list, to 2^-17 of themselves (bf16 queries). The last bits
+ * of a row may depend on the other rows of its block (up to 256 rows of a KV
+ * head), and with them on tokens that only those see: in which order its
+ * support is added, and of float32 queries over a BF16 cache which tokens are
+ * taken again in float32, is decided for the block. Of such queries |q| stays
  * below 2^127. Results do not depend on what else runs (no atomics on results).
- * Weights on hundreds of tokens (beyond 128 from alpha 1.5, 256 below) are right
- * but slow: their rows go over all scores once a threshold step.
+ * Many weights are right but slow: a row whose support is too long for a list
+ * goes over all of its scores once a threshold step (a prompt of 2048 with weights
+ * on all tokens 4.2 ms, with few 0.12; one token over 32K 5.0 ms, with few 0.04;
+ * 32 heads of 128, alpha 1.5). A list holds 128 tokens from alpha 1.5, 256 below;
+ * but a row is slow as soon as one share of its tokens alone would give more than
+ * the share's list holds their weight, also where tokens elsewhere outweigh these:
+ * of a part of its tokens 120 or 124 from alpha 1.5, 376 or 380 below (BF16 or F32
+ * cache), and in blocks of at most 16 rows of a quarter of a part 64 or 80.
  * Workspace: entmaxkv_entmax_chunk_ws bytes, for one call at a time (calls that
  * may overlap, graphs that replay side by side, need one each); it holds nothing
- * between calls. Kernels launched: 3 (lists of the
- * tokens that may have a weight; tau and the output; rows whose support is too
- * long for a list), or 2 for few tokens, the last within the second (events'
- * pair 2 then encloses nothing).
+ * between calls. It has a list of 128 entries (from alpha 1.5) or 384 of 8 bytes
+ * for every token, head and part, and for 16 rows of every sequence, KV head and
+ * part (parts: 1 for long steps, up to 64 for few tokens): with 32 heads 0.14 GB up
+ * to 4096 tokens, 1.1 GB for 32K, 4.4 GB for 128K at alpha 1.5, three times that
+ * below; slices need less. Kernels launched: 3 (lists of the tokens that may have
+ * a weight; tau and the output; rows whose support is too long for a list), or 2
+ * for few tokens, the last within the second (events' pair 2 then encloses
+ * nothing). A call of 2^24 workgroups or more (one for 16 rows, and for a block's
+ * part) returns ENTMAXKV_ERR_UNSUPPORTED.
  */
 int entmaxkv_entmax_chunk(const entmaxkv_shape* shape, const void* q, int32_t q_dtype,
                           int32_t num_tokens, const int32_t* token_starts, const void* k_pool,
