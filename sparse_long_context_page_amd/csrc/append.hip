@@ -314,9 +314,15 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
 }
 
 // Tokens of a workgroup: one, so that few tokens still fill the chip, up to
-// kAppendFew; four beyond, which share the angles' work (32/8 heads of 128 dims,
-// one against four, us: 64 tokens 4.5 : 8.8, 1024 7.5 : 11.6, 4096 23.3 : 24.7,
-// 8192 40.4 : 36.8).
+// kAppendFew; four beyond, which share the angles' work. One against four, us:
+//   tokens             64          1024         3001         4096         8192
+//   32/8 heads of 128  4.3 : 8.3   7.7 : 12.6   18.7 : 22.4  23.4 : 24.9  40.2 : 36.6
+//   64/8 heads of 128  5.1 : 12.0  12.2 : 23.5  26.9 : 33.9  33.9 : 37.6  60.1 : 58.3
+//   16/8, three axes   3.5 : 6.7   5.3 : 8.1    13.3 : 16.7  16.6 : 19.3  29.7 : 27.2
+//   8/8 of 64, float32 3.4 : 4.8   5.9 : 6.7    13.5 : 13.5  18.7 : 17.5  34.3 : 33.2
+//   1/1 of 64          3.4 : 3.3   4.0 : 3.4    5.0 : 3.6    5.8 : 3.7    8.6 : 4.4
+// (fewer lanes than a workgroup's have a head of a lone token in the last two, 96
+// and 12 of 256: they would pass over earlier.)
 constexpr int kAppendFew = 4096;
 
 template <bool XBF, bool QBF, bool KVBF, int D>

@@ -42,7 +42,7 @@ struct ChunkArgs {
   float am1, m;  // alpha - 1 and 1 / (alpha - 1)
   float rooted;  // 2 - alpha = 1 - 1/m
   float window;  // of a score below the row's maximum that may have a weight
-  int whole;     // m if it is 1, 2, 3 or 4, else 0
+  int whole;     // m if it is 1, 2, 3 or 4, else 0 (alpha = 4/3 of float32: 2.9999996)
   int tok_bits;  // 2^tok_bits tokens a list block
   int splits, few_splits;  // parts of a row's tokens; of blocks of at most 16 rows
   int cap;                 // entries of a list
@@ -221,7 +221,10 @@ struct DenseLds {
 // all of their scores: the maximum, one pass a threshold step, and the weights'
 // product with V. The workgroup's waves share the rows and take turns at the
 // tiles. The other rows keep what their lists gave, in other roundings (with
-// bf16 queries the weights of these are off by 2^-17).
+// bf16 queries the weights of these are off by 2^-17). Right, but slow: K is read
+// once a step for 16 rows, and a row's tokens are never split (weights on all
+// tokens, alpha 1.5, 32/8 heads of 128 dims: a prompt of 2048 4.2 ms, 512 of 32K 15.1,
+// one token over 32K 5.0).
 template <bool BF, int D, int PARTS>
 __device__ __forceinline__ void dense_rows(const ChunkArgs& a, const Rows& w, unsigned which,
                                            DenseLds<D>& sh) {
@@ -617,8 +620,10 @@ __device__ __forceinline__ Cache cache_of(const ChunkArgs& a, const Rows& w, int
   return x;
 }
 
-// Stages whose tiles' own maxima go before the bounds (none, 2, 8 of them: a prompt
-// of 2048 88, 85, 86 us; mixed batch of 32 693, 694, 701).
+// Stages whose tiles' own maxima go before the bounds. Whole calls with none, 2 and 8
+// of them, us (the same one again differs by 0.3, of the mixed batch by 1.5): prompts
+// of 64 23.7, 21.8, 21.8, of 256 44.2, 41.6, 42.0, of 2048 124.3, 121.2, 122.8; mixed
+// batch of 32 757.7, 756.5, 757.4.
 constexpr int kYoung = 2;
 
 // Row tiles a wave holds: with a bf16 cache 64 rows share each K operand read from
@@ -827,7 +832,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       const uint64_t long_ones = __ballot(pending);
       if (long_ones == 0) break;
-  // prune that row's list and its neighbours', 4 rows at a time; thresholds are
+      // prune that row's list and its neighbours', 4 rows at a time; thresholds are
       // solved where three quarters stay (where half do: 3.12 ms in place of 2.88, as
       // above with 256 entries)
       const int r = __builtin_amdgcn_readlane(row, __builtin_ctzll(long_ones));
@@ -877,7 +882,7 @@ __device__ __forceinline__ void flush(const ChunkArgs& a, WaveRows<NZ>& w, int c
 
 // More than 16 rows: every wave has NT row tiles of its own, K staged in LDS for
 // all of them. Bound by the matrix instructions, and beside them by hits (queue
-// and flush): 4096 of 32K tokens, 32/8 heads of 128 dims, 1.15 ms or 900 TFLOP/s
+// and flush): 4096 of 32K tokens, 32/8 heads of 128 dims, 1.16 ms or 890 TFLOP/s
 // of the score product alone; without a hit 0.88 ms. A prompt of 2048, whose rows
 // have nearly all of their hits before the bounds have settled: 86 us, its product
 // 17.
@@ -1313,8 +1318,7 @@ struct Run {
 // a SIMD: float32 queries, 4096 of 32K tokens, 187 us; without it 209). A prompt of
 // 2048 39 us, of which 34 without the threshold's steps and 38 without the V rows.
 // kDense: rows for the dense kernel are done here, by few workgroups, which need
-// not share a CU: a launch less (four short chats 27.4 us against 29.1; a prompt of
-// 2048, which has 16 workgroups a CU, 163 against 122).
+// not share a CU: a launch less (kFewTiles).
 template <bool BF, int D, int PARTS, int LE, bool kDense>
 __global__ __launch_bounds__(kChunkWaves * kWave, kDense ? 1 : 5) void finish_kernel(ChunkArgs a, int tok_bits) {
   constexpr int kJoinCap = 16 * LE;
@@ -1618,7 +1622,12 @@ hipError_t launch(const ChunkArgs& a, const ChunkPlan& p, int kernel, hipStream_
   return hipGetLastError();
 }
 
-// Workgroups of the finish kernel up to which the dense rows are done there.
+// Workgroups of the finish kernel up to which the dense rows are done there (beyond,
+// the passes' registers keep too few of them on a CU). Prompts of 40, 264, 520, 648,
+// 1032, 4104 workgroups, us: 13.3, 28.3, 39.6, 40.9, 48.6, 159 with the dense rows
+// there, 15.2, 30.0, 41.5, 37.8, 44.8, 123 in a kernel of their own; with weights on
+// all tokens 15.0, 51.9, 403, 428, 699, 4896 against 16.9, 53.3, 405, 416, 655, 4148;
+// a float32 cache, 264, 520, 1032 workgroups: 57.5, 65.8, 106 against 59.2, 67.5, 89.
 constexpr long long kFewTiles = 2 * kNumCUs;
 
 }  // namespace
