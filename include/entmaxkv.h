@@ -596,8 +596,10 @@ int entmaxkv_append_kv(const entmaxkv_shape* shape, const entmaxkv_append* appen
  * tau = NaN, support = 0, and so does one whose scores are all -inf, by
  * overflow. What lies in hidden tokens' rows and in page tails has no effect,
  * NaN and infinities included, nor do values of zero weight; a seen score that
- * is NaN or +inf makes its row's out and tau NaN. Scores are float32, as in
- * entmaxkv_softmax_window; weights are used in float32 or, in rows whose support
+ * is NaN or +inf makes its row's out and tau NaN (with float32 queries over a
+ * BF16 cache a seen key that holds an infinity may, whatever its score: it is
+ * multiplied by the query's three bf16 parts, zeros among them). Scores are
+ * float32, as in entmaxkv_softmax_window; weights are used in float32 or, in rows whose support
  * is too long for a list, to 2^-17 of themselves (bf16 queries). The last bits
  * of a row may depend on the other rows of its block (up to 256 rows of a KV
  * head), and with them on tokens that only those see: in which order its
